@@ -383,10 +383,116 @@ JEPA_API jepa_status jepa_qkv_rope(const void* A, const void* W, const float* bi
                                    int grid_t, int grid_h, int grid_w, int layout, int interpolate, int ref_grid,
                                    float theta, const int32_t* pos_ids, void* stream);
 
+/* ---------------------------------------------------------------- training operators
+ * What training a head on the encoder's tokens needs beside the forward
+ * operations above.  The source pages stop at inference; these operators have
+ * no counterpart there.
+ *
+ * Common to all of them:
+ *   - dtype (jepa_dtype) is the type T of the matrices; sums, statistics and
+ *     gradients of vectors are fp32.  Matrices are row-major and contiguous;
+ *     a buffer need only be aligned to its element, and no width has to be a
+ *     multiple of anything.  In F16/BF16 the tensor cores are used when every
+ *     matrix starts on 16 bytes and its rows are multiples of 16 bytes; other
+ *     layouts, and F32, run on the CUDA cores.
+ *   - Rows 0 is valid: gradients of weights are then zeros.  Row counts and
+ *     widths are at most 2^24 (layer norm: dim at most 2^20).
+ *   - `workspace` is a device buffer of the caller, 256-byte aligned, of at
+ *     least the bytes that the _workspace_bytes function gives for the same
+ *     arguments (it returns 0 for arguments that the call refuses).  Its
+ *     contents mean nothing between calls.  Two calls that may run at the same
+ *     time need two workspaces; nothing else is shared between calls.
+ *   - Outputs must not overlap inputs, the workspace or each other.  Gradients
+ *     are written, not added to.
+ *   - Results do not depend on scheduling: every sum has a fixed order.
+ *   - The calls only enqueue kernels and memsets and can be captured into a
+ *     CUDA graph; the first call on a device (which allocates that device's
+ *     status word) has to be made outside a capture. */
+
+/* Layer norm over the last dimension: y = (x - mean) rstd w + b, with the
+ * biased centred variance, rstd = 1/sqrt(var + eps).
+ *   x: x_dtype [rows, dim]; y: y_dtype [rows, dim]; w, b: float [dim];
+ *   mean, rstd: float [rows] for jepa_layernorm_bwd, or NULL.
+ * y_dtype equals x_dtype, or x_dtype is F32 (the residual stream). */
+JEPA_API jepa_status jepa_layernorm_fwd(const void* x, const float* w, const float* b, void* y, float* mean,
+                                        float* rstd, int rows, int dim, int x_dtype, int y_dtype, float eps,
+                                        void* stream);
+/* Its backward pass: with xh = (x - mean) rstd and c = dy w,
+ *   dx = rstd (c - mean(c) - xh mean(c xh)) + residual,
+ *   dw = sum_rows dy xh, db = sum_rows dy.
+ *   dy: y_dtype [rows, dim]; x, dx: x_dtype [rows, dim]; mean, rstd: what
+ *   jepa_layernorm_fwd gave; residual: x_dtype [rows, dim], the gradient that
+ *   reaches x past the norm, or NULL; dw, db: float [dim], either may be NULL. */
+JEPA_API size_t jepa_layernorm_bwd_workspace_bytes(int rows, int dim);
+JEPA_API jepa_status jepa_layernorm_bwd(const void* dy, const void* x, const float* w, const float* mean,
+                                        const float* rstd, const void* residual, void* dx, float* dw, float* db,
+                                        int rows, int dim, int x_dtype, int y_dtype, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* Softmax cross entropy of a linear classifier, z = x W^T + bias, without
+ * ever holding z: it is computed in tiles that are reduced at once.  Per row
+ *   lse  = log sum_v exp(z_v),
+ *   loss = lse - (1 - smoothing) z_label - smoothing mean_v(z_v).
+ *   x: dtype [M, D]; W: dtype [V, D]; bias: float [V] or NULL;
+ *   labels: device int64 [M]; loss: float [M] or NULL; lse: float [M].
+ * A row whose label equals ignore_index has loss 0 and no gradient (lse is
+ * still its own).  A label outside [0, V) that is not ignore_index gives loss
+ * NaN, no gradient, and JEPA_ERR_ARG from the next jepa_ops_sync.  A bias of
+ * -infinity takes a class out (its gradient is 0 without smoothing); NaN
+ * logits give a NaN row. */
+JEPA_API size_t jepa_linear_ce_workspace_bytes(int M, int D, int V, int dtype, int backward);
+JEPA_API jepa_status jepa_linear_ce_fwd(const void* x, const void* W, const float* bias, const int64_t* labels,
+                                        float* loss, float* lse, int M, int D, int V, int dtype, int64_t ignore_index,
+                                        float smoothing, void* workspace, size_t workspace_bytes, void* stream);
+/* Its gradients, from lse and the gradient dloss (float [M]) of each row's
+ * loss: dz = dloss (exp(z - lse) - (1 - smoothing) [v = label] - smoothing / V),
+ *   dx = dz W (dtype [M, D]), dW = dz^T x (dtype [V, D]), dbias = sum_rows dz
+ *   (float [V]); each may be NULL, not all.
+ * z is recomputed.  In F16/BF16 dz is rounded to the type before the products
+ * dx and dW (in F16 scaled by a power of two chosen from max |dloss|, so that
+ * small probabilities stay normal numbers); dbias is summed before that. */
+JEPA_API jepa_status jepa_linear_ce_bwd(const void* x, const void* W, const float* bias, const int64_t* labels,
+                                        const float* lse, const float* dloss, void* dx, void* dW, float* dbias, int M,
+                                        int D, int V, int dtype, int64_t ignore_index, float smoothing,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gated feed-forward, the up half of a gated MLP: h = act(x Wg^T + bg) *
+ * (x Wu^T + bu), the down projection being jepa_linear on h.
+ *   x: dtype [M, D]; Wg, Wu: dtype [F, D]; bg, bu: float [F], each or NULL;
+ *   h: dtype [M, F]; act: jepa_gate_act, silu(g) = g / (1 + exp(-g)) or the
+ *   exact-erf GELU. */
+typedef enum { JEPA_GATE_SILU = 0, JEPA_GATE_GELU = 1 } jepa_gate_act;
+JEPA_API size_t jepa_gated_ffn_workspace_bytes(int M, int D, int F, int dtype, int backward);
+JEPA_API jepa_status jepa_gated_ffn_fwd(const void* x, const void* Wg, const void* Wu, const float* bg,
+                                        const float* bu, void* h, int M, int D, int F, int dtype, int act,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+/* Its gradients from dh (dtype [M, F]); the two projections g and u are
+ * recomputed, so the forward pass keeps nothing:
+ *   dg = dh u act'(g), du = dh act(g),
+ *   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dbg, dbu = column sums
+ *   (float [F]); each output may be NULL, not all.
+ * In F16/BF16 dg and du are rounded to the type before the products dx, dWg
+ * and dWu (F16: use a loss scale that keeps them inside the type's range). */
+JEPA_API jepa_status jepa_gated_ffn_bwd(const void* dh, const void* x, const void* Wg, const void* Wu, const float* bg,
+                                        const float* bu, void* dx, void* dWg, void* dWu, float* dbg, float* dbu, int M,
+                                        int D, int F, int dtype, int act, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+/* Backward pass of out = A W^T + bias (jepa_linear's epilogues 0, 1 and 2):
+ *   dA = dout W (dtype [M, K]), dW = dout^T A (dtype [N, K]), dbias = sum_rows
+ *   dout (float [N]); each may be NULL, not all (W is needed for dA, A for dW).
+ *   dout: dtype [M, N]; A: dtype [M, K]; W: dtype [N, K]. */
+JEPA_API size_t jepa_linear_bwd_workspace_bytes(int M, int N, int K, int dtype);
+JEPA_API jepa_status jepa_linear_bwd(const void* dout, const void* A, const void* W, void* dA, void* dW, float* dbias,
+                                     int M, int N, int K, int dtype, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
 /* Synchronises `stream` and reports a device-side timeout recorded by any
- * earlier single-operation call (jepa_attention, jepa_linear, jepa_qkv_rope)
+ * earlier single-operation call (jepa_attention, jepa_linear, jepa_qkv_rope,
+ * jepa_linear_ce_*, jepa_gated_ffn_*, jepa_linear_bwd)
  * of this process (then clears it), or ids outside the grid given to
- * jepa_qkv_rope (JEPA_ERR_ARG). */
+ * jepa_qkv_rope, or labels outside the vocabulary given to jepa_linear_ce_*
+ * (JEPA_ERR_ARG). */
 JEPA_API jepa_status jepa_ops_sync(void* stream);
 
 /* Failure-detection self test: launches one kernel that waits on a barrier

@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) V-JEPA 2 / 2.1 video ViT encoder forward.
+"""GB300 (sm_103a) V-JEPA 2 / 2.1 video ViT encoder forward, and the operators
+for training a head on its tokens.
 
 The compute lives in ``libjepa_gb300.so`` (hand-written CUDA behind the C ABI
 of ``include/jepa_gb300.h``); this package only marshals arguments.
@@ -9,4 +10,7 @@ from .binding import (  # noqa: F401
     layernorm_f32, linear,
     ops_sync, pack_blob, predictor_params, predictor_tensor_order, qkv_rope, rope3d_f32,
     selftest_wait_timeout,
+)
+from .training import (  # noqa: F401
+    gated_ffn_bwd, gated_ffn_fwd, layernorm_bwd, layernorm_fwd, linear_bwd, linear_ce_bwd, linear_ce_fwd,
 )

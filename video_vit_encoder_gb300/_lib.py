@@ -19,6 +19,7 @@ STATUS_NAMES = {0: "OK", 1: "ERR_ARG", 2: "ERR_BLOB", 3: "ERR_UNSUPPORTED", 4: "
 DT_F32, DT_F16, DT_BF16 = 0, 1, 2
 CLIP_U8_THWC, CLIP_F32_CTHW = 0, 1
 MODALITY_VIDEO, MODALITY_IMAGE, MODALITY_AUTO = 0, 1, 2
+GATE_SILU, GATE_GELU = 0, 1
 
 
 class JepaError(RuntimeError):
@@ -50,7 +51,7 @@ class HeadParams(C.Structure):
                 ("n_classes", C.c_int), ("ln_eps", C.c_float), ("dtype", C.c_int)]
 
 
-VP, I, F, ST, U64 = C.c_void_p, C.c_int, C.c_float, C.c_int, C.c_size_t
+VP, I, F, ST, U64, I64 = C.c_void_p, C.c_int, C.c_float, C.c_int, C.c_size_t, C.c_int64
 
 # name: (restype, argtypes)
 SIGNATURES = {
@@ -89,6 +90,17 @@ SIGNATURES = {
     "jepa_head_forward": (ST, [VP, VP, I, I, VP, VP, VP]),
     "jepa_head_sync": (ST, [VP, VP]),
     "jepa_head_set_graphs": (ST, [VP, I]),
+    "jepa_layernorm_fwd": (ST, [VP, VP, VP, VP, VP, VP, I, I, I, I, F, VP]),
+    "jepa_layernorm_bwd_workspace_bytes": (U64, [I, I]),
+    "jepa_layernorm_bwd": (ST, [VP, VP, VP, VP, VP, VP, VP, VP, VP, I, I, I, I, VP, U64, VP]),
+    "jepa_linear_ce_workspace_bytes": (U64, [I, I, I, I, I]),
+    "jepa_linear_ce_fwd": (ST, [VP, VP, VP, VP, VP, VP, I, I, I, I, I64, F, VP, U64, VP]),
+    "jepa_linear_ce_bwd": (ST, [VP, VP, VP, VP, VP, VP, VP, VP, VP, I, I, I, I, I64, F, VP, U64, VP]),
+    "jepa_gated_ffn_workspace_bytes": (U64, [I, I, I, I, I]),
+    "jepa_gated_ffn_fwd": (ST, [VP, VP, VP, VP, VP, VP, I, I, I, I, I, VP, U64, VP]),
+    "jepa_gated_ffn_bwd": (ST, [VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, I, I, I, I, I, VP, U64, VP]),
+    "jepa_linear_bwd_workspace_bytes": (U64, [I, I, I, I]),
+    "jepa_linear_bwd": (ST, [VP, VP, VP, VP, VP, VP, I, I, I, I, VP, U64, VP]),
     "jepa_last_error": (C.c_char_p, []),
     "jepa_abi_version": (C.c_int, []),
 }

@@ -18,6 +18,7 @@
 #include <string>
 #include <vector>
 
+#include "api_internal.h"
 #include "internal.h"
 #include "jepa_gb300.h"
 
@@ -562,12 +563,23 @@ jepa_status read_status(int* d_status, cudaStream_t s) {
   if (h != 0) {
     CUDA_TRY(cudaMemset(d_status, 0, sizeof(int)));
     if (h & DEV_TIMEOUT) return fail(JEPA_ERR_DEVICE_TIMEOUT, "a kernel gave up waiting on a barrier (status 0x%x)", h);
-    return fail(JEPA_ERR_ARG, "token ids outside the grid (clamped; results invalid) (status 0x%x)", h);
+    return fail(JEPA_ERR_ARG, "token ids outside the grid (clamped) or labels outside the vocabulary: results invalid (status 0x%x)", h);
   }
   return JEPA_OK;
 }
 
 }  // namespace
+
+// The messages and the status word, for the entry points of other translation units.
+jepa_status jepa::api_fail(jepa_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(st, "%s", buf);
+}
+jepa_status jepa::api_ops_status(int** out) { return ops_status(out); }
 
 namespace jepa {
 // Lets other translation units set the message returned by jepa_last_error().

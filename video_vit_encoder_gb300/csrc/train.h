@@ -1,0 +1,71 @@
+// Declarations of the training operators: layer norm with its backward pass,
+// the gated feed-forward, the linear layer's backward pass and the softmax
+// cross entropy of a linear classifier.
+#pragma once
+#include "internal.h"
+
+namespace jepa {
+
+// ----------------------------------------------------------------------------- layer norm (layernorm_fwd.cu, layernorm_bwd.cu)
+// x_dtype / y_dtype: equal, or x in fp32 and y in a 16-bit type.
+cudaError_t layernorm_fwd(int x_dtype, int y_dtype, const void* x, const float* w, const float* b, void* y, float* mean,
+                          float* rstd, long rows, int dim, float eps, cudaStream_t s);
+// Upper bound on the number of row strips of the backward pass, each of which
+// writes one partial sum of dw and db: two per SM of the 152.
+constexpr int kLnBwdStrips = 304;
+size_t layernorm_bwd_workspace(long rows, int dim);
+cudaError_t layernorm_bwd(int x_dtype, int y_dtype, const void* dy, const void* x, const float* w, const float* mean,
+                          const float* rstd, const void* res, void* dx, float* dw, float* db, long rows, int dim,
+                          float* ws, cudaStream_t s);
+
+// ----------------------------------------------------------------------------- general product on the CUDA cores (gemm_any.cu)
+// An operand: element (r, k) at p[r * rs + k * ks], one of rs and ks being 1.
+struct AnyMat {
+  const void* p;
+  int dtype;
+  long rs, ks;
+};
+// C[m, n] (+)= sum_k A(m, k) B(n, k) (+ bias[n]), fp32 accumulation; C in
+// c_dtype with row stride ldc.  accumulate: add to what C (fp32) holds.
+cudaError_t gemm_any(const AnyMat& A, const AnyMat& B, void* C, int c_dtype, long ldc, int M, int N, int K,
+                     const float* bias, bool accumulate, cudaStream_t s);
+
+// ----------------------------------------------------------------------------- operators (train_ops.cu)
+enum GateAct : int { ACT_SILU = 0, ACT_GELU = 1 };
+
+struct CeArgs {
+  const void* x;          // T [M, D]
+  const void* w;          // T [V, D]
+  const float* bias;      // [V] or null
+  const int64_t* labels;  // [M]
+  int M, D, V, dtype;
+  long ignore_index;
+  float smoothing;
+  int* status;
+  int num_sms;
+};
+size_t linear_ce_workspace(int M, int D, int V, int dtype, bool backward);
+cudaError_t linear_ce_fwd(const CeArgs& a, float* loss, float* lse, void* ws, cudaStream_t s);
+cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss, void* dx, void* dw, float* dbias,
+                          void* ws, cudaStream_t s);
+
+struct FfnArgs {
+  const void* x;        // T [M, D]
+  const void* wg;       // T [F, D]
+  const void* wu;       // T [F, D]
+  const float* bg;      // [F] or null
+  const float* bu;      // [F] or null
+  int M, D, F, dtype, act;
+  int* status;
+  int num_sms;
+};
+size_t gated_ffn_workspace(int M, int D, int F, int dtype, bool backward);
+cudaError_t gated_ffn_fwd(const FfnArgs& a, void* h, void* ws, cudaStream_t s);
+cudaError_t gated_ffn_bwd(const FfnArgs& a, const void* dh, void* dx, void* dwg, void* dwu, float* dbg, float* dbu,
+                          void* ws, cudaStream_t s);
+
+size_t linear_bwd_workspace(int M, int N, int K, int dtype);
+cudaError_t linear_bwd(int dtype, const void* dout, const void* A, const void* W, void* dA, void* dW, float* dbias,
+                       int M, int N, int K, void* ws, int* status, int num_sms, cudaStream_t s);
+
+}  // namespace jepa
