@@ -7,7 +7,7 @@
 // that.  The workspace holds one piece, never the whole [rows, width] matrix.
 // The products (gemm_any.cu) take nearly all the time, so the kernels here
 // are plain single passes.
-#include "train.h"
+#include "train_tc.h"
 
 namespace jepa {
 
@@ -16,6 +16,7 @@ namespace {
 constexpr int kBlock = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
+size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 size_t elem(int dtype) { return dtype == DTYPE_F32 ? 4 : 2; }
 unsigned blocks_for(long n, int block) { return (unsigned)((n + block - 1) / block); }
@@ -253,12 +254,14 @@ cudaError_t zero(void* p, size_t bytes, cudaStream_t s) {
 // 16-bit) the fp32 sum of dx over the pieces.
 size_t linear_ce_workspace(int M, int D, int V, int dtype, bool backward) {
   const size_t z = align256(sizeof(float) * (size_t)M * piece_cols(M, V, 1));
-  if (!backward) return align256(sizeof(CeState) * (size_t)M) + z;
-  return z + (dtype == DTYPE_F32 ? 0 : align256(sizeof(float) * (size_t)M * D));
+  size_t b = backward ? z + (dtype == DTYPE_F32 ? 0 : align256(sizeof(float) * (size_t)M * D))
+                      : align256(sizeof(CeState) * (size_t)M) + z;
+  return dtype != DTYPE_F32 && D % 8 == 0 ? larger(b, linear_ce_tc_workspace(M, D, V, backward)) : b;
 }
 
 cudaError_t linear_ce_fwd(const CeArgs& a, float* loss, float* lse, void* ws, cudaStream_t s) {
   if (a.M == 0) return cudaSuccess;
+  if (linear_ce_tc_ok(a, nullptr, nullptr)) return linear_ce_fwd_tc(a, loss, lse, ws, s);
   CeState* state = static_cast<CeState*>(ws);
   float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(sizeof(CeState) * (size_t)a.M));
   const int pc = piece_cols(a.M, a.V, 1);
@@ -282,6 +285,7 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
     JEPA_TRY_CUDA(zero(dw, es * (size_t)a.V * a.D, s));
     return zero(dbias, sizeof(float) * (size_t)a.V, s);
   }
+  if (linear_ce_tc_ok(a, dx, dw)) return linear_ce_bwd_tc(a, lse, dloss, dx, dw, dbias, ws, s);
   const int pc = piece_cols(a.M, a.V, 1);
   float* z = static_cast<float*>(ws);
   float* dxa = a.dtype == DTYPE_F32
@@ -313,8 +317,9 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
 // Workspace: the piece's two projections, and (backward, 16-bit) the fp32 sum
 // of dx over the pieces.
 size_t gated_ffn_workspace(int M, int D, int F, int dtype, bool backward) {
-  const size_t gu = 2 * align256(sizeof(float) * (size_t)M * piece_cols(M, F, 2));
-  return gu + (backward && dtype != DTYPE_F32 ? align256(sizeof(float) * (size_t)M * D) : 0);
+  size_t b = 2 * align256(sizeof(float) * (size_t)M * piece_cols(M, F, 2));
+  if (backward && dtype != DTYPE_F32) b += align256(sizeof(float) * (size_t)M * D);
+  return dtype != DTYPE_F32 && D % 8 == 0 && F % 8 == 0 ? larger(b, gated_ffn_tc_workspace(M, D, F, backward)) : b;
 }
 
 namespace {
@@ -343,6 +348,7 @@ cudaError_t ffn_project(const FfnArgs& a, const FfnPiece& p, int f0, int n, cuda
 
 cudaError_t gated_ffn_fwd(const FfnArgs& a, void* h, void* ws, cudaStream_t s) {
   if (a.M == 0) return cudaSuccess;
+  if (gated_ffn_tc_ok(a, h, nullptr, nullptr, nullptr)) return gated_ffn_fwd_tc(a, h, s);
   const FfnPiece p = ffn_buffers(a, ws);
   for (int f0 = 0; f0 < a.F; f0 += p.pc) {
     const int n = a.F - f0 < p.pc ? a.F - f0 : p.pc;
@@ -368,6 +374,7 @@ cudaError_t gated_ffn_bwd(const FfnArgs& a, const void* dh, void* dx, void* dwg,
     JEPA_TRY_CUDA(zero(dbg, sizeof(float) * (size_t)a.F, s));
     return zero(dbu, sizeof(float) * (size_t)a.F, s);
   }
+  if (gated_ffn_tc_ok(a, dh, dx, dwg, dwu)) return gated_ffn_bwd_tc(a, dh, dx, dwg, dwu, dbg, dbu, ws, s);
   const FfnPiece p = ffn_buffers(a, ws);
   float* dxa = a.dtype == DTYPE_F32
                    ? static_cast<float*>(dx)
@@ -403,14 +410,18 @@ cudaError_t gated_ffn_bwd(const FfnArgs& a, const void* dh, void* dx, void* dwg,
 }
 
 // ----------------------------------------------------------------------------- linear layer backward
-size_t linear_bwd_workspace(int, int, int, int) { return 0; }
+size_t linear_bwd_workspace(int M, int N, int K, int dtype) {
+  return dtype != DTYPE_F32 && N % 8 == 0 && K % 8 == 0 ? linear_bwd_tc_workspace(M, N, K) : 0;
+}
 
 cudaError_t linear_bwd(int dtype, const void* dout, const void* A, const void* W, void* dA, void* dW, float* dbias,
-                       int M, int N, int K, void*, int*, int, cudaStream_t s) {
+                       int M, int N, int K, void* ws, int* status, int num_sms, cudaStream_t s) {
   if (M == 0) {
     JEPA_TRY_CUDA(zero(dW, elem(dtype) * (size_t)N * K, s));
     return zero(dbias, sizeof(float) * (size_t)N, s);
   }
+  if (linear_bwd_tc_ok(dtype, dout, A, W, dA, dW, N, K))
+    return linear_bwd_tc(dtype, dout, A, W, dA, dW, dbias, M, N, K, ws, status, num_sms, s);
   if (dA != nullptr)
     JEPA_TRY_CUDA(gemm_any(rows_k(dout, dtype, N), k_rows(W, dtype, K), dA, dtype, K, M, K, N, nullptr, false, s));
   if (dW != nullptr)
