@@ -390,11 +390,14 @@ JEPA_API jepa_status jepa_qkv_rope(const void* A, const void* W, const float* bi
  *
  * Common to all of them:
  *   - dtype (jepa_dtype) is the type T of the matrices; sums, statistics and
- *     gradients of vectors are fp32.  Matrices are row-major and contiguous;
- *     a buffer need only be aligned to its element, and no width has to be a
- *     multiple of anything.  In F16/BF16 the tensor cores are used when every
- *     matrix starts on 16 bytes and its rows are multiples of 16 bytes; other
- *     layouts, and F32, run on the CUDA cores.
+ *     gradients of vectors are fp32.  Matrices are row-major, contiguous and
+ *     16-byte aligned (layer norm: aligned to their element), vectors aligned
+ *     to their element; no width has to be a multiple of anything.
+ *   - Products run on the tensor cores in every type.  F32 operands are split
+ *     into three bf16 terms each (24 bits; the products of terms below 2^-24
+ *     are dropped) and summed in fp32, so results have fp32's accuracy; an
+ *     infinity in an F32 matrix gives NaN where it takes part.  Widths whose
+ *     16-bit rows are not multiples of 16 bytes cost a copy of the matrix.
  *   - Rows 0 is valid: gradients of weights are then zeros.  Row counts and
  *     widths are at most 2^24 (layer norm: dim at most 2^20).
  *   - `workspace` is a device buffer of the caller, 256-byte aligned, of at
@@ -449,8 +452,8 @@ JEPA_API jepa_status jepa_linear_ce_fwd(const void* x, const void* W, const floa
  *   dx = dz W (dtype [M, D]), dW = dz^T x (dtype [V, D]), dbias = sum_rows dz
  *   (float [V]); each may be NULL, not all.
  * z is recomputed.  In F16/BF16 dz is rounded to the type before the products
- * dx and dW (in F16 scaled by a power of two chosen from max |dloss|, so that
- * small probabilities stay normal numbers); dbias is summed before that. */
+ * dx and dW, in units of max |dloss| (so dloss itself costs no precision, and
+ * in F16 small probabilities stay normal numbers); dbias is summed before. */
 JEPA_API jepa_status jepa_linear_ce_bwd(const void* x, const void* W, const float* bias, const int64_t* labels,
                                         const float* lse, const float* dloss, void* dx, void* dW, float* dbias, int M,
                                         int D, int V, int dtype, int64_t ignore_index, float smoothing,

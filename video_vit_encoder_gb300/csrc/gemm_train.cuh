@@ -9,16 +9,31 @@
 //   K-major:  one box of 128 rows x 64 k (128 bytes a row);
 //   MN-major: two boxes of 64 k x 64 rows, each 64 k-lines of 128 bytes.
 //
+// fp32 operands (SPLIT) come as three bf16 planes x = x0 + x1 + x2, each the
+// rounding of what the ones before leave, 24 bits and more together.  Of the
+// nine products of planes the six with i + j <= 2 are taken; the others are
+// below 2^-24 of the first.  That is 6 times the work of a bf16 product and
+// still several times the FFMA rate.
+//
+// The tensor core truncates its fp32 accumulator at every step of 16 k: after n
+// steps a sum has lost about n 2^-25 of itself (measured: logits over 1024 k
+// 1.5e-6 too small).  Epilogues whose results are fp32 therefore take the
+// accumulator out every kb_chunk blocks and add the pieces in registers, with
+// rounding; SPLIT does so every block, with the products of the small planes
+// first, whose steps then truncate a small accumulator.
+//
 // Work units are runs of tiles: the cross entropy carries its row statistics
 // over a run of column tiles, everything else has runs of one.  K may consist
 // of two segments with their own operands (dx = dg Wg + du Wu is one product),
 // and may be split between units, each writing its own fp32 slab, which a
 // second kernel adds in a fixed order.
 //
-// Warp roles (320 threads): warp 0 loads, warp 1 issues the MMAs (the even
-// CTA's, for the pair), warps 2-9 run the epilogue, two warps per 32 TMEM
-// lanes, each half the tile's columns.  Two accumulators of 256 columns fill
-// tensor memory, so a tile's epilogue overlaps the next tile's main loop.
+// Warp roles: warp 0 loads, warp 1 issues the MMAs (the even CTA's, for the
+// pair), eight warps run the epilogue, two per 32 TMEM lanes, each half the
+// tile's columns.  Two accumulators of 256 columns fill tensor memory, so a
+// tile's epilogue overlaps the next tile's main loop.  Epilogues that hold
+// their 128 columns in registers run in three warpgroups, of which the first
+// (load, issue, two idle warps) hands registers to the other two.
 #pragma once
 #include "train.h"
 
@@ -28,8 +43,8 @@ namespace tg {
 constexpr int kBM = 128;        // rows per CTA, 256 per pair
 constexpr int kBN = 256;        // columns per pair tile
 constexpr int kBK = 64;
-constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
+constexpr int kRegsControl = 72, kRegsEpi = 216;   // 128 x 72 + 256 x 216 = 384 x 168, the launch allocation
 constexpr int kStages = 6;
 constexpr int kGroupM = 8;      // row tiles that share a sweep over the columns (operand reuse in L2)
 
@@ -44,12 +59,12 @@ static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 enum Epi : int {
   STORE = 0,     // C (T) = acc * scale
-  F32 = 1,       // slab (fp32) = acc
-  F32_ADD = 2,   // slab (fp32) += acc
+  F32 = 1,       // slab, or C in fp32 = acc
+  F32_ADD = 2,   // slab, or C in fp32 += acc
   CE_FWD = 3,    // row statistics of z = acc + bias
-  CE_BWD = 4,    // dz (T) from z = acc + bias
-  GATE_FWD = 5,  // h (T); columns 0-127 of the tile are gates, 128-255 the same columns' ups
-  GATE_BWD = 6   // dg, du (T)
+  CE_BWD = 4,    // dz (T, or planes) from z = acc + bias
+  GATE_FWD = 5,  // h (T, or fp32); columns 0-127 of the tile are gates, 128-255 the same columns' ups
+  GATE_BWD = 6   // dg, du (T, or planes)
 };
 
 struct EpiArgs {
@@ -61,7 +76,7 @@ struct EpiArgs {
   long ignore_index;
   const float* lse;
   const float* dloss;
-  const float* dz_scale;   // CE_BWD: power of two on the device, or null
+  const float* dz_scale;   // CE_BWD, 16-bit: [0] what dloss is divided by, [1] the factor of every dz
   float smoothing;
   int v0, V;
   float2* part_ms;         // CE_FWD: [parts][M] (max, sum) in base 2
@@ -70,7 +85,8 @@ struct EpiArgs {
   float* col_part;         // CE_BWD, GATE_BWD: [ceil(M/32)][ld_col] column sums of 32 rows, or null
   float* col_part2;
   int ld_col;
-  const void* dh;          // GATE_BWD: T [M, N]
+  const void* dh;          // GATE_BWD: [M, N] in the operator's type
+  int dh_vec;              // its rows start on 16 bytes
   int act;
 };
 
@@ -82,7 +98,11 @@ struct Params {
   int kb_seg, nseg;      // K blocks per segment, segments
   int nz;                // products that share B (a[z], c[z])
   int splits, kb_split;  // K splits, blocks per split
+  int kb_chunk;          // blocks accumulated in tensor memory before the epilogue takes them
+  int a_plane, b_plane, c_plane;  // SPLIT: rows from one plane to the next
   int slab_rows;         // rows of a slab (F32, F32_ADD)
+  void* plain;           // C where TMA cannot store it (rows not multiples of 16 bytes), else null
+  long plain_ld;
   EpiArgs ep;
   int* status;
 };
@@ -131,28 +151,97 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Sum over the warp's 32 lanes of v[j] for each j: lane j returns column j's.
-// Each step halves the columns a lane still carries; the order is fixed.
-__device__ __forceinline__ float warp_col_sum32(float (&v)[32], int lane) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const bool up = (lane & o) != 0;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float send = up ? v[i] : v[i + o];
-      const float keep = up ? v[i + o] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-    }
-  }
-  return v[0];
+// Arrival on a barrier of the pair that hands back tensor memory: the loads
+// before it have completed (tcgen05.wait::ld and the fence), and no memory is
+// passed on, so it need not wait for the thread's stores as a release does.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// This warp's staged 32 x 128-byte block, written by `put` (which stores lane's
-// row), goes out with one TMA store; the buffer's previous store has been read.
+// Packed arithmetic on two neighbouring values: (a, b) = (a, b) m + (c, c), and
+// products with one factor.  The epilogues are bound by instruction issue.
+__device__ __forceinline__ void fma2(float& a, float& b, float m, float c) {
+  uint64_t v, k, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(k) : "f"(m));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(c));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(k), "l"(d));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ void mul2(float& a, float& b, float m) {
+  uint64_t v, k;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(k) : "f"(m));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(k));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
+  uint64_t v, k;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(k) : "f"(x), "f"(y));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(k));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// v += the 32 biases from column col on; columns at or past n get `past`.
+// Every lane reads the same addresses.
+__device__ __forceinline__ void add_bias(const float* bias, int col, int n, float past, float* v) {
+  const float* b = bias + col;
+  if (col + 32 <= n && (reinterpret_cast<uintptr_t>(b) & 15) == 0) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(b + j));
+      add2f(v[j], v[j + 1], q.x, q.y);
+      add2f(v[j + 2], v[j + 3], q.z, q.w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] += col + j < n ? __ldg(b + j) : past;
+  }
+}
+
+// Column sums over the warp's 32 rows of 32 columns, written to part[0 .. n):
+// the block goes through the staging buffer (its last store has to have been
+// read), eight rows are summed by a lane for four columns, and the four row
+// groups joined.
+__device__ __forceinline__ void col_sum32(const float* v, uint8_t* buf, int lane, float* part, int n) {
+  uint8_t* row = buf + lane * 128;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    *reinterpret_cast<float4*>(row + ((k ^ (lane & 7)) << 4)) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  __syncwarp();
+  const int k = lane & 7, g = lane >> 3;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const float4 q = *reinterpret_cast<const float4*>(buf + (g * 8 + r) * 128 + ((k ^ r) << 4));
+    add2f(s.x, s.y, q.x, q.y);
+    add2f(s.z, s.w, q.z, q.w);
+  }
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {
+    s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+    s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+    s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
+    s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+  }
+  __syncwarp();   // the buffer has been read
+  // lane (g, k) writes column 4 k + g
+  const float out = g == 0 ? s.x : (g == 1 ? s.y : (g == 2 ? s.z : s.w));
+  if (4 * k + g < n) part[4 * k + g] = out;
+}
+
+// This warp's 32 x 128-byte block of C at column x, row y, from each lane's row
+// of eight 16-byte words: through the staging buffer (swizzled, so neither side
+// has bank conflicts) and out with one TMA store, which clips it to C.
 template <typename Put>
-__device__ __forceinline__ void stage_store(const CUtensorMap* c, uint8_t* buf, int lane, int x, int y, bool add,
-                                            Put&& put) {
-  if (lane == 0) bulk_wait_read_all();
+__device__ __forceinline__ void emit(const CUtensorMap* c, uint8_t* buf, int lane, int x, int y, bool add, Put&& put) {
+  if (lane == 0) bulk_wait_read_all();   // the previous store has read the buffer
   __syncwarp();
   uint8_t* row = buf + lane * 128;
 #pragma unroll
@@ -165,6 +254,27 @@ __device__ __forceinline__ void stage_store(const CUtensorMap* c, uint8_t* buf, 
     bulk_commit_group();
   }
 }
+// The same with plain stores, a row at a time, for a C that TMA cannot address.
+template <typename E, typename Put>
+__device__ __forceinline__ void emit_plain(E* c, long ld, int rows, int cols, uint8_t* buf, int lane, int x, int y,
+                                           Put&& put) {
+  __syncwarp();
+  uint8_t* row = buf + lane * 128;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(row + ((k ^ (lane & 7)) << 4)) = put(k);
+  __syncwarp();
+  constexpr int kPer = 4 / sizeof(E);
+  for (int r = 0; r < 32 && y + r < rows; ++r) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+    E e[kPer];
+    memcpy(e, &w, 4);
+    E* dst = c + (long)(y + r) * ld + x + lane * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (x + lane * kPer + i < cols) dst[i] = e[i];
+  }
+  __syncwarp();
+}
 
 __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
@@ -172,6 +282,25 @@ __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&v)[32]) {
   tmem_wait_ld();
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 64 columns v[at ..] of an intermediate operand (dz, dg, du): the type's
+// rounding, or three bf16 planes, each the rounding of what the ones before
+// leave (v is used up).
+template <typename T, bool SPLIT>
+__device__ __forceinline__ void emit_operand(const Params& p, const CUtensorMap* c, float (&v)[128], int at,
+                                             uint8_t* buf, int lane, int x, int y) {
+#pragma unroll
+  for (int pl = 0; pl < (SPLIT ? 3 : 1); ++pl) {
+    emit(c, buf, lane, x, y + pl * p.c_plane, false, [&](int k) {
+      const float* q = v + at + 8 * k;
+      return make_uint4(pack2<T>(q[0], q[1]), pack2<T>(q[2], q[3]), pack2<T>(q[4], q[5]), pack2<T>(q[6], q[7]));
+    });
+    if (SPLIT && pl < 2) {
+#pragma unroll
+      for (int j = 0; j < 64; ++j) v[at + j] -= DT<T>::to(DT<T>::from(v[at + j]));
+    }
+  }
 }
 
 // Gate and its slope.  silu: a = g s, a' = s (1 + g (1 - s)) with s = 1 / (1 +
@@ -196,199 +325,256 @@ struct RowStats {
 };
 
 template <bool SUM>
-__device__ __forceinline__ void ce_fwd_tile(const Params& p, uint32_t taddr, int row, int col0, int lane, int label,
+__device__ __forceinline__ void ce_fwd_tile(const Params& p, float (&v)[128], int row, int col0, int lane, int label,
                                             RowStats& st) {
   const EpiArgs& ep = p.ep;
-#pragma unroll 1
-  for (int c = 0; c < kBN / 64; ++c) {
-    const int col = col0 + c * 32;
-    if (col >= p.N) break;
-    // lane j holds column j's bias in base 2, -inf past the vocabulary (whose accumulators are 0)
-    const float b = col + lane < p.N ? (ep.bias != nullptr ? __ldg(ep.bias + col + lane) : 0.f) : -INFINITY;
-    float v[32];
-    tmem_ld32f(taddr + c * 32, v);
-    const bool plain = ep.bias == nullptr && col + 32 <= p.N;
-    const int ly = label - col;
-    if (ly >= 0 && ly < 32) {
-      float zy = 0.f;
+  const int ly = label - col0;
+  if (ly >= 0 && ly < 128) {
+    float zy = 0.f;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) zy = j == ly ? v[j] : zy;
-      ep.zy[row] = zy + (ep.bias != nullptr ? __ldg(ep.bias + label) : 0.f);
+    for (int j = 0; j < 128; ++j) zy = j == ly ? v[j] : zy;
+    ep.zy[row] = zy + (ep.bias != nullptr ? __ldg(ep.bias + label) : 0.f);
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int col = col0 + c * 32;
+    if (col >= p.N) continue;
+    float* w = v + c * 32;
+    if (ep.bias != nullptr) {
+      add_bias(ep.bias, col, p.N, -INFINITY, w);
+    } else if (col + 32 > p.N) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) w[j] = col + j < p.N ? w[j] : -INFINITY;
     }
     if constexpr (SUM) {
       float s = 0.f;
+      if (col + 32 <= p.N) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float bj = __shfl_sync(0xffffffffu, b, j);
-        s += col + j < p.N ? v[j] + bj : 0.f;
+        for (int j = 0; j < 32; ++j) s += w[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) s += col + j < p.N ? w[j] : 0.f;
       }
       st.sum += s;
     }
-    if (plain) {
+    float m0 = max3(w[0], w[1], w[2]), m1 = max3(w[3], w[4], w[5]);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] *= kLog2e;
-    } else {
-      const float b2 = b * kLog2e;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], kLog2e, __shfl_sync(0xffffffffu, b2, j));
+    for (int j = 6; j < 30; j += 4) {
+      m0 = max3(m0, w[j], w[j + 1]);
+      m1 = max3(m1, w[j + 2], w[j + 3]);
     }
-    float m0 = v[0], m1 = v[1], m2 = v[2], m3 = v[3];
-#pragma unroll
-    for (int j = 4; j < 32; j += 4) {
-      m0 = fmaxf(m0, v[j]); m1 = fmaxf(m1, v[j + 1]); m2 = fmaxf(m2, v[j + 2]); m3 = fmaxf(m3, v[j + 3]);
-    }
-    const float m = fmaxf(st.m, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
+    const float m = fmaxf(st.m, max3(m0, m1, fmaxf(w[30], w[31])) * kLog2e);
     const float ref = m == -INFINITY ? 0.f : m;   // nothing but -inf so far: every power is 0
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
-      s0 += ex2(v[j] - ref); s1 += ex2(v[j + 1] - ref); s2 += ex2(v[j + 2] - ref); s3 += ex2(v[j + 3] - ref);
+      fma2(w[j], w[j + 1], kLog2e, -ref);
+      fma2(w[j + 2], w[j + 3], kLog2e, -ref);
+      add2f(s0, s1, ex2(w[j]), ex2(w[j + 1]));
+      add2f(s2, s3, ex2(w[j + 2]), ex2(w[j + 3]));
     }
     st.s = fmaf(st.s, ex2(st.m - ref), (s0 + s1) + (s2 + s3));
     st.m = m;
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void ce_bwd_tile(const Params& p, uint32_t taddr, int row, int col0, uint8_t* buf, int lane) {
+// What the cross entropy's gradient needs of a thread's row.  A row that takes
+// no part (past M, ignored, bad label) gets zeros.
+struct RowGrad {
+  bool part;
+  int label;      // the label's column of this piece, if it lies in it
+  float l2, g;    // lse in base 2, the row's factor
+};
+template <bool SPLIT>
+__device__ __forceinline__ RowGrad ce_bwd_row(const Params& p, int row, bool report) {
   const EpiArgs& ep = p.ep;
-  // a row that takes no part (past M, ignored, bad label) gets zeros
-  bool part = false;
-  int label = -1;       // the label's column of this piece, if it lies in it
-  float l2 = 0.f, g = 0.f;
+  RowGrad r{false, -1, 0.f, 0.f};
   if (row < p.M) {
-    const long y = ep.labels[row];
-    part = y != ep.ignore_index && y >= 0 && y < ep.V;
-    if (part) {
-      label = (int)y - ep.v0;
-      l2 = ep.lse[row] * kLog2e;
-      g = ep.dloss[row];
-    } else if (y != ep.ignore_index && col0 == 0) {
+    const long y = __ldg(reinterpret_cast<const long long*>(ep.labels) + row);
+    const float lse = __ldg(ep.lse + row), dl = __ldg(ep.dloss + row);
+    r.part = y != ep.ignore_index && y >= 0 && y < ep.V;
+    if (r.part) {
+      r.label = (int)y - ep.v0;
+      r.l2 = lse * kLog2e;
+      r.g = dl;
+      if constexpr (!SPLIT) r.g = dl / __ldg(ep.dz_scale) * __ldg(ep.dz_scale + 1);
+    } else if (y != ep.ignore_index && report) {
       atomicOr(p.status, DEV_BAD_INDEX);
     }
   }
-  const float uni = ep.smoothing / (float)ep.V, hit = 1.0f - ep.smoothing;
-  const float zs = ep.dz_scale != nullptr ? __ldg(ep.dz_scale) : 1.0f;
-#pragma unroll 1
-  for (int c = 0; c < kBN / 128; ++c) {
-    const int col = col0 + c * 64;
-    if (col >= p.N) break;
-    uint32_t w[32];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int cc = col + h * 32;
-      float v[32];
-      tmem_ld32f(taddr + c * 64 + h * 32, v);
-      if (ep.bias == nullptr && cc + 32 <= p.N) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(v[j], kLog2e, -l2));
-      } else {
-        const float b2 = (cc + lane < p.N ? (ep.bias != nullptr ? __ldg(ep.bias + cc + lane) : 0.f) : -INFINITY) * kLog2e;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(v[j], kLog2e, __shfl_sync(0xffffffffu, b2, j)) - l2);
-      }
-      if (ep.smoothing > 0.f) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] -= uni;
-      }
-      const int ly = label - cc;
-      if (part && ly >= 0 && ly < 32) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = j == ly ? v[j] - hit : v[j];
-      }
-      if (part) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= g;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j) w[h * 16 + j] = pack2<T>(v[2 * j] * zs, v[2 * j + 1] * zs);
-      if (ep.col_part != nullptr) {
-        const float s = warp_col_sum32(v, lane);
-        if (cc + lane < p.N && row - lane < p.M) ep.col_part[(size_t)(row >> 5) * ep.ld_col + cc + lane] = s;
-      }
-    }
-    stage_store(&p.c[0], buf, lane, col, row - lane, false,
-                [&](int k) { return make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]); });
-  }
+  return r;
 }
 
-// 64 output columns col .. col + 63 from the gates at tg and the ups at tu.
-template <typename T, int ACT, bool BWD>
-__device__ __forceinline__ void gate_tile(const Params& p, uint32_t tg, uint32_t tu, int row, int col, uint8_t* buf,
-                                          int lane) {
+template <typename T, bool SPLIT>
+__device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], const RowGrad& rg, int row, int col0,
+                                            uint8_t* buf, int lane) {
   const EpiArgs& ep = p.ep;
-  uint32_t wg[32], wu[BWD ? 32 : 1];
+  const bool part = rg.part;
+  const int label = rg.label;
+  const float l2 = rg.l2, g = rg.g;
+  // 16-bit dz is held as g ((p - e / V) / (1 - e) - [v = y]) with g = dloss / max |dloss| (times 2^14 in fp16): with one
+  // dloss for all rows, as a mean's, the label's entry is then near -1, which 16 bits hold exactly.  (As dloss (p - (1 - e)
+  // [v = y] - e / V) those entries, which make up most of dx and dW, were all off by the same rounding of dloss: dx and
+  // dW 3.0e-3 from the exact gradients in norm instead of 1.7e-3 at 1999 x 768 x 50021 in bf16.)
+  const float uni = ep.smoothing / (float)ep.V;
+  const float cs = SPLIT ? 1.0f : 1.0f / (1.0f - ep.smoothing), hit = SPLIT ? 1.0f - ep.smoothing : 1.0f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int cc = col0 + c * 32;
+    float* w = v + c * 32;
+    if (cc >= p.N) continue;
+    // columns past N keep finite values: nothing reads them
+    if (ep.bias != nullptr) add_bias(ep.bias, cc, p.N, 0.f, w);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      fma2(w[j], w[j + 1], kLog2e, -l2);
+      w[j] = ex2(w[j]);
+      w[j + 1] = ex2(w[j + 1]);
+    }
+    if (ep.smoothing > 0.f) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) fma2(w[j], w[j + 1], cs, -uni * cs);
+    }
+    const int ly = label - cc;
+    if (part && ly >= 0 && ly < 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) w[j] = j == ly ? w[j] - hit : w[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) mul2(w[j], w[j + 1], g);
+    if (!part) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) w[j] = 0.f;
+    }
+  }
+  const int y = row - lane;
+  if (ep.col_part != nullptr) {
+    if (lane == 0) bulk_wait_read_all();
+    __syncwarp();
+    float* to = ep.col_part + (size_t)(y >> 5) * ep.ld_col + col0;
+    const int n = y < p.M ? p.N - col0 : 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (col0 + c * 32 < p.N) col_sum32(v + c * 32, buf, lane, to + c * 32, n - c * 32);
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    if (col0 + c * 64 < p.N) emit_operand<T, SPLIT>(p, &p.c[0], v, c * 64, buf, lane, col0 + c * 64, y);
+}
+
+// Copies this warp's 32 x 64 block of dh into the staging buffer (swizzled as
+// emit's), whose last store has to have been read; rows are multiples of 16
+// bytes.
+template <typename T>
+__device__ __forceinline__ void fetch_dh(const Params& p, uint8_t* buf, int lane, int col, int row0) {
+  if (lane == 0) bulk_wait_read_all();
+  __syncwarp();
+  const int k = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = i * 4 + (lane >> 3);
+    const bool in = row0 + r < p.M && col + 8 * k < p.N;
+    const T* src = static_cast<const T*>(p.ep.dh) + (in ? (size_t)(row0 + r) * p.N + col + 8 * k : 0);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(buf + r * 128 + ((k ^ (r & 7)) << 4))),
+                 "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// 64 output columns col .. col + 63 from the gates v[0..63] and the ups v[64..127].
+template <typename T, bool SPLIT, int ACT, bool BWD>
+__device__ __forceinline__ void gate_tile(const Params& p, float (&v)[128], int row, int col, uint8_t* buf, int lane) {
+  using TD = typename std::conditional<SPLIT, float, T>::type;   // the operator's type
+  const EpiArgs& ep = p.ep;
+  if constexpr (BWD && !SPLIT) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+  }
+  if (col >= p.N) return;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int cc = col + h * 32;
-    float g[32], u[32];
-    uint4 d[BWD ? 4 : 1];
-    if constexpr (BWD) {
-      // rows are multiples of 16 bytes: an 8-column piece is inside or outside as a whole
-      const T* dh = static_cast<const T*>(ep.dh) + (size_t)row * p.N + cc;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        d[i] = row < p.M && cc + 8 * i < p.N ? __ldg(reinterpret_cast<const uint4*>(dh) + i) : make_uint4(0, 0, 0, 0);
-    }
-    tmem_ld32f(tg + h * 32, g);
-    tmem_ld32f(tu + h * 32, u);
-    if (ep.bias != nullptr) {
-      const float b = cc + lane < p.N ? __ldg(ep.bias + cc + lane) : 0.f;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) g[j] += __shfl_sync(0xffffffffu, b, j);
-    }
-    if (ep.bias2 != nullptr) {
-      const float b = cc + lane < p.N ? __ldg(ep.bias2 + cc + lane) : 0.f;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) u[j] += __shfl_sync(0xffffffffu, b, j);
-    }
+    float* g = v + h * 32;
+    float* u = v + 64 + h * 32;
+    if (ep.bias != nullptr) add_bias(ep.bias, cc, p.N, 0.f, g);
+    if (ep.bias2 != nullptr) add_bias(ep.bias2, cc, p.N, 0.f, u);
     if constexpr (!BWD) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        float a0, a1, da;
-        gate<ACT, false>(g[j], a0, da);
-        gate<ACT, false>(g[j + 1], a1, da);
-        wg[h * 16 + j / 2] = pack2<T>(a0 * u[j], a1 * u[j + 1]);
+      for (int j = 0; j < 32; ++j) {
+        float a, da;
+        gate<ACT, false>(g[j], a, da);
+        g[j] = a * u[j];
       }
     } else {
-      const uint32_t* dw = reinterpret_cast<const uint32_t*>(d);
+      constexpr int kPer = 16 / sizeof(TD);   // values of dh in 16 bytes
+      const TD* dh = static_cast<const TD*>(ep.dh) + (size_t)row * p.N + cc;
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        T t[2];
-        memcpy(t, &dw[j / 2], 4);
+      for (int j = 0; j < 32; j += kPer) {
+        TD d[kPer];
+        if (ep.dh_vec) {
+          uint4 q;
+          if constexpr (!SPLIT)   // fetch_dh has put it into the staging buffer
+            q = *reinterpret_cast<const uint4*>(buf + lane * 128 + (((h * 4 + j / 8) ^ (lane & 7)) << 4));
+          else   // rows are multiples of 16 bytes: a piece is inside or outside as a whole
+            q = row < p.M && cc + j < p.N ? __ldg(reinterpret_cast<const uint4*>(dh + j)) : make_uint4(0, 0, 0, 0);
+          memcpy(d, &q, 16);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < kPer; ++i) d[i] = row < p.M && cc + j + i < p.N ? dh[j + i] : DT<TD>::from(0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
           float a, da;
           gate<ACT, true>(g[j + i], a, da);
-          const float dd = DT<T>::to(t[i]);
+          const float dd = DT<TD>::to(d[i]);
           g[j + i] = dd * u[j + i] * da;
           u[j + i] = dd * a;
         }
-        wg[h * 16 + j / 2] = pack2<T>(g[j], g[j + 1]);
-        wu[h * 16 + j / 2] = pack2<T>(u[j], u[j + 1]);
-      }
-      const bool put = cc + lane < p.N && row - lane < p.M;
-      if (ep.col_part != nullptr) {
-        const float s = warp_col_sum32(g, lane);
-        if (put) ep.col_part[(size_t)(row >> 5) * ep.ld_col + cc + lane] = s;
-      }
-      if (ep.col_part2 != nullptr) {
-        const float s = warp_col_sum32(u, lane);
-        if (put) ep.col_part2[(size_t)(row >> 5) * ep.ld_col + cc + lane] = s;
       }
     }
   }
-  if (col >= p.N) return;
-  stage_store(&p.c[0], buf, lane, col, row - lane, false,
-              [&](int k) { return make_uint4(wg[4 * k], wg[4 * k + 1], wg[4 * k + 2], wg[4 * k + 3]); });
-  if constexpr (BWD)
-    stage_store(&p.c[1], buf, lane, col, row - lane, false,
-                [&](int k) { return make_uint4(wu[4 * k], wu[4 * k + 1], wu[4 * k + 2], wu[4 * k + 3]); });
+  if constexpr (BWD) {
+    const int y = row - lane;
+    __syncwarp();   // dh has been read from the staging buffer
+    if (ep.col_part != nullptr || ep.col_part2 != nullptr) {
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float* part = k == 0 ? ep.col_part : ep.col_part2;
+        if (part == nullptr) continue;
+        float* to = part + (size_t)(y >> 5) * ep.ld_col + col;
+        const int n = y < p.M ? p.N - col : 0;
+        col_sum32(v + k * 64, buf, lane, to, n);
+        col_sum32(v + k * 64 + 32, buf, lane, to + 32, n - 32);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) emit_operand<T, SPLIT>(p, &p.c[k], v, k * 64, buf, lane, col, y);
+  } else if constexpr (!SPLIT) {
+    auto put = [&](int k) {
+      const float* q = v + 8 * k;
+      return make_uint4(pack2<T>(q[0], q[1]), pack2<T>(q[2], q[3]), pack2<T>(q[4], q[5]), pack2<T>(q[6], q[7]));
+    };
+    if (p.plain == nullptr) emit(&p.c[0], buf, lane, col, row - lane, false, put);
+    else emit_plain(static_cast<T*>(p.plain), p.plain_ld, p.M, p.N, buf, lane, col, row - lane, put);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      auto put = [&](int k) {
+        const float* q = v + h * 32 + 4 * k;
+        return make_uint4(__float_as_uint(q[0]), __float_as_uint(q[1]), __float_as_uint(q[2]), __float_as_uint(q[3]));
+      };
+      const int cc = col + h * 32;
+      if (cc >= p.N) break;
+      if (p.plain == nullptr) emit(&p.c[0], buf, lane, cc, row - lane, false, put);
+      else emit_plain(static_cast<float*>(p.plain), p.plain_ld, p.M, p.N, buf, lane, cc, row - lane, put);
+    }
+  }
 }
 
+// 128 columns of a 16-bit C straight from tensor memory.
 template <typename T>
 __device__ __forceinline__ void store_tile(const Params& p, const CUtensorMap* c, uint32_t taddr, int row0, int col0,
                                            uint8_t* buf, int lane) {
@@ -404,11 +590,11 @@ __device__ __forceinline__ void store_tile(const Params& p, const CUtensorMap* c
 #pragma unroll
       for (int j = 0; j < 16; ++j) w[h * 16 + j] = pack2<T>(v[2 * j] * sc, v[2 * j + 1] * sc);
     }
-    stage_store(c, buf, lane, col0 + c0, row0, false,
-                [&](int k) { return make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]); });
+    emit(c, buf, lane, col0 + c0, row0, false,
+         [&](int k) { return make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]); });
   }
 }
-
+// 128 columns of an fp32 C: straight from tensor memory, or the register sums.
 __device__ __forceinline__ void slab_tile(const Params& p, const CUtensorMap* c, uint32_t taddr, int row0, int col0,
                                           uint8_t* buf, int lane, bool add) {
 #pragma unroll 1
@@ -417,14 +603,39 @@ __device__ __forceinline__ void slab_tile(const Params& p, const CUtensorMap* c,
     uint32_t w[32];
     tmem_ld32(taddr + c0, w);
     tmem_wait_ld();
-    stage_store(c, buf, lane, col0 + c0, row0, add,
-                [&](int k) { return make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]); });
+    emit(c, buf, lane, col0 + c0, row0, add,
+         [&](int k) { return make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]); });
+  }
+}
+__device__ __forceinline__ void slab_regs(const Params& p, const CUtensorMap* c, const float (&v)[128], int row0,
+                                          int col0, uint8_t* buf, int lane, bool add) {
+#pragma unroll
+  for (int c0 = 0; c0 < 128; c0 += 32) {
+    if (col0 + c0 >= p.N) continue;
+    emit(c, buf, lane, col0 + c0, row0, add, [&](int k) {
+      const float* q = v + c0 + 4 * k;
+      return make_uint4(__float_as_uint(q[0]), __float_as_uint(q[1]), __float_as_uint(q[2]), __float_as_uint(q[3]));
+    });
   }
 }
 
-template <typename T, bool AMN, bool BMN, int EPI>
-__global__ void __launch_bounds__(kThreads, 1) train_gemm_kernel(const __grid_constant__ Params p) {
+// Whether an epilogue adds a tile's chunks in registers, and the block's shape.
+template <bool SPLIT, int EPI>
+struct Shape {
+  static constexpr bool kRegs = SPLIT || EPI >= CE_FWD;
+  static constexpr int kFirstEpi = kRegs ? 4 : 2;
+  static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+};
+
+template <typename T, bool SPLIT, bool AMN, bool BMN, int EPI>
+__global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_kernel(const __grid_constant__ Params p) {
   constexpr bool kGate = EPI == GATE_FWD || EPI == GATE_BWD;
+  constexpr int kPlanes = SPLIT ? 3 : 1;
+  static_assert(kStages % kPlanes == 0, "the planes of a block take consecutive stages");
+  static_assert(!SPLIT || EPI != STORE, "a split product has fp32 results");
+  constexpr bool kRegs = Shape<SPLIT, EPI>::kRegs;
+  constexpr int kFirstEpi = Shape<SPLIT, EPI>::kFirstEpi;
+  constexpr bool kStageDh = EPI == GATE_BWD && !SPLIT;   // 64 columns of 16 bits are a row of the staging buffer
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -468,131 +679,153 @@ __global__ void __launch_bounds__(kThreads, 1) train_gemm_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
-      const uint32_t full0 = mapa_shared(smem_u32(full), 0);
-      int stage = 0;
-      uint32_t phase = 0;
-      long issued = 0;
-      bool stop = false;
-      for (int u = first; u < num_units && !stop; u += stride) {
-        const Unit t = unit_of(p, u);
-        const int ra = (t.m * 2 + rank) * kBM;
-        for (int r = 0; r < t.nr && !stop; ++r) {
-          const int rb = kGate ? (t.n0 + r) * (kBN / 2) : (t.n0 + r) * kBN + rank * (kBN / 2);
-          for (int kb = t.kb0; kb < t.kb1; ++kb) {
-            if (*abort_flag || !mbar_wait(&empty[stage], phase ^ 1)) {
-              atomicOr(p.status, DEV_TIMEOUT);
-              *abort_flag = 1;
-              stop = true;
-              break;
-            }
-            const int seg = kb >= p.kb_seg ? 1 : 0;
-            const int k = (kb - seg * p.kb_seg) * kBK;
-            const CUtensorMap* ma = &p.a[seg + t.z];
-            const CUtensorMap* mb = &p.b[kGate ? rank : seg];
-            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
-            const uint32_t bar = full0 + 8 * stage;
-            uint8_t* da = sA + stage * kABytes;
-            uint8_t* db = sB + stage * kBBytes;
-            if constexpr (AMN) {
-              tma_load_2d_pair(da, ma, bar, ra, k);
-              tma_load_2d_pair(da + 8192, ma, bar, ra + 64, k);
-            } else {
-              tma_load_2d_pair(da, ma, bar, k, ra);
-            }
-            if constexpr (BMN) {
-              tma_load_2d_pair(db, mb, bar, rb, k);
-              tma_load_2d_pair(db + 8192, mb, bar, rb + 64, k);
-            } else {
-              tma_load_2d_pair(db, mb, bar, k, rb);
-            }
-            ++issued;
-            if (++stage == kStages) {
-              stage = 0;
-              phase ^= 1;
+  if (warp < kFirstEpi) {
+    if constexpr (kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    if (warp == 0) {
+      // ------------------------------------------------------------ TMA producer (both CTAs)
+      if (lane == 0) {
+        const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+        int stage = 0;
+        uint32_t phase = 0;
+        long issued = 0;
+        bool stop = false;
+        for (int u = first; u < num_units && !stop; u += stride) {
+          const Unit t = unit_of(p, u);
+          const int ra = (t.m * 2 + rank) * kBM;
+          for (int r = 0; r < t.nr && !stop; ++r) {
+            const int rb = kGate ? (t.n0 + r) * (kBN / 2) : (t.n0 + r) * kBN + rank * (kBN / 2);
+            for (int q = t.kb0 * kPlanes; q < t.kb1 * kPlanes; ++q) {
+              if (*abort_flag || !mbar_wait(&empty[stage], phase ^ 1)) {
+                atomicOr(p.status, DEV_TIMEOUT);
+                *abort_flag = 1;
+                stop = true;
+                break;
+              }
+              const int kb = SPLIT ? q / 3 : q, plane = SPLIT ? q - 3 * kb : 0;
+              const int seg = kb >= p.kb_seg ? 1 : 0;
+              const int k = (kb - seg * p.kb_seg) * kBK;
+              const CUtensorMap* ma = &p.a[seg + t.z];
+              const CUtensorMap* mb = &p.b[kGate ? rank : seg];
+              if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+              const uint32_t bar = full0 + 8 * stage;
+              uint8_t* da = sA + stage * kABytes;
+              uint8_t* db = sB + stage * kBBytes;
+              // the planes lie one after another along the stored matrix's rows
+              const int pa = plane * p.a_plane, pb = plane * p.b_plane;
+              if constexpr (AMN) {
+                tma_load_2d_pair(da, ma, bar, ra, k + pa);
+                tma_load_2d_pair(da + 8192, ma, bar, ra + 64, k + pa);
+              } else {
+                tma_load_2d_pair(da, ma, bar, k, ra + pa);
+              }
+              if constexpr (BMN) {
+                tma_load_2d_pair(db, mb, bar, rb, k + pb);
+                tma_load_2d_pair(db + 8192, mb, bar, rb + 64, k + pb);
+              } else {
+                tma_load_2d_pair(db, mb, bar, k, rb + pb);
+              }
+              ++issued;
+              if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+              }
             }
           }
         }
+        // Every copy issued must land before the CTAs exit.  The even CTA's
+        // barriers count the bytes of both CTAs of the pair.
+        if (leader) {
+          const long pending = issued < kStages ? issued : kStages;
+          for (long i = 0; i < pending; ++i) {
+            if (--stage < 0) {
+              stage = kStages - 1;
+              phase ^= 1;
+            }
+            mbar_wait(&full[stage], phase);
+          }
+        }
       }
-      // Every copy issued must land before the CTAs exit.  The even CTA's
-      // barriers count the bytes of both CTAs of the pair.
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer (the even CTA)
       if (leader) {
-        const long pending = issued < kStages ? issued : kStages;
-        for (long i = 0; i < pending; ++i) {
-          if (--stage < 0) {
-            stage = kStages - 1;
-            phase ^= 1;
-          }
-          mbar_wait(&full[stage], phase);
-        }
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (the even CTA)
-    if (leader) {
-      constexpr uint32_t idesc =
-          idesc_f16<T, 2 * kBM, kBN>() | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
-      int stage = 0;
-      uint32_t phase = 0;
-      int acc = 0;
-      bool ok = true;
-      for (int u = first; u < num_units && ok; u += stride) {
-        const Unit t = unit_of(p, u);
-        for (int r = 0; r < t.nr && ok; ++r, ++acc) {
-          if (__any_sync(0xffffffffu, *abort_flag)) {
-            ok = false;
-            break;
-          }
-          const int buf = acc & 1;
-          if (!__all_sync(0xffffffffu, mbar_wait(&tempty[buf], ((acc >> 1) & 1) ^ 1))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d = tmem_base + buf * kBN;
-          for (int kb = t.kb0; kb < t.kb1; ++kb) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t aa = smem_u32(sA + stage * kABytes), bb = smem_u32(sB + stage * kBBytes);
-            const uint64_t da = AMN ? smem_desc_mnmajor(aa) : smem_desc_kmajor<128>(aa);
-            const uint64_t db = BMN ? smem_desc_mnmajor(bb) : smem_desc_kmajor<128>(bb);
+        constexpr uint32_t idesc =
+            idesc_f16<T, 2 * kBM, kBN>() | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
+        int stage = 0;
+        uint32_t phase = 0;
+        int acc = 0;
+        bool ok = true;
+        for (int u = first; u < num_units && ok; u += stride) {
+          const Unit t = unit_of(p, u);
+          for (int r = 0; r < t.nr && ok; ++r) {
+            for (int c0 = t.kb0; c0 < t.kb1 && ok; c0 += p.kb_chunk, ++acc) {
+              if (__any_sync(0xffffffffu, *abort_flag)) {
+                ok = false;
+                break;
+              }
+              const int buf = acc & 1;
+              if (!__all_sync(0xffffffffu, mbar_wait(&tempty[buf], ((acc >> 1) & 1) ^ 1))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t d = tmem_base + buf * kBN;
+              const int c1 = min(c0 + p.kb_chunk, t.kb1);
+              for (int kb = c0; kb < c1 && ok; ++kb) {
 #pragma unroll
-            for (int k = 0; k < kBK / 16; ++k)
-              umma_f16_ss_pair_warp(d, da + k * (AMN ? 128 : 2), db + k * (BMN ? 128 : 2), idesc,
-                                    kb != t.kb0 || k != 0);
-            umma_commit_pair_warp(&empty[stage], (uint16_t)0x3);
-            if (++stage == kStages) {
-              stage = 0;
-              phase ^= 1;
+                for (int pl = 0; pl < kPlanes; ++pl)
+                  ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[stage + pl], phase));
+                if (!ok) break;
+                tc_fence_after();
+                uint64_t da[kPlanes], db[kPlanes];
+#pragma unroll
+                for (int pl = 0; pl < kPlanes; ++pl) {
+                  const uint32_t aa = smem_u32(sA + (stage + pl) * kABytes), bb = smem_u32(sB + (stage + pl) * kBBytes);
+                  da[pl] = AMN ? smem_desc_mnmajor(aa) : smem_desc_kmajor<128>(aa);
+                  db[pl] = BMN ? smem_desc_mnmajor(bb) : smem_desc_kmajor<128>(bb);
+                }
+                // planes (i, j) with i + j = 2, then 1, then 0: the small products first
+#pragma unroll
+                for (int order = kPlanes - 1; order >= 0; --order)
+#pragma unroll
+                  for (int i = 0; i <= order; ++i)
+#pragma unroll
+                    for (int k = 0; k < kBK / 16; ++k)
+                      umma_f16_ss_pair_warp(d, da[i] + k * (AMN ? 128 : 2), db[order - i] + k * (BMN ? 128 : 2), idesc,
+                                            kb != c0 || order != kPlanes - 1 || i != 0 || k != 0);
+#pragma unroll
+                for (int pl = 0; pl < kPlanes; ++pl) umma_commit_pair_warp(&empty[stage + pl], (uint16_t)0x3);
+                stage += kPlanes;
+                if (stage == kStages) {
+                  stage = 0;
+                  phase ^= 1;
+                }
+              }
+              if (ok) umma_commit_pair_warp(&tfull[buf], (uint16_t)0x3);
             }
           }
-          if (!ok) break;
-          umma_commit_pair_warp(&tfull[buf], (uint16_t)0x3);
         }
+        if (!ok && lane == 0) {
+          atomicOr(p.status, DEV_TIMEOUT);
+          *abort_flag = 1;
+        }
+        umma_commit_pair_warp(mma_done, (uint16_t)0x1);   // no MMA may still run when tensor memory is released
+        mbar_wait(mma_done, 0);
       }
-      if (!ok && lane == 0) {
-        atomicOr(p.status, DEV_TIMEOUT);
-        *abort_flag = 1;
-      }
-      umma_commit_pair_warp(mma_done, (uint16_t)0x1);   // no MMA may still run when tensor memory is released
-      mbar_wait(mma_done, 0);
     }
   } else {
+    if constexpr (kRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
     // ------------------------------------------------------------ epilogue (both CTAs)
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int quarter = warp & 3, half = (warp - kFirstEpi) >> 2;
     const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
-    uint8_t* buf_s = sEpi + (warp - 2) * kEpiStage;
+    uint8_t* buf_s = sEpi + (warp - kFirstEpi) * kEpiStage;
     int acc = 0;
     bool stop = false;
     for (int u = first; u < num_units && !stop; u += stride) {
       const Unit t = unit_of(p, u);
       const int row = (t.m * 2 + rank) * kBM + quarter * 32 + lane;
       RowStats st{-INFINITY, 0.f, 0.f};
+      RowGrad rg{};
+      if constexpr (EPI == CE_BWD) rg = ce_bwd_row<SPLIT>(p, row, t.n0 == 0 && half == 0);
       int label = -1;
       if constexpr (EPI == CE_FWD) {
         if (row < p.M) {
@@ -600,38 +833,104 @@ __global__ void __launch_bounds__(kThreads, 1) train_gemm_kernel(const __grid_co
           label = y >= 0 && y < p.ep.V ? (int)y : -1;
         }
       }
-      for (int r = 0; r < t.nr; ++r, ++acc) {
-        const int buf = acc & 1;
-        const bool ok = mbar_wait(&tfull[buf], (acc >> 1) & 1);
-        // tcgen05.ld is warp-collective: the stop decision is warp-uniform
-        if (__any_sync(0xffffffffu, !ok || *abort_flag)) {
-          if (lane == 0) atomicOr(p.status, DEV_TIMEOUT);
-          *abort_flag = 1;
+      for (int r = 0; r < t.nr && !stop; ++r) {
+        const int col = (t.n0 + r) * kBN + half * (kBN / 2);
+        const uint32_t tl = tmem_base + ((uint32_t)(quarter * 32) << 16);
+        float v[kRegs ? 128 : 1];
+        // waits for the accumulator of the next chunk; false: the kernel is winding down
+        auto chunk_ready = [&](int buf) {
+          const bool ok = mbar_wait(&tfull[buf], (acc >> 1) & 1);
+          // tcgen05.ld is warp-collective: the stop decision is warp-uniform
+          if (__any_sync(0xffffffffu, !ok || *abort_flag)) {
+            if (lane == 0) atomicOr(p.status, DEV_TIMEOUT);
+            *abort_flag = 1;
+            return false;
+          }
+          tc_fence_after();
+          return true;
+        };
+        auto chunk_taken = [&](int buf) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + 8 * buf);
+          ++acc;
+        };
+        // of this thread's 128 columns, where the c-th 32 start (gates: this half's 64 gate columns, then its 64 up columns)
+        auto column = [&](int c) {
+          return (uint32_t)(kGate ? half * 64 + (c & 1) * 32 + (c >> 1) * (kBN / 2) : half * (kBN / 2) + c * 32);
+        };
+        // what the epilogue reads from memory, on its way while the products run
+        float warm = 0.f;
+        if constexpr (EPI >= CE_FWD) {
+          const int c = kGate ? (t.n0 + r) * (kBN / 2) + half * 64 + lane * 2 : col + lane * 4;
+          const int at = min(c, p.N - 1);
+          if (p.ep.bias != nullptr) warm = __ldg(p.ep.bias + at);
+          if (kGate && p.ep.bias2 != nullptr) warm += __ldg(p.ep.bias2 + at);
+        }
+        if constexpr (kStageDh) {
+          if (p.ep.dh_vec) fetch_dh<T>(p, buf_s, lane, (t.n0 + r) * (kBN / 2) + half * 64, row - lane);
+        }
+        if (!chunk_ready(acc & 1)) {
           stop = true;
           break;
         }
-        tc_fence_after();
-        const uint32_t tl = tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * kBN;
-        const int col = (t.n0 + r) * kBN + half * (kBN / 2);
-        if constexpr (EPI == STORE) {
-          store_tile<T>(p, &p.c[t.z], tl + half * (kBN / 2), row - lane, col, buf_s, lane);
-        } else if constexpr (EPI == F32 || EPI == F32_ADD) {
-          slab_tile(p, &p.c[t.z], tl + half * (kBN / 2), row - lane + t.split * p.slab_rows, col, buf_s, lane,
-                    EPI == F32_ADD);
-        } else if constexpr (EPI == CE_FWD) {
-          if (p.ep.part_sum != nullptr) ce_fwd_tile<true>(p, tl + half * (kBN / 2), row, col, lane, label, st);
-          else ce_fwd_tile<false>(p, tl + half * (kBN / 2), row, col, lane, label, st);
-        } else if constexpr (EPI == CE_BWD) {
-          ce_bwd_tile<T>(p, tl + half * (kBN / 2), row, col, buf_s, lane);
+        asm volatile("" ::"f"(warm));
+        if constexpr (kRegs) {
+          {
+            const uint32_t tb = tl + (acc & 1) * kBN;
+            uint32_t w[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tb + column(c), w[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[c * 32 + j] = __uint_as_float(w[c][j]);
+            chunk_taken(acc & 1);
+          }
+#pragma unroll 1
+          for (int c0 = t.kb0 + p.kb_chunk; c0 < t.kb1; c0 += p.kb_chunk) {
+            if (!chunk_ready(acc & 1)) {
+              stop = true;
+              break;
+            }
+            const uint32_t tb = tl + (acc & 1) * kBN;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t w[32];
+              tmem_ld32(tb + column(c), w);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; j += 2)
+                add2f(v[c * 32 + j], v[c * 32 + j + 1], __uint_as_float(w[j]), __uint_as_float(w[j + 1]));
+            }
+            chunk_taken(acc & 1);
+          }
         } else {
-          const int oc = (t.n0 + r) * (kBN / 2) + half * 64;
-          const uint32_t tg = tl + half * 64, tu = tg + kBN / 2;
-          if (p.ep.act == ACT_SILU) gate_tile<T, ACT_SILU, EPI == GATE_BWD>(p, tg, tu, row, oc, buf_s, lane);
-          else gate_tile<T, ACT_GELU, EPI == GATE_BWD>(p, tg, tu, row, oc, buf_s, lane);
+          const int buf = acc & 1;
+          const uint32_t tb = tl + buf * kBN;
+          if constexpr (EPI == STORE)
+            store_tile<T>(p, &p.c[t.z], tb + half * (kBN / 2), row - lane, col, buf_s, lane);
+          else
+            slab_tile(p, &p.c[t.z], tb + half * (kBN / 2), row - lane + t.split * p.slab_rows, col, buf_s, lane,
+                      EPI == F32_ADD);
+          chunk_taken(buf);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * buf);
+        if constexpr (kRegs) {
+          if (stop) break;
+          if constexpr (EPI == CE_FWD) {
+            if (p.ep.part_sum != nullptr) ce_fwd_tile<true>(p, v, row, col, lane, label, st);
+            else ce_fwd_tile<false>(p, v, row, col, lane, label, st);
+          } else if constexpr (EPI == CE_BWD) {
+            ce_bwd_tile<T, SPLIT>(p, v, rg, row, col, buf_s, lane);
+          } else if constexpr (kGate) {
+            const int oc = (t.n0 + r) * (kBN / 2) + half * 64;
+            if (p.ep.act == ACT_SILU) gate_tile<T, SPLIT, ACT_SILU, EPI == GATE_BWD>(p, v, row, oc, buf_s, lane);
+            else gate_tile<T, SPLIT, ACT_GELU, EPI == GATE_BWD>(p, v, row, oc, buf_s, lane);
+          } else {
+            slab_regs(p, &p.c[t.z], v, row - lane + t.split * p.slab_rows, col, buf_s, lane, EPI == F32_ADD);
+          }
+        }
       }
       if constexpr (EPI == CE_FWD) {
         if (!stop && row < p.M) {
@@ -654,11 +953,12 @@ __global__ void __launch_bounds__(kThreads, 1) train_gemm_kernel(const __grid_co
 }
 
 // Launches over the resident CTA pairs of the current device.
-template <typename T, bool AMN, bool BMN, int EPI>
+template <typename T, bool SPLIT, bool AMN, bool BMN, int EPI>
 cudaError_t launch(const Params& p, int num_sms, cudaStream_t s) {
-  auto kern = train_gemm_kernel<T, AMN, BMN, EPI>;
+  auto kern = train_gemm_kernel<T, SPLIT, AMN, BMN, EPI>;
+  using S = Shape<SPLIT, EPI>;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -674,6 +974,13 @@ cudaError_t launch(const Params& p, int num_sms, cudaStream_t s) {
   cudaError_t e = setup.run([&](int d) -> cudaError_t {
     cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (r != cudaSuccess) return r;
+    if constexpr (S::kRegs) {
+      // setmaxnreg.inc waits for registers of the block's launch allocation: refuse to launch when that is short
+      cudaFuncAttributes fa;
+      r = cudaFuncGetAttributes(&fa, kern);
+      if (r != cudaSuccess) return r;
+      if (fa.numRegs * S::kThreads < 128 * kRegsControl + 256 * kRegsEpi) return cudaErrorInvalidConfiguration;
+    }
     int resident = num_sms / 2, n = 0;
     cudaLaunchConfig_t probe = cfg;
     probe.gridDim = dim3(2 * (num_sms / 2));
@@ -692,23 +999,25 @@ cudaError_t launch(const Params& p, int num_sms, cudaStream_t s) {
 }  // namespace tg
 }  // namespace jepa
 
-// The instantiations for one type; each type has its own translation unit.
-#define JEPA_TRAIN_GEMM_INSTANCES(T, NAME)                                                                  \
+// The instantiations for one operand type; each has its own translation unit.
+#define JEPA_TRAIN_GEMM_INSTANCES(T, SPLIT, NAME)                                                           \
   namespace jepa {                                                                                          \
   namespace tg {                                                                                            \
   cudaError_t NAME(bool amn, bool bmn, int epi, const Params& p, int num_sms, cudaStream_t s) {             \
     if (!amn && !bmn) {                                                                                     \
-      if (epi == CE_FWD) return launch<T, false, false, CE_FWD>(p, num_sms, s);                             \
-      if (epi == CE_BWD) return launch<T, false, false, CE_BWD>(p, num_sms, s);                             \
-      if (epi == GATE_FWD) return launch<T, false, false, GATE_FWD>(p, num_sms, s);                         \
-      if (epi == GATE_BWD) return launch<T, false, false, GATE_BWD>(p, num_sms, s);                         \
+      if (epi == CE_FWD) return launch<T, SPLIT, false, false, CE_FWD>(p, num_sms, s);                      \
+      if (epi == CE_BWD) return launch<T, SPLIT, false, false, CE_BWD>(p, num_sms, s);                      \
+      if (epi == GATE_FWD) return launch<T, SPLIT, false, false, GATE_FWD>(p, num_sms, s);                  \
+      if (epi == GATE_BWD) return launch<T, SPLIT, false, false, GATE_BWD>(p, num_sms, s);                  \
     } else if (!amn) {                                                                                      \
-      if (epi == STORE) return launch<T, false, true, STORE>(p, num_sms, s);                                \
-      if (epi == F32) return launch<T, false, true, F32>(p, num_sms, s);                                    \
-      if (epi == F32_ADD) return launch<T, false, true, F32_ADD>(p, num_sms, s);                            \
+      if constexpr (!SPLIT)                                                                                 \
+        if (epi == STORE) return launch<T, SPLIT, false, true, STORE>(p, num_sms, s);                       \
+      if (epi == F32) return launch<T, SPLIT, false, true, F32>(p, num_sms, s);                             \
+      if (epi == F32_ADD) return launch<T, SPLIT, false, true, F32_ADD>(p, num_sms, s);                     \
     } else if (bmn) {                                                                                       \
-      if (epi == STORE) return launch<T, true, true, STORE>(p, num_sms, s);                                 \
-      if (epi == F32) return launch<T, true, true, F32>(p, num_sms, s);                                     \
+      if constexpr (!SPLIT)                                                                                 \
+        if (epi == STORE) return launch<T, SPLIT, true, true, STORE>(p, num_sms, s);                        \
+      if (epi == F32) return launch<T, SPLIT, true, true, F32>(p, num_sms, s);                              \
     }                                                                                                       \
     return cudaErrorInvalidValue;                                                                           \
   }                                                                                                         \

@@ -1,3 +1,3 @@
 #include "gemm_train.cuh"
 
-JEPA_TRAIN_GEMM_INSTANCES(__nv_bfloat16, gemm_bf16)
+JEPA_TRAIN_GEMM_INSTANCES(__nv_bfloat16, false, gemm_bf16)

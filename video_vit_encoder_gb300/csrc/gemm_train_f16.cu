@@ -1,3 +1,3 @@
 #include "gemm_train.cuh"
 
-JEPA_TRAIN_GEMM_INSTANCES(__half, gemm_f16)
+JEPA_TRAIN_GEMM_INSTANCES(__half, false, gemm_f16)

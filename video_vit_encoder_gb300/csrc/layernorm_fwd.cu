@@ -12,26 +12,55 @@ namespace {
 
 constexpr int kBlock = 256;
 
-template <typename TX, typename TY, int V, int NV, int TPR>
+template <typename TX, typename TY, int V, int NV, int TPR, bool SHIFT>
 __global__ void __launch_bounds__(kBlock) ln_fwd_kernel(const TX* __restrict__ x, const float* __restrict__ w,
                                                         const float* __restrict__ b, TY* __restrict__ y,
                                                         float* __restrict__ mean, float* __restrict__ rstd, long rows,
                                                         int dim, float eps) {
   __shared__ float red[kBlock / 32];
+  extern __shared__ __align__(16) float table[];   // SHIFT: w, then b, in the threads' columns: [NV * V / 4][thread] float4
   constexpr int kRows = kBlock / TPR;   // rows a block works on at a time
-  const int t = threadIdx.x % TPR;
+  constexpr int kTable = NV * V * kBlock;
+  const int tid = threadIdx.x, t = tid % TPR;
+  const long first = (long)blockIdx.x * kRows + tid / TPR;
   const long stride = (long)gridDim.x * kRows;
+  const long total = rows * dim;
+  const int o = SHIFT ? (int)((first * dim) % V) : 0;
   const float inv = 1.0f / (float)dim;
-  for (long row = (long)blockIdx.x * kRows + threadIdx.x / TPR; row < rows; row += stride) {
-    const TX* xr = x + row * dim;
+  if constexpr (SHIFT) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = (t + i * TPR) * V - o + j;
+        const int k = ((i * V + j) / 4 * kBlock + tid) * 4 + j % 4;
+        table[k] = c >= 0 && c < dim ? __ldg(w + c) : 0.f;
+        table[kTable + k] = c >= 0 && c < dim ? __ldg(b + c) : 0.f;
+      }
+  }
+  for (long row = first; row < rows; row += stride) {
     float v[NV][V];
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (t + i * TPR) * V;
+      const int c0 = (t + i * TPR) * V - o;
+      const long at = row * dim + c0;
 #pragma unroll
       for (int j = 0; j < V; ++j) v[i][j] = 0.f;
-      if (c < dim) ln_load<TX, V>(xr + c, v[i]);
+      if (c0 < dim) {
+        if (!SHIFT || at + V <= total) {
+          ln_load<TX, V>(x + at, v[i]);
+        } else {   // the last row's last vector ends with the operand
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (at + j < total) v[i][j] = DT<TX>::to(x[at + j]);
+        }
+        if (SHIFT && !ln_whole<V>(c0, dim)) {   // the neighbouring rows' values
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (c0 + j < 0 || c0 + j >= dim) v[i][j] = 0.f;
+        }
+      }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -41,14 +70,20 @@ __global__ void __launch_bounds__(kBlock) ln_fwd_kernel(const TX* __restrict__ x
     const float mu = s[0] * inv;
     float q[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if ((t + i * TPR) * V < dim) {
+    for (int i = 0; i < NV; ++i) {
+      const int c0 = (t + i * TPR) * V - o;
+      if (c0 < dim) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          v[i][j] -= mu;
-          q[0] = fmaf(v[i][j], v[i][j], q[0]);
+        for (int j = 0; j < V; ++j) v[i][j] -= mu;
+        if (SHIFT && !ln_whole<V>(c0, dim)) {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (c0 + j < 0 || c0 + j >= dim) v[i][j] = 0.f;
         }
+#pragma unroll
+        for (int j = 0; j < V; ++j) q[0] = fmaf(v[i][j], v[i][j], q[0]);
       }
+    }
     ln_row_sum<TPR, 1>(q, red);
     const float rs = 1.0f / sqrtf(q[0] * inv + eps);
     if (t == 0) {
@@ -58,21 +93,32 @@ __global__ void __launch_bounds__(kBlock) ln_fwd_kernel(const TX* __restrict__ x
     TY* yr = y + row * dim;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (t + i * TPR) * V;
-      if (c < dim) {
-        float ww[V], bb[V], o[V];
-        ln_load<float, V>(w + c, ww);
-        ln_load<float, V>(b + c, bb);
+      const int c0 = (t + i * TPR) * V - o;
+      if (c0 < dim) {
+        float ww[V], bb[V], out[V];
+        if constexpr (SHIFT) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) o[j] = v[i][j] * rs * ww[j] + bb[j];
-        ln_store<TY, V>(yr + c, o);
+          for (int j = 0; j < V; j += 4) {
+            const float4 qw = *reinterpret_cast<const float4*>(table + ((i * V + j) / 4 * kBlock + tid) * 4);
+            const float4 qb = *reinterpret_cast<const float4*>(table + kTable + ((i * V + j) / 4 * kBlock + tid) * 4);
+            ww[j] = qw.x; ww[j + 1] = qw.y; ww[j + 2] = qw.z; ww[j + 3] = qw.w;
+            bb[j] = qb.x; bb[j + 1] = qb.y; bb[j + 2] = qb.z; bb[j + 3] = qb.w;
+          }
+        } else {
+          ln_load<float, V>(w + c0, ww);
+          ln_load<float, V>(b + c0, bb);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) out[j] = v[i][j] * rs * ww[j] + bb[j];
+        if constexpr (SHIFT) ln_store_part<TY, V>(yr, c0, dim, out);
+        else ln_store<TY, V>(yr + c0, out);
       }
     }
   }
 }
 
-// Rows wider than a block's registers: three sweeps over the row, the second
-// and third out of L2.
+// Rows wider than a block's registers, and operands that do not start on their
+// vector: three sweeps over the row, the second and third out of L2.
 template <typename TX, typename TY>
 __global__ void __launch_bounds__(kBlock) ln_fwd_wide_kernel(const TX* __restrict__ x, const float* __restrict__ w,
                                                              const float* __restrict__ b, TY* __restrict__ y,
@@ -103,35 +149,55 @@ __global__ void __launch_bounds__(kBlock) ln_fwd_wide_kernel(const TX* __restric
   }
 }
 
-template <typename TX, typename TY, int V>
-cudaError_t fwd_v(const TX* x, const float* w, const float* b, TY* y, float* mean, float* rstd, long rows, int dim,
-                  float eps, cudaStream_t s) {
-  const int per_row = dim <= 1024 ? kBlock / 32 : 1;
+constexpr int kMostBlocks = 152 * 8;
+int blocks_of(long rows, int per_row) {
   const long need = (rows + per_row - 1) / per_row;
-  const int blocks = (int)(need < 152 * 8 ? need : 152 * 8);
-#define JEPA_LN_FWD(NVE, TPR) \
-  ln_fwd_kernel<TX, TY, V, (NVE) / V, TPR><<<blocks, kBlock, 0, s>>>(x, w, b, y, mean, rstd, rows, dim, eps)
-  if (dim <= 256) JEPA_LN_FWD(8, 32);
-  else if (dim <= 512) JEPA_LN_FWD(16, 32);
-  else if (dim <= 1024) JEPA_LN_FWD(32, 32);
-  else if (dim <= 2048) JEPA_LN_FWD(8, 256);
-  else if (dim <= 4096) JEPA_LN_FWD(16, 256);
-  else if (dim <= 8192) JEPA_LN_FWD(32, 256);
-  else ln_fwd_wide_kernel<TX, TY><<<blocks, kBlock, 0, s>>>(x, w, b, y, mean, rstd, rows, dim, eps);
-#undef JEPA_LN_FWD
+  return (int)(need < kMostBlocks ? need : kMostBlocks);
+}
+
+template <typename TX, typename TY, int V, int NV, int TPR, bool SHIFT>
+cudaError_t launch_rows(const TX* x, const float* w, const float* b, TY* y, float* mean, float* rstd, long rows,
+                        int dim, float eps, cudaStream_t s) {
+  auto kern = ln_fwd_kernel<TX, TY, V, NV, TPR, SHIFT>;
+  constexpr size_t kSmem = SHIFT ? sizeof(float) * 2 * NV * V * kBlock : 0;
+  if constexpr (kSmem > 48 * 1024) {
+    static DeviceOnce setup;
+    const cudaError_t e = setup.run([&](int) {
+      return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  // a thread's rows have to be a multiple of V apart where its columns depend on them: 8 rows a block, or
+  // a full grid of one-row blocks (a multiple of 8), or one row a block
+  kern<<<blocks_of(rows, kBlock / TPR), kBlock, kSmem, s>>>(x, w, b, y, mean, rstd, rows, dim, eps);
   return cudaGetLastError();
 }
 
-template <typename TX, typename TY>
-cudaError_t fwd_t(const void* x, const float* w, const float* b, void* y, float* mean, float* rstd, long rows, int dim,
+template <typename TX, typename TY, int V, bool SHIFT>
+cudaError_t fwd_v(const TX* x, const float* w, const float* b, TY* y, float* mean, float* rstd, long rows, int dim,
                   float eps, cudaStream_t s) {
+  const int n = dim + (SHIFT ? V - 1 : 0);   // columns that the vectors cover
+  if (n <= 256) return launch_rows<TX, TY, V, 8 / V, 32, SHIFT>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+  if (n <= 512) return launch_rows<TX, TY, V, 16 / V, 32, SHIFT>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+  if (n <= 1024) return launch_rows<TX, TY, V, 32 / V, 32, SHIFT>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+  if (n <= 4096) return launch_rows<TX, TY, V, 16 / V, 256, SHIFT>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+  return launch_rows<TX, TY, V, 32 / V, 256, SHIFT>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+}
+
+constexpr int kLongest = 8192;   // columns that a block's registers hold
+
+template <typename TX, typename TY>
+cudaError_t fwd_t(const void* x_, const float* w, const float* b, void* y_, float* mean, float* rstd, long rows,
+                  int dim, float eps, cudaStream_t s) {
   constexpr int V = sizeof(TX) == 4 ? 4 : 8;
-  const bool vec = dim % V == 0 && ln_aligned(x, V * sizeof(TX)) && ln_aligned(y, V * sizeof(TY)) &&
-                   ln_aligned(w, 16) && ln_aligned(b, 16);
-  const TX* xx = static_cast<const TX*>(x);
-  TY* yy = static_cast<TY*>(y);
-  return vec ? fwd_v<TX, TY, V>(xx, w, b, yy, mean, rstd, rows, dim, eps, s)
-             : fwd_v<TX, TY, 1>(xx, w, b, yy, mean, rstd, rows, dim, eps, s);
+  const TX* x = static_cast<const TX*>(x_);
+  TY* y = static_cast<TY*>(y_);
+  const bool vec = ln_aligned(x, V * sizeof(TX)) && ln_aligned(y, V * sizeof(TY));
+  if (vec && dim % V == 0 && dim <= kLongest && ln_aligned(w, 16) && ln_aligned(b, 16))
+    return fwd_v<TX, TY, V, false>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+  if (vec && dim + V - 1 <= kLongest) return fwd_v<TX, TY, V, true>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+  ln_fwd_wide_kernel<TX, TY><<<blocks_of(rows, 1), kBlock, 0, s>>>(x, w, b, y, mean, rstd, rows, dim, eps);
+  return cudaGetLastError();
 }
 
 }  // namespace

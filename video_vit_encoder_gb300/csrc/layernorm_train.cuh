@@ -1,10 +1,15 @@
 // Row access shared by the layer norm's forward and backward kernels.
 //
 // A row of `dim` values is held in registers by TPR threads (one warp, or a
-// whole block), each owning NV vectors of V consecutive columns: vector i of
-// thread t starts at column (t + i * TPR) * V.  V is 4 or 8 where every row
-// of every 16-bit or 32-bit operand starts on a multiple of the vector (16
-// bytes of the widest operand), else 1; columns past dim read as zero.
+// whole block), each owning NV vectors of V consecutive columns (16 bytes of
+// the widest operand).  Where dim is a multiple of V, vector i of thread t
+// starts at column (t + i * TPR) * V.  Where it is not, rows start at any
+// element, so the vectors are laid on the aligned memory under the row: they
+// start at column (t + i * TPR) * V - o with o = (row * dim) mod V, and the
+// first and last one share their memory with the neighbouring rows.  A
+// thread's rows are a multiple of V apart, so o, and with it the columns a
+// thread owns, are the same for all its rows.  Operands that do not start on
+// their vector take V = 1.
 #pragma once
 #include "train.h"
 
@@ -84,6 +89,39 @@ __device__ __forceinline__ void ln_row_sum(float (&v)[N], float* red) {
       for (int i = 0; i < W; ++i) s += red[j * W + i];
       v[j] = s;
     }
+  }
+}
+
+// Shared memory is filled with the vector at p, of which the first `bytes`
+// bytes exist (the rest become zeros).
+template <int N>
+__device__ __forceinline__ void ln_copy_async(void* dst, const void* p, int bytes) {
+  static_assert(N == 8 || N == 16, "vector size");
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(p), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(p), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void ln_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ln_copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Whether a vector whose first column is c0 lies inside the row as a whole.
+template <int V>
+__device__ __forceinline__ bool ln_whole(int c0, int dim) {
+  return c0 >= 0 && c0 + V <= dim;
+}
+// Stores the part of a vector that lies inside the row.
+template <typename T, int V>
+__device__ __forceinline__ void ln_store_part(T* row, int c0, int dim, const float (&v)[V]) {
+  if (ln_whole<V>(c0, dim)) {
+    ln_store<T, V>(row + c0, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (c0 + j >= 0 && c0 + j < dim) row[c0 + j] = DT<T>::from(v[j]);
   }
 }
 

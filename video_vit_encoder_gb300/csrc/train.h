@@ -10,25 +10,10 @@ namespace jepa {
 // x_dtype / y_dtype: equal, or x in fp32 and y in a 16-bit type.
 cudaError_t layernorm_fwd(int x_dtype, int y_dtype, const void* x, const float* w, const float* b, void* y, float* mean,
                           float* rstd, long rows, int dim, float eps, cudaStream_t s);
-// Upper bound on the number of row strips of the backward pass, each of which
-// writes one partial sum of dw and db: two per SM of the 152.
-constexpr int kLnBwdStrips = 304;
 size_t layernorm_bwd_workspace(long rows, int dim);
 cudaError_t layernorm_bwd(int x_dtype, int y_dtype, const void* dy, const void* x, const float* w, const float* mean,
                           const float* rstd, const void* res, void* dx, float* dw, float* db, long rows, int dim,
                           float* ws, cudaStream_t s);
-
-// ----------------------------------------------------------------------------- general product on the CUDA cores (gemm_any.cu)
-// An operand: element (r, k) at p[r * rs + k * ks], one of rs and ks being 1.
-struct AnyMat {
-  const void* p;
-  int dtype;
-  long rs, ks;
-};
-// C[m, n] (+)= sum_k A(m, k) B(n, k) (+ bias[n]), fp32 accumulation; C in
-// c_dtype with row stride ldc.  accumulate: add to what C (fp32) holds.
-cudaError_t gemm_any(const AnyMat& A, const AnyMat& B, void* C, int c_dtype, long ldc, int M, int N, int K,
-                     const float* bias, bool accumulate, cudaStream_t s);
 
 // ----------------------------------------------------------------------------- operators (train_ops.cu)
 enum GateAct : int { ACT_SILU = 0, ACT_GELU = 1 };

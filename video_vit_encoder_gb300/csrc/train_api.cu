@@ -1,5 +1,7 @@
 // C entry points of the training operators: argument checks, then the kernels.
 // Everything a call can refuse is refused here, before anything is enqueued.
+#include <initializer_list>
+
 #include "api_internal.h"
 #include "train.h"
 
@@ -35,6 +37,14 @@ jepa_status check_ws(const void* ws, size_t bytes, size_t need) {
   if (bytes < need) return api_fail(JEPA_ERR_ARG, "workspace holds %zu bytes, %zu needed", bytes, need);
   return JEPA_OK;
 }
+
+// Matrices of products start on 16 bytes, as TMA wants.
+bool matrix_misaligned(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (misaligned(p, 16)) return true;
+  return false;
+}
+jepa_status bad_matrix() { return api_fail(JEPA_ERR_ARG, "matrices must be 16-byte aligned"); }
 
 bool bad_rows(int m) { return m < 0 || m > kMaxSize; }
 bool bad_width(int n) { return n < 1 || n > kMaxSize; }
@@ -121,8 +131,8 @@ jepa_status jepa_linear_ce_fwd(const void* x, const void* W, const float* bias, 
   ARG_TRY(check_ce(M, D, V, dtype, smoothing));
   if (M == 0) return JEPA_OK;
   if (!x || !W || !labels || !lse) return api_fail(JEPA_ERR_ARG, "NULL buffer");
-  const size_t e = elem_size(dtype);
-  if (misaligned(x, e) || misaligned(W, e) || misaligned(bias, 4) || misaligned(labels, 8) || misaligned(loss, 4) ||
+  if (matrix_misaligned({x, W})) return bad_matrix();
+  if (misaligned(bias, 4) || misaligned(labels, 8) || misaligned(loss, 4) ||
       misaligned(lse, 4))
     return api_fail(JEPA_ERR_ARG, "a buffer is not aligned to its element");
   ARG_TRY(check_ws(workspace, workspace_bytes, linear_ce_workspace(M, D, V, dtype, false)));
@@ -138,9 +148,8 @@ jepa_status jepa_linear_ce_bwd(const void* x, const void* W, const float* bias, 
   ARG_TRY(check_ce(M, D, V, dtype, smoothing));
   if (M > 0 && (!x || !W || !labels || !lse || !dloss)) return api_fail(JEPA_ERR_ARG, "NULL buffer");
   if (!dx && !dW && !dbias) return api_fail(JEPA_ERR_ARG, "no gradient asked for (dx, dW and dbias are NULL)");
-  const size_t e = elem_size(dtype);
-  if (misaligned(x, e) || misaligned(W, e) || misaligned(bias, 4) || misaligned(labels, 8) || misaligned(lse, 4) ||
-      misaligned(dloss, 4) || misaligned(dx, e) || misaligned(dW, e) || misaligned(dbias, 4))
+  if (matrix_misaligned({x, W, dx, dW})) return bad_matrix();
+  if (misaligned(bias, 4) || misaligned(labels, 8) || misaligned(lse, 4) || misaligned(dloss, 4) || misaligned(dbias, 4))
     return api_fail(JEPA_ERR_ARG, "a buffer is not aligned to its element");
   if (M > 0) ARG_TRY(check_ws(workspace, workspace_bytes, linear_ce_workspace(M, D, V, dtype, true)));
   CeArgs a{x, W, bias, labels, M, D, V, dtype, (long)ignore_index, smoothing, nullptr, 0};
@@ -160,9 +169,8 @@ jepa_status jepa_gated_ffn_fwd(const void* x, const void* Wg, const void* Wu, co
   ARG_TRY(check_ffn(M, D, F, dtype, act));
   if (M == 0) return JEPA_OK;
   if (!x || !Wg || !Wu || !h) return api_fail(JEPA_ERR_ARG, "NULL buffer");
-  const size_t e = elem_size(dtype);
-  if (misaligned(x, e) || misaligned(Wg, e) || misaligned(Wu, e) || misaligned(h, e) || misaligned(bg, 4) ||
-      misaligned(bu, 4))
+  if (matrix_misaligned({x, Wg, Wu, h})) return bad_matrix();
+  if (misaligned(bg, 4) || misaligned(bu, 4))
     return api_fail(JEPA_ERR_ARG, "a buffer is not aligned to its element");
   ARG_TRY(check_ws(workspace, workspace_bytes, gated_ffn_workspace(M, D, F, dtype, false)));
   FfnArgs a{x, Wg, Wu, bg, bu, M, D, F, dtype, act, nullptr, 0};
@@ -176,10 +184,8 @@ jepa_status jepa_gated_ffn_bwd(const void* dh, const void* x, const void* Wg, co
   ARG_TRY(check_ffn(M, D, F, dtype, act));
   if (M > 0 && (!dh || !x || !Wg || !Wu)) return api_fail(JEPA_ERR_ARG, "NULL buffer");
   if (!dx && !dWg && !dWu && !dbg && !dbu) return api_fail(JEPA_ERR_ARG, "no gradient asked for (every output is NULL)");
-  const size_t e = elem_size(dtype);
-  if (misaligned(dh, e) || misaligned(x, e) || misaligned(Wg, e) || misaligned(Wu, e) || misaligned(bg, 4) ||
-      misaligned(bu, 4) || misaligned(dx, e) || misaligned(dWg, e) || misaligned(dWu, e) || misaligned(dbg, 4) ||
-      misaligned(dbu, 4))
+  if (matrix_misaligned({dh, x, Wg, Wu, dx, dWg, dWu})) return bad_matrix();
+  if (misaligned(bg, 4) || misaligned(bu, 4) || misaligned(dbg, 4) || misaligned(dbu, 4))
     return api_fail(JEPA_ERR_ARG, "a buffer is not aligned to its element");
   if (M > 0) ARG_TRY(check_ws(workspace, workspace_bytes, gated_ffn_workspace(M, D, F, dtype, true)));
   FfnArgs a{x, Wg, Wu, bg, bu, M, D, F, dtype, act, nullptr, 0};
@@ -200,10 +206,8 @@ jepa_status jepa_linear_bwd(const void* dout, const void* A, const void* W, void
   if (bad_dtype(dtype)) return api_fail(JEPA_ERR_ARG, "dtype %d", dtype);
   if (!dA && !dW && !dbias) return api_fail(JEPA_ERR_ARG, "no gradient asked for (dA, dW and dbias are NULL)");
   if (M > 0 && (!dout || (dA && !W) || (dW && !A))) return api_fail(JEPA_ERR_ARG, "NULL buffer");
-  const size_t e = elem_size(dtype);
-  if (misaligned(dout, e) || misaligned(A, e) || misaligned(W, e) || misaligned(dA, e) || misaligned(dW, e) ||
-      misaligned(dbias, 4))
-    return api_fail(JEPA_ERR_ARG, "a buffer is not aligned to its element");
+  if (matrix_misaligned({dout, A, W, dA, dW})) return bad_matrix();
+  if (misaligned(dbias, 4)) return api_fail(JEPA_ERR_ARG, "a buffer is not aligned to its element");
   if (M > 0) ARG_TRY(check_ws(workspace, workspace_bytes, linear_bwd_workspace(M, N, K, dtype)));
   int* st = nullptr;
   int sms = 0;

@@ -1,165 +1,448 @@
-// The training operators on the CUDA cores: the path of fp32, and of 16-bit
-// operands whose rows do not start on 16 bytes.
+// The training operators: which products they launch, in which pieces, and the
+// small kernels between them.
 //
-// Each works over pieces of its wide dimension (the vocabulary, the hidden
-// width): the piece's products go to an fp32 workspace, a row-wise kernel
-// turns them into what the piece contributes, and further products reduce
-// that.  The workspace holds one piece, never the whole [rows, width] matrix.
-// The products (gemm_any.cu) take nearly all the time, so the kernels here
-// are plain single passes.
-#include "train_tc.h"
+// fp32 matrices are split into three bf16 planes first; 16-bit ones whose rows
+// are not multiples of 16 bytes are copied to rows that are (TMA addresses
+// nothing else).  Everything else reads the caller's matrices in place.
+#include "gemm_train.cuh"
 
 namespace jepa {
 
+namespace tg {
+cudaError_t gemm_bf16(bool amn, bool bmn, int epi, const Params& p, int num_sms, cudaStream_t s);
+cudaError_t gemm_f16(bool amn, bool bmn, int epi, const Params& p, int num_sms, cudaStream_t s);
+cudaError_t gemm_f32(bool amn, bool bmn, int epi, const Params& p, int num_sms, cudaStream_t s);
+}  // namespace tg
+
 namespace {
 
+using tg::Params;
+
 constexpr int kBlock = 256;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kPairs = 76;      // CTA pairs of 152 SMs: the plans (and workspaces) assume it, the launch asks the device
+constexpr int kWhole = 1 << 30; // all of K in tensor memory
 
-size_t larger(size_t a, size_t b) { return a > b ? a : b; }
+#define JEPA_TRY_CUDA(expr)                 \
+  do {                                      \
+    const cudaError_t e_ = (expr);          \
+    if (e_ != cudaSuccess) return e_;       \
+  } while (0)
+
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
-size_t elem(int dtype) { return dtype == DTYPE_F32 ? 4 : 2; }
+int ceil_div(long a, long b) { return (int)((a + b - 1) / b); }
+long round_up(long a, long b) { return (a + b - 1) / b * b; }
 unsigned blocks_for(long n, int block) { return (unsigned)((n + block - 1) / block); }
+size_t elem(int dtype) { return dtype == DTYPE_F32 ? 4 : 2; }
+bool split(int dtype) { return dtype == DTYPE_F32; }
 
-AnyMat rows_k(const void* p, int dtype, long ld) { return AnyMat{p, dtype, ld, 1}; }  // p is [r, k]
-AnyMat k_rows(const void* p, int dtype, long ld) { return AnyMat{p, dtype, 1, ld}; }  // p is [k, r]
+// A workspace cut into 256-byte aligned buffers; over a null base, its size.
+struct Carver {
+  uint8_t* p;
+  size_t used = 0;
+  template <typename U>
+  U* take(size_t bytes) {
+    U* r = reinterpret_cast<U*>(p + used);
+    used += align256(bytes);
+    return r;
+  }
+};
 
-// Columns of the wide dimension (of `total`) per piece: a multiple of 128 of
-// which `bufs` fp32 arrays of M rows stay within 64 MB (they then live in L2
-// between the kernels that write and read them), but at least 1024 columns,
-// so that each product still fills the machine.
-int piece_cols(int M, int total, int bufs) {
-  const size_t per = sizeof(float) * (size_t)bufs * (M > 0 ? M : 1);
-  size_t c = ((size_t)64 << 20) / per / 128 * 128;
-  if (c < 1024) c = 1024;
-  const size_t all = ((size_t)total + 127) / 128 * 128;
-  return (int)(c < all ? c : all);
+// ----------------------------------------------------------------------------- operands
+// A 16-bit matrix that TMA can address: rows x cols, row stride ld, and for
+// fp32 three planes of it, plane_rows apart (0: one plane).
+struct Mat {
+  const uint8_t* p = nullptr;
+  long rows = 0, cols = 0, ld = 0, plane_rows = 0;
+  bool own = false;   // a copy in the workspace
+};
+// Where the operator's matrix is or will be: in place, or in the workspace.
+Mat operand(int dtype, const void* src, long rows, long cols, Carver& cv) {
+  Mat m;
+  m.rows = rows;
+  m.cols = cols;
+  m.ld = round_up(cols, 8);
+  m.own = split(dtype) || cols % 8 != 0;
+  if (split(dtype)) m.plane_rows = round_up(rows, 64);
+  m.p = m.own ? cv.take<uint8_t>(2 * (size_t)m.ld * (split(dtype) ? 3 * m.plane_rows : rows))
+              : static_cast<const uint8_t*>(src);
+  return m;
+}
+// Rows from r0 on.
+Mat rows_from(const Mat& m, long r0, long rows) {
+  Mat t = m;
+  t.p += 2 * (size_t)r0 * m.ld;
+  t.rows = rows;
+  return t;
+}
+
+// The extent of the map's row dimension: a single plane ends at its rows (TMA
+// reads zeros past them); planes run on, and a row past a plane's end is the
+// zero padding or the next plane's, whose products are dropped or meet zeros.
+long map_rows(const Mat& m, long r0) { return m.plane_rows != 0 ? 3 * m.plane_rows - r0 : m.rows; }
+// m is [rows, k]: boxes of 64 k x 128 rows.  r0: how far m starts into its plane.
+cudaError_t map_k(CUtensorMap* t, const Mat& m, long r0 = 0) {
+  return make_tmap_2d(t, m.p, 2, m.cols, map_rows(m, r0), m.ld * 2, tg::kBK, tg::kBM);
+}
+// m is [k, rows]: boxes of 64 rows x 64 k.
+cudaError_t map_mn(CUtensorMap* t, const Mat& m, long r0 = 0) {
+  return make_tmap_2d(t, m.p, 2, m.cols, map_rows(m, r0), m.ld * 2, 64, tg::kBK);
+}
+// Outputs: 16-bit in blocks of 64 columns x 32 rows, fp32 of 32 x 32.
+cudaError_t map_out16(CUtensorMap* t, void* p, long rows, long cols, long ld) {
+  return make_tmap_2d(t, p, 2, cols, rows, ld * 2, 64, 32);
+}
+cudaError_t map_out32(CUtensorMap* t, void* p, long rows, long cols, long ld) {
+  return make_tmap_2d(t, p, 4, cols, rows, ld * 4, 32, 32);
+}
+
+// Rows of src to rows of 16 bytes.  8 columns a thread.
+__global__ void __launch_bounds__(kBlock) pad_kernel(const uint16_t* __restrict__ src, long rows, int cols,
+                                                     uint16_t* __restrict__ dst, int ld8) {
+  const long i = (long)blockIdx.x * kBlock + threadIdx.x;
+  const long r = i / ld8;
+  if (r >= rows) return;
+  const int c = (int)(i - r * ld8) * 8;
+  uint16_t h[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) h[j] = c + j < cols ? __ldg(src + r * cols + c + j) : (uint16_t)0;
+  uint4 q;
+  memcpy(&q, h, 16);
+  reinterpret_cast<uint4*>(dst)[i] = q;
+}
+// fp32 rows to three bf16 planes x = x0 + x1 + x2, each the rounding of what
+// the ones before leave.  A finite value that rounds to infinity is truncated
+// instead; one that is not finite has no further planes.  Padding is zero.
+// VEC: rows start on 16 bytes.  8 columns a thread.
+template <bool VEC>
+__global__ void __launch_bounds__(kBlock) split_kernel(const float* __restrict__ src, long rows, int cols,
+                                                       uint16_t* __restrict__ dst, int ld8, long plane_rows) {
+  const long i = (long)blockIdx.x * kBlock + threadIdx.x;
+  const long r = i / ld8;
+  if (r >= plane_rows) return;
+  const int c = (int)(i - r * ld8) * 8;
+  float x[8];
+  const float* p = src + r * cols + c;
+#pragma unroll
+  for (int j = 0; j < 8; j += 4) {
+    if (VEC) {   // cols is a multiple of 4
+      const float4 q = r < rows && c + j < cols ? __ldg(reinterpret_cast<const float4*>(p + j)) : make_float4(0, 0, 0, 0);
+      x[j] = q.x; x[j + 1] = q.y; x[j + 2] = q.z; x[j + 3] = q.w;
+    } else {
+#pragma unroll
+      for (int k = j; k < j + 4; ++k) x[k] = r < rows && c + k < cols ? __ldg(p + k) : 0.f;
+    }
+  }
+  __nv_bfloat16 h[3][8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    h[0][j] = __float2bfloat16_rn(x[j]);
+    if (fabsf(x[j]) > 3.3895e38f) h[0][j] = __float2bfloat16_rz(x[j]);
+    float rem = x[j] - __bfloat162float(h[0][j]);
+    if (!(fabsf(x[j]) < INFINITY)) rem = 0.f;
+    h[1][j] = __float2bfloat16_rn(rem);
+    h[2][j] = __float2bfloat16_rn(rem - __bfloat162float(h[1][j]));
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    uint4 q;
+    memcpy(&q, h[k], 16);
+    reinterpret_cast<uint4*>(dst)[k * plane_rows * ld8 + i] = q;
+  }
+}
+// Fills an operand that lives in the workspace.
+cudaError_t fill(int dtype, const void* src, const Mat& m, cudaStream_t s) {
+  if (!m.own) return cudaSuccess;
+  const int ld8 = (int)(m.ld / 8);
+  uint16_t* dst = reinterpret_cast<uint16_t*>(const_cast<uint8_t*>(m.p));
+  if (!split(dtype)) {
+    pad_kernel<<<blocks_for(m.rows * ld8, kBlock), kBlock, 0, s>>>((const uint16_t*)src, m.rows, (int)m.cols, dst, ld8);
+  } else {
+    const unsigned b = blocks_for(m.plane_rows * ld8, kBlock);
+    if (m.cols % 4 == 0)
+      split_kernel<true><<<b, kBlock, 0, s>>>((const float*)src, m.rows, (int)m.cols, dst, ld8, m.plane_rows);
+    else
+      split_kernel<false><<<b, kBlock, 0, s>>>((const float*)src, m.rows, (int)m.cols, dst, ld8, m.plane_rows);
+  }
+  return cudaGetLastError();
+}
+
+// ----------------------------------------------------------------------------- products
+Params base_params(long M, long N, int cols_per_tile, int* status) {
+  Params p{};
+  p.M = (int)M;
+  p.N = (int)N;
+  p.num_m = ceil_div(M, 2 * tg::kBM);
+  p.num_n = ceil_div(N, cols_per_tile);
+  p.run = p.nseg = p.nz = p.splits = 1;
+  p.kb_chunk = kWhole;
+  p.status = status;
+  return p;
+}
+void set_k(Params& p, long k_per_seg, int nseg, int splits) {
+  p.kb_seg = ceil_div(k_per_seg, tg::kBK);
+  p.nseg = nseg;
+  const int total = p.kb_seg * nseg;
+  p.kb_split = ceil_div(total, splits);
+  p.splits = ceil_div(total, p.kb_split);
+}
+
+// K splits of a product of nz outputs M x N over kb blocks, from the time of
+// the schedule: rounds of the 76 pairs, each a unit's blocks (0.27 us a block,
+// 6 times that for planes) plus about 1.6 us to fill and drain, and, when
+// split, writing the fp32 slabs and adding them (5 TB/s, and 2 us to launch).
+int plan_splits(int dtype, long M, long N, int nz, int kb) {
+  const long tiles = (long)ceil_div(M, 256) * ceil_div(N, 256) * nz;
+  const double block = split(dtype) ? 1.6 : 0.27;
+  const int least = split(dtype) ? 1 : 4;
+  int best = 1;
+  double best_t = 1e300;
+  for (int s = 1; s <= 16 && (s == 1 || kb / s >= least); ++s) {
+    const int per = ceil_div(kb, s);
+    const int real = ceil_div(kb, per);
+    double t = (double)ceil_div(tiles * real, kPairs) * (per * block + 1.6);
+    if (real > 1) t += 2.0 + 2.0 * real * nz * (double)M * N * 4.0 / 5e6;
+    if (t < best_t) {
+      best_t = t;
+      best = real;
+    }
+  }
+  return best;
+}
+
+// K blocks between the register sums of a 16-bit product with fp32 results.
+// 8 (512 k) cost next to nothing where a tile's products hide the sums (cross
+// entropy backward, 4096 x 1024 x 32768: 0.54 ms, in one go 0.53, with 4
+// blocks 0.62, with 2 blocks 0.65).  Column sums (dbias) over few classes
+// cancel, so that the truncation shows: at 1789 x 448 x 12 they are 4.9e-6 off
+// with 8 blocks.  Such products have few tiles, and few blocks are affordable.
+int chunk_blocks(const Params& p, bool column_sums) {
+  const long tiles = (long)p.num_m * p.num_n;
+  return !column_sums || tiles > 4 * kPairs ? 8 : (tiles > kPairs ? 4 : 2);
+}
+
+cudaError_t gemm(int dtype, bool amn, bool bmn, int epi, const Params& p, int num_sms, cudaStream_t s) {
+  if (dtype == DTYPE_F32) return tg::gemm_f32(amn, bmn, epi, p, num_sms, s);
+  return dtype == DTYPE_BF16 ? tg::gemm_bf16(amn, bmn, epi, p, num_sms, s) : tg::gemm_f16(amn, bmn, epi, p, num_sms, s);
+}
+
+// How a reducing product's C [M, N] of the operator's type comes about:
+// written by the product, or through fp32 slabs, one per split.
+struct Reduce {
+  int splits = 1;
+  bool direct = false;
+  long np = 0, mp = 0;    // a slab's columns and rows
+  float* slab = nullptr;
+};
+Reduce plan_reduce(int dtype, long M, long N, int nz, int kb, bool add, Carver& cv) {
+  Reduce r;
+  r.splits = plan_splits(dtype, M, N, nz, kb);
+  // fp32 adds pieces in place; 16-bit pieces add up in fp32
+  r.direct = r.splits == 1 && (split(dtype) ? N % 4 == 0 : N % 8 == 0 && !add);
+  r.np = round_up(N, 8);
+  r.mp = round_up(M, 256);
+  if (!r.direct) r.slab = cv.take<float>((size_t)r.splits * r.mp * r.np * 4);
+  return r;
+}
+
+// out[r, c] = scale * sum over the slabs, in slab order.  VEC: N is the slabs'
+// row length, 8 values a thread; else one.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kBlock) slab_sum_kernel(const float* __restrict__ slab, long stride, int n_slabs,
+                                                          T* __restrict__ out, long rows, int N, int np,
+                                                          const float* __restrict__ scale) {
+  const long i = (long)blockIdx.x * kBlock + threadIdx.x;
+  const float sc = scale != nullptr ? __ldg(scale) : 1.f;
+  if constexpr (VEC) {
+    if (i * 8 >= rows * N) return;
+    float v[8] = {};
+    const float4* a = reinterpret_cast<const float4*>(slab) + 2 * i;
+#pragma unroll 4
+    for (int k = 0; k < n_slabs; ++k, a += stride / 4) {
+      const float4 x = __ldg(a), y = __ldg(a + 1);
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w; v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= sc;
+    if constexpr (sizeof(T) == 2) {
+      reinterpret_cast<uint4*>(out)[i] =
+          make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+    } else {
+      reinterpret_cast<float4*>(out)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(out)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+    const long r = i / N;
+    if (r >= rows) return;
+    const float* a = slab + r * np + (i - r * N);
+    float v = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < n_slabs; ++k, a += stride) v += __ldg(a);
+    out[i] = DT<T>::from(v * sc);
+  }
+}
+template <typename T>
+cudaError_t slab_sum_t(const Reduce& rd, int n_slabs, long slab_rows, void* out, long rows, long N, const float* scale,
+                       cudaStream_t s) {
+  const long stride = slab_rows * rd.np;
+  if (N % 8 == 0)
+    slab_sum_kernel<T, true><<<blocks_for(rows * N / 8, kBlock), kBlock, 0, s>>>(rd.slab, stride, n_slabs, (T*)out, rows,
+                                                                                 (int)N, (int)rd.np, scale);
+  else
+    slab_sum_kernel<T, false><<<blocks_for(rows * N, kBlock), kBlock, 0, s>>>(rd.slab, stride, n_slabs, (T*)out, rows,
+                                                                              (int)N, (int)rd.np, scale);
+  return cudaGetLastError();
+}
+cudaError_t slab_sum(int dtype, const Reduce& rd, int n_slabs, long slab_rows, void* out, long rows, long N,
+                     const float* scale, cudaStream_t s) {
+  if (dtype == DTYPE_F32) return slab_sum_t<float>(rd, n_slabs, slab_rows, out, rows, N, scale, s);
+  if (dtype == DTYPE_F16) return slab_sum_t<__half>(rd, n_slabs, slab_rows, out, rows, N, scale, s);
+  return slab_sum_t<__nv_bfloat16>(rd, n_slabs, slab_rows, out, rows, N, scale, s);
+}
+
+// Sets p's output z for a reducing product of `rows` rows and returns its
+// epilogue; with slabs, slab_sum is still to come.
+cudaError_t reduce_output(int dtype, const Reduce& rd, Params& p, int z, void* out, float* slab, bool add, int* epi) {
+  const long rows = p.M, N = p.N;
+  *epi = add ? tg::F32_ADD : tg::F32;
+  if (rd.direct) {
+    if (split(dtype)) return map_out32(&p.c[z], out, rows, N, N);
+    *epi = tg::STORE;
+    return map_out16(&p.c[z], out, rows, N, N);
+  }
+  p.slab_rows = (int)round_up(rows, 256);
+  return map_out32(&p.c[z], slab, (long)p.slab_rows * p.splits, rd.np, rd.np);
 }
 
 // ----------------------------------------------------------------------------- column sums
-// out[c] = sum over the rows of a[r, c]: 32 columns a block, 8 threads a
-// column, each over every eighth row, joined in a fixed order.
-template <typename T>
-__global__ void __launch_bounds__(kBlock) col_sum_kernel(const T* __restrict__ a, long ld, int M, int n,
-                                                         float* __restrict__ out) {
-  __shared__ float sm[8][33];
+// out[c] = scale * sum over r of a[r, c], for two matrices at once (grid.y):
+// 32 columns a block, 32 threads a column, each over every 32nd row, joined in
+// a fixed order.
+struct ColSums {
+  const float* a[2];
+  float* out[2];
+};
+__global__ void __launch_bounds__(1024) part_sum_kernel(ColSums cs, long ld, int rows, int n,
+                                                        const float* __restrict__ scale) {
+  __shared__ float sm[32][33];
+  const float* a = cs.a[blockIdx.y];
+  float* out = cs.out[blockIdx.y];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < n)
-    for (int r = g; r < M; r += 8) s += DT<T>::to(a[(long)r * ld + c]);
+  if (c < n) {
+#pragma unroll 4
+    for (int r = g; r < rows; r += 32) s += __ldg(a + (long)r * ld + c);
+  }
   sm[g][lane] = s;
   __syncthreads();
-  if (g == 0 && c < n) {
-    for (int k = 1; k < 8; ++k) s += sm[k][lane];
-    out[c] = s;
-  }
+  s = sm[lane][g];   // warp g joins column g
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int cc = blockIdx.x * 32 + g;
+  if (lane == 0 && cc < n) out[cc] = scale != nullptr ? s * __ldg(scale) : s;
 }
-cudaError_t col_sum(const void* a, int dtype, long ld, int M, int n, float* out, cudaStream_t s) {
-  const unsigned b = blocks_for(n, 32);
-  if (dtype == DTYPE_F32) col_sum_kernel<float><<<b, kBlock, 0, s>>>((const float*)a, ld, M, n, out);
-  else if (dtype == DTYPE_F16) col_sum_kernel<__half><<<b, kBlock, 0, s>>>((const __half*)a, ld, M, n, out);
-  else col_sum_kernel<__nv_bfloat16><<<b, kBlock, 0, s>>>((const __nv_bfloat16*)a, ld, M, n, out);
+cudaError_t part_sum(const ColSums& cs, int count, long ld, int rows, int n, const float* scale, cudaStream_t s) {
+  part_sum_kernel<<<dim3(blocks_for(n, 32), count), 1024, 0, s>>>(cs, ld, rows, n, scale);
   return cudaGetLastError();
 }
 
-template <typename T>
-__global__ void cast_kernel(const float* __restrict__ a, T* __restrict__ out, long n) {
-  const long i = (long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i < n) out[i] = DT<T>::from(a[i]);
+// Column sums of an [M, N] matrix: block (256 columns, strip of rows), 8
+// consecutive columns a thread (VEC: rows of 16 bytes) or 8 columns 32 apart,
+// 8 rows at a time.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kBlock) col_strip_kernel(const T* __restrict__ a, int M, int N, int rows_per,
+                                                           float* __restrict__ part) {
+  __shared__ float sm[8][256 + 8];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int c = blockIdx.x * 256 + (VEC ? lane * 8 : lane);
+  const int r0 = blockIdx.y * rows_per, r1 = min(M, r0 + rows_per);
+  float v[8] = {};
+#pragma unroll 4
+  for (int r = r0 + g; r < r1; r += 8) {
+    const T* p = a + (size_t)r * N + c;
+    if constexpr (VEC) {
+      constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+      for (int j = 0; j < 8; j += kPer) {
+        if (c + j < N) {
+          const uint4 q = __ldg(reinterpret_cast<const uint4*>(p + j));
+          T h[kPer];
+          memcpy(h, &q, 16);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) v[j + i] += DT<T>::to(h[i]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + 32 * j < N) v[j] += DT<T>::to(p[32 * j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sm[g][VEC ? lane * 8 + j : lane + 32 * j] = v[j];
+  __syncthreads();
+  const int cc = blockIdx.x * 256 + threadIdx.x;
+  if (cc < N) {
+    float s = 0.f;
+    for (int k = 0; k < 8; ++k) s += sm[k][threadIdx.x];
+    part[(size_t)blockIdx.y * N + cc] = s;
+  }
 }
-cudaError_t cast_to(const float* a, int dtype, void* out, long n, cudaStream_t s) {
-  if (n == 0) return cudaSuccess;
-  if (dtype == DTYPE_F16) cast_kernel<__half><<<blocks_for(n, kBlock), kBlock, 0, s>>>(a, (__half*)out, n);
-  else cast_kernel<__nv_bfloat16><<<blocks_for(n, kBlock), kBlock, 0, s>>>(a, (__nv_bfloat16*)out, n);
-  return cudaGetLastError();
+int col_strips(int M, int N) {
+  const int want = ceil_div(4 * 152, ceil_div(N, 256)), most = ceil_div(M, 64);
+  return want < most ? want : most;
+}
+template <typename T>
+cudaError_t col_sum_t(const void* a, int M, int N, float* part, float* out, cudaStream_t s) {
+  const int strips = col_strips(M, N), per = ceil_div(M, strips);
+  float* to = strips == 1 ? out : part;
+  const dim3 g(ceil_div(N, 256), strips);
+  if ((N * sizeof(T)) % 16 == 0) col_strip_kernel<T, true><<<g, kBlock, 0, s>>>((const T*)a, M, N, per, to);
+  else col_strip_kernel<T, false><<<g, kBlock, 0, s>>>((const T*)a, M, N, per, to);
+  JEPA_TRY_CUDA(cudaGetLastError());
+  if (strips == 1) return cudaSuccess;
+  return part_sum(ColSums{{part, nullptr}, {out, nullptr}}, 1, N, strips, N, nullptr, s);
+}
+
+cudaError_t zero(void* p, size_t bytes, cudaStream_t s) {
+  return p == nullptr || bytes == 0 ? cudaSuccess : cudaMemsetAsync(p, 0, bytes, s);
 }
 
 // ----------------------------------------------------------------------------- softmax cross entropy
-// Label of a row: -1 for a row that takes no part (ignored, or bad).
-__device__ __forceinline__ long row_label(long label, long ignore_index, int V) {
-  return label == ignore_index || label < 0 || label >= V ? -1 : label;
-}
-
-// Running statistics of a row over the pieces seen so far: the max m of its
-// logits, sum of exp(z - m), sum of z, and the label's logit.
-struct CeState {
-  float m, s, sum, zy;
+// Joins the (max, sum of 2^(z - max)) of a row's parts; 32 rows a block, the
+// block's 8 warps take every eighth part.
+struct Ms {
+  float m, s, sum;
 };
-
-// Joins (m, s) with (m2, s2); a side that has seen nothing but -inf has s = 0.
-__device__ __forceinline__ void ce_join(float& m, float& s, float m2, float s2) {
-  const float mm = fmaxf(m, m2);
-  // exp(-inf - -inf) would be NaN: nothing has been summed on that side
-  const float f1 = m == -INFINITY ? 0.f : exp2f((m - mm) * kLog2e);
-  const float f2 = m2 == -INFINITY ? 0.f : exp2f((m2 - mm) * kLog2e);
-  s = (m == -INFINITY ? 0.f : s * f1) + (m2 == -INFINITY ? 0.f : s2 * f2);
-  m = mm;
+__device__ __forceinline__ void ms_join(Ms& a, float m, float s, float sum) {
+  const float mm = fmaxf(a.m, m);
+  const float ref = mm == -INFINITY ? 0.f : mm;   // a side that has seen only -inf has 2^-inf = 0
+  a.s = a.s * tg::ex2(a.m - ref) + s * tg::ex2(m - ref);
+  a.m = mm;
+  a.sum += sum;
 }
-
-// One block a row: adds the piece's logits z[row, 0:n) (columns v0..) to the state.
-__global__ void __launch_bounds__(kBlock) ce_piece_kernel(const float* __restrict__ z, long ld, int n, int v0, int V,
-                                                          const int64_t* __restrict__ labels, long ignore_index,
-                                                          CeState* __restrict__ state, int first) {
-  __shared__ float sm[3][kBlock / 32];
-  const long row = blockIdx.x;
-  const float* zr = z + row * ld;
-  float m = -INFINITY, s = 0.f, sum = 0.f;
-  bool nan = false;
-  for (int c = threadIdx.x; c < n; c += kBlock) {
-    const float v = zr[c];
-    nan |= v != v;
-    sum += v;
-    m = fmaxf(m, v);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) sm[0][warp] = m;
-  __syncthreads();
-  for (int k = 0; k < kBlock / 32; ++k) m = fmaxf(m, sm[0][k]);
-  if (m != -INFINITY)
-    for (int c = threadIdx.x; c < n; c += kBlock) s += exp2f((zr[c] - m) * kLog2e);
-  if (nan) s = NAN;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  }
-  if (lane == 0) {
-    sm[1][warp] = s;
-    sm[2][warp] = sum;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    s = sum = 0.f;
-    for (int k = 0; k < kBlock / 32; ++k) {
-      s += sm[1][k];
-      sum += sm[2][k];
+__global__ void __launch_bounds__(kBlock) ce_join_kernel(const float2* __restrict__ ms, const float* __restrict__ sums,
+                                                         const float* __restrict__ zy, int parts, int M, int V,
+                                                         const int64_t* __restrict__ labels, long ignore_index,
+                                                         float smoothing, float* __restrict__ loss,
+                                                         float* __restrict__ lse_out, int* status) {
+  __shared__ Ms sm[8][33];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int row = blockIdx.x * 32 + lane;
+  Ms a{-INFINITY, 0.f, 0.f};
+  if (row < M) {
+#pragma unroll 4
+    for (int k = g; k < parts; k += 8) {
+      const float2 q = __ldg(ms + (size_t)k * M + row);
+      ms_join(a, q.x, q.y, sums != nullptr ? __ldg(sums + (size_t)k * M + row) : 0.f);
     }
-    if (s != s) m = NAN;
-    CeState st = first ? CeState{-INFINITY, 0.f, 0.f, 0.f} : state[row];
-    if (m != m || st.m != st.m) {
-      st.m = NAN;
-    } else {
-      ce_join(st.m, st.s, m, s);
-    }
-    st.sum += sum;
-    const long y = row_label(labels[row], ignore_index, V);
-    if (y >= v0 && y < (long)v0 + n) st.zy = zr[y - v0];
-    state[row] = st;
   }
-}
-
-// loss = lse - (1 - e) z_y - e mean(z); 0 for an ignored row, NaN (and the
-// status bit) for a label outside [0, V).
-__global__ void ce_finish_kernel(const CeState* __restrict__ state, const int64_t* __restrict__ labels, int M, int V,
-                                 long ignore_index, float smoothing, float* __restrict__ loss,
-                                 float* __restrict__ lse_out, int* status) {
-  const int row = blockIdx.x * blockDim.x + threadIdx.x;
-  if (row >= M) return;
-  const CeState st = state[row];
-  const float lse = st.m == -INFINITY ? -INFINITY : st.m + logf(st.s);
+  sm[g][lane] = a;
+  __syncthreads();
+  if (g != 0 || row >= M) return;
+  for (int k = 1; k < 8; ++k) ms_join(a, sm[k][lane].m, sm[k][lane].s, sm[k][lane].sum);
+  // lse = ln(2^m s)
+  const float lse = (a.m + log2f(a.s)) * 0.69314718055994531f;
   const long label = labels[row];
   float l;
   if (label == ignore_index) {
@@ -168,250 +451,419 @@ __global__ void ce_finish_kernel(const CeState* __restrict__ state, const int64_
     l = NAN;
     atomicOr(status, DEV_BAD_INDEX);
   } else {
-    l = lse - (1.0f - smoothing) * st.zy;
-    if (smoothing > 0.f) l -= smoothing * (st.sum / (float)V);
+    l = lse - (1.0f - smoothing) * zy[row];
+    if (smoothing > 0.f) l -= smoothing * (a.sum / (float)V);
   }
   if (loss != nullptr) loss[row] = l;
-  if (lse_out != nullptr) lse_out[row] = lse;
+  lse_out[row] = lse;
 }
 
-// z -> dz in place: dz = dloss (exp(z - lse) - (1 - e) [v == y] - e / V); rows
-// that take no part get zeros.
-__global__ void __launch_bounds__(kBlock) ce_grad_kernel(float* __restrict__ z, long ld, int n, int v0, int V,
-                                                         const int64_t* __restrict__ labels, long ignore_index,
-                                                         const float* __restrict__ lse,
-                                                         const float* __restrict__ dloss, float smoothing,
-                                                         int* status) {
-  const long row = blockIdx.x;
-  float* zr = z + row * ld;
-  const long label = labels[row];
-  const long y = row_label(label, ignore_index, V);
-  if (y < 0) {
-    if (threadIdx.x == 0 && label != ignore_index) atomicOr(status, DEV_BAD_INDEX);
-    for (int c = threadIdx.x; c < n; c += kBlock) zr[c] = 0.f;
-    return;
-  }
-  const float l = lse[row], g = dloss[row], uni = smoothing / (float)V;
-  for (int c = threadIdx.x; c < n; c += kBlock) {
-    float d = exp2f((zr[c] - l) * kLog2e) - uni;
-    if (v0 + c == y) d -= 1.0f - smoothing;
-    zr[c] = d * g;
+// What dz is held in units of: scale[0] = max |dloss| (1 if that is 0 or not
+// finite), scale[1] = F, and scale[2] = scale[0] (1 - smoothing) / F brings
+// products of dz back.  F is 2^14 in fp16, so that |dz| stays below fp16's
+// largest value and small probabilities stay normal numbers, and 1 in bf16.
+__global__ void __launch_bounds__(1024) dz_scale_kernel(const float* __restrict__ dloss, int M, float f,
+                                                        float smoothing, float* scale) {
+  __shared__ float sm[32];
+  float m = 0.f;
+  for (int i = threadIdx.x; i < M; i += 1024) m = fmaxf(m, fabsf(dloss[i]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < 32; ++k) m = fmaxf(m, sm[k]);
+    if (!(m > 0.f && m < INFINITY)) m = 1.f;
+    scale[0] = m;
+    scale[1] = f;
+    scale[2] = m * (1.0f - smoothing) / f;
   }
 }
 
-// ----------------------------------------------------------------------------- gate
-__device__ __forceinline__ void gate_value(int act, float g, float& a, float& da) {
-  if (act == ACT_SILU) {
-    const float s = 1.0f / (1.0f + __expf(-g));
-    a = g * s;
-    da = s * (1.0f + g * (1.0f - s));
-  } else {
-    const float cdf = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
-    a = g * cdf;
-    da = cdf + g * 0.3989422804014327f * __expf(-0.5f * g * g);
-  }
+// Column tiles per unit of the forward pass: at least 8 units a pair, at most 16 tiles.
+int ce_run(long M, long V) {
+  const long tiles = (long)ceil_div(M, 256) * ceil_div(V, 256);
+  const long r = tiles / (kPairs * 8);
+  return (int)(r < 1 ? 1 : (r > 16 ? 16 : r));
 }
 
-template <typename T>
-__global__ void gate_fwd_kernel(const float* __restrict__ g, const float* __restrict__ u, long ld, int M, int n, int act,
-                                T* __restrict__ h, long ldh) {
-  const long i = (long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (long)M * n) return;
-  const long r = i / n, c = i - r * n;
-  float a, da;
-  gate_value(act, g[r * ld + c], a, da);
-  h[r * ldh + c] = DT<T>::from(a * u[r * ld + c]);
+struct CeFwd {
+  Mat x, w;
+  int run, parts;
+  float2* ms;
+  float *sums, *zy;
+  size_t bytes;
+};
+CeFwd ce_fwd_layout(const CeArgs& a, void* ws) {
+  Carver cv{static_cast<uint8_t*>(ws)};
+  CeFwd l;
+  l.x = operand(a.dtype, a.x, a.M, a.D, cv);
+  l.w = operand(a.dtype, a.w, a.V, a.D, cv);
+  l.run = ce_run(a.M, a.V);
+  l.parts = 2 * ceil_div(ceil_div(a.V, 256), l.run);
+  const size_t n = (size_t)l.parts * a.M;
+  l.ms = cv.take<float2>(n * 8);
+  l.sums = a.smoothing > 0.f ? cv.take<float>(n * 4) : nullptr;
+  l.zy = cv.take<float>((size_t)a.M * 4);
+  l.bytes = cv.used;
+  return l;
 }
 
-// g, u -> dg, du in place.
-template <typename T>
-__global__ void gate_bwd_kernel(float* __restrict__ g, float* __restrict__ u, long ld, int M, int n, int act,
-                                const T* __restrict__ dh, long ldh) {
-  const long i = (long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (long)M * n) return;
-  const long r = i / n, c = i - r * n;
-  float a, da;
-  gate_value(act, g[r * ld + c], a, da);
-  const float d = DT<T>::to(dh[r * ldh + c]);
-  g[r * ld + c] = d * u[r * ld + c] * da;
-  u[r * ld + c] = d * a;
-}
-
-#define JEPA_TRY_CUDA(expr)                 \
-  do {                                      \
-    const cudaError_t e_ = (expr);          \
-    if (e_ != cudaSuccess) return e_;       \
-  } while (0)
-
-cudaError_t zero(void* p, size_t bytes, cudaStream_t s) {
-  return p == nullptr || bytes == 0 ? cudaSuccess : cudaMemsetAsync(p, 0, bytes, s);
+// The backward pass goes over the vocabulary in pieces whose dz takes at most
+// 256 MB, all of the same width up to rounding to 256.
+struct CeBwd {
+  Mat x, w;
+  int piece, dz_plane;
+  uint8_t* dz;
+  float *scale, *colp;
+  Reduce dx, dw;
+  size_t bytes;
+};
+CeBwd ce_bwd_layout(const CeArgs& a, void* ws) {
+  Carver cv{static_cast<uint8_t*>(ws)};
+  CeBwd l;
+  l.x = operand(a.dtype, a.x, a.M, a.D, cv);
+  l.w = operand(a.dtype, a.w, a.V, a.D, cv);
+  const long rows = split(a.dtype) ? 3 * round_up(a.M, 256) : a.M;
+  long most = ((long)256 << 20) / (2 * rows) / 256 * 256;
+  if (most < 4096) most = 4096;
+  int pieces = ceil_div(a.V, most);
+  l.piece = (int)round_up(ceil_div(a.V, pieces), 256);
+  pieces = ceil_div(a.V, l.piece);
+  l.dz_plane = split(a.dtype) ? (int)round_up(a.M, 256) : 0;
+  l.dz = cv.take<uint8_t>((size_t)rows * l.piece * 2);
+  l.scale = cv.take<float>(3 * sizeof(float));
+  l.colp = cv.take<float>((size_t)ceil_div(a.M, 32) * l.piece * 4);
+  const int n = a.V < l.piece ? a.V : l.piece;
+  l.dx = plan_reduce(a.dtype, a.M, a.D, 1, ceil_div(n, tg::kBK), pieces > 1, cv);
+  l.dw = plan_reduce(a.dtype, n, a.D, 1, ceil_div(a.M, tg::kBK), false, cv);
+  l.bytes = cv.used;
+  return l;
 }
 
 }  // namespace
 
-// ----------------------------------------------------------------------------- softmax cross entropy
-// Workspace: the rows' state (forward), the piece's logits, and (backward,
-// 16-bit) the fp32 sum of dx over the pieces.
 size_t linear_ce_workspace(int M, int D, int V, int dtype, bool backward) {
-  const size_t z = align256(sizeof(float) * (size_t)M * piece_cols(M, V, 1));
-  size_t b = backward ? z + (dtype == DTYPE_F32 ? 0 : align256(sizeof(float) * (size_t)M * D))
-                      : align256(sizeof(CeState) * (size_t)M) + z;
-  return dtype != DTYPE_F32 && D % 8 == 0 ? larger(b, linear_ce_tc_workspace(M, D, V, backward)) : b;
+  if (M == 0) return 0;
+  CeArgs a{};
+  a.M = M;
+  a.D = D;
+  a.V = V;
+  a.dtype = dtype;
+  a.smoothing = 0.5f;   // the larger layout
+  return backward ? ce_bwd_layout(a, nullptr).bytes : ce_fwd_layout(a, nullptr).bytes;
 }
 
 cudaError_t linear_ce_fwd(const CeArgs& a, float* loss, float* lse, void* ws, cudaStream_t s) {
   if (a.M == 0) return cudaSuccess;
-  if (linear_ce_tc_ok(a, nullptr, nullptr)) return linear_ce_fwd_tc(a, loss, lse, ws, s);
-  CeState* state = static_cast<CeState*>(ws);
-  float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(sizeof(CeState) * (size_t)a.M));
-  const int pc = piece_cols(a.M, a.V, 1);
-  const AnyMat x = rows_k(a.x, a.dtype, a.D);
-  for (int v0 = 0; v0 < a.V; v0 += pc) {
-    const int n = a.V - v0 < pc ? a.V - v0 : pc;
-    const AnyMat w = rows_k(static_cast<const uint8_t*>(a.w) + elem(a.dtype) * (size_t)v0 * a.D, a.dtype, a.D);
-    JEPA_TRY_CUDA(gemm_any(x, w, z, DTYPE_F32, pc, a.M, n, a.D, a.bias ? a.bias + v0 : nullptr, false, s));
-    ce_piece_kernel<<<a.M, kBlock, 0, s>>>(z, pc, n, v0, a.V, a.labels, a.ignore_index, state, v0 == 0);
-    JEPA_TRY_CUDA(cudaGetLastError());
-  }
-  ce_finish_kernel<<<blocks_for(a.M, kBlock), kBlock, 0, s>>>(state, a.labels, a.M, a.V, a.ignore_index, a.smoothing,
-                                                              loss, lse, a.status);
+  const CeFwd l = ce_fwd_layout(a, ws);
+  JEPA_TRY_CUDA(fill(a.dtype, a.x, l.x, s));
+  JEPA_TRY_CUDA(fill(a.dtype, a.w, l.w, s));
+  Params p = base_params(a.M, a.V, tg::kBN, a.status);
+  p.run = l.run;
+  set_k(p, a.D, 1, 1);
+  p.kb_chunk = split(a.dtype) ? 1 : chunk_blocks(p, false);
+  JEPA_TRY_CUDA(map_k(&p.a[0], l.x));
+  JEPA_TRY_CUDA(map_k(&p.b[0], l.w));
+  p.a_plane = (int)l.x.plane_rows;
+  p.b_plane = (int)l.w.plane_rows;
+  p.ep.bias = a.bias;
+  p.ep.labels = a.labels;
+  p.ep.V = a.V;
+  p.ep.part_ms = l.ms;
+  p.ep.part_sum = l.sums;
+  p.ep.zy = l.zy;
+  JEPA_TRY_CUDA(gemm(a.dtype, false, false, tg::CE_FWD, p, a.num_sms, s));
+  ce_join_kernel<<<blocks_for(a.M, 32), kBlock, 0, s>>>(l.ms, l.sums, l.zy, l.parts, a.M, a.V, a.labels, a.ignore_index,
+                                                        a.smoothing, loss, lse, a.status);
   return cudaGetLastError();
 }
 
 cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss, void* dx, void* dw, float* dbias,
                           void* ws, cudaStream_t s) {
-  const size_t es = elem(a.dtype);
   if (a.M == 0) {
-    JEPA_TRY_CUDA(zero(dw, es * (size_t)a.V * a.D, s));
+    JEPA_TRY_CUDA(zero(dw, elem(a.dtype) * (size_t)a.V * a.D, s));
     return zero(dbias, sizeof(float) * (size_t)a.V, s);
   }
-  if (linear_ce_tc_ok(a, dx, dw)) return linear_ce_bwd_tc(a, lse, dloss, dx, dw, dbias, ws, s);
-  const int pc = piece_cols(a.M, a.V, 1);
-  float* z = static_cast<float*>(ws);
-  float* dxa = a.dtype == DTYPE_F32
-                   ? static_cast<float*>(dx)
-                   : reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(sizeof(float) * (size_t)a.M * pc));
-  const AnyMat x = rows_k(a.x, a.dtype, a.D);
-  for (int v0 = 0; v0 < a.V; v0 += pc) {
-    const int n = a.V - v0 < pc ? a.V - v0 : pc;
-    const uint8_t* wp = static_cast<const uint8_t*>(a.w) + es * (size_t)v0 * a.D;
-    JEPA_TRY_CUDA(gemm_any(x, rows_k(wp, a.dtype, a.D), z, DTYPE_F32, pc, a.M, n, a.D, a.bias ? a.bias + v0 : nullptr,
-                           false, s));
-    ce_grad_kernel<<<a.M, kBlock, 0, s>>>(z, pc, n, v0, a.V, a.labels, a.ignore_index, lse, dloss, a.smoothing,
-                                          a.status);
+  const CeBwd l = ce_bwd_layout(a, ws);
+  const bool sp = split(a.dtype);
+  JEPA_TRY_CUDA(fill(a.dtype, a.x, l.x, s));
+  JEPA_TRY_CUDA(fill(a.dtype, a.w, l.w, s));
+  const float* unscale = nullptr;
+  if (!sp) {
+    dz_scale_kernel<<<1, 1024, 0, s>>>(dloss, a.M, a.dtype == DTYPE_F16 ? 16384.f : 1.f, a.smoothing, l.scale);
     JEPA_TRY_CUDA(cudaGetLastError());
-    if (dx != nullptr)
-      JEPA_TRY_CUDA(gemm_any(rows_k(z, DTYPE_F32, pc), k_rows(wp, a.dtype, a.D), dxa, DTYPE_F32, a.D, a.M, a.D, n,
-                             nullptr, v0 != 0, s));
-    if (dw != nullptr)
-      JEPA_TRY_CUDA(gemm_any(k_rows(z, DTYPE_F32, pc), k_rows(a.x, a.dtype, a.D),
-                             static_cast<uint8_t*>(dw) + es * (size_t)v0 * a.D, a.dtype, a.D, n, a.D, a.M, nullptr,
-                             false, s));
-    if (dbias != nullptr) JEPA_TRY_CUDA(col_sum(z, DTYPE_F32, pc, a.M, n, dbias + v0, s));
+    unscale = l.scale + 2;
   }
-  if (dx != nullptr && a.dtype != DTYPE_F32) JEPA_TRY_CUDA(cast_to(dxa, a.dtype, dx, (long)a.M * a.D, s));
+  int dx_slabs = 1;
+  for (int v0 = 0; v0 < a.V; v0 += l.piece) {
+    const int n = a.V - v0 < l.piece ? a.V - v0 : l.piece;
+    const Mat w = rows_from(l.w, v0, n);
+    Mat dz;
+    dz.p = l.dz;
+    dz.rows = a.M;
+    dz.cols = n;
+    dz.ld = l.piece;
+    dz.plane_rows = l.dz_plane;
+    {
+      Params p = base_params(a.M, n, tg::kBN, a.status);
+      set_k(p, a.D, 1, 1);
+      p.kb_chunk = sp ? 1 : (dbias != nullptr ? chunk_blocks(p, true) : kWhole);
+      JEPA_TRY_CUDA(map_k(&p.a[0], l.x));
+      JEPA_TRY_CUDA(map_k(&p.b[0], w, v0));
+      JEPA_TRY_CUDA(map_out16(&p.c[0], l.dz, sp ? 3 * (long)l.dz_plane : a.M, l.piece, l.piece));
+      p.a_plane = (int)l.x.plane_rows;
+      p.b_plane = (int)l.w.plane_rows;
+      p.c_plane = l.dz_plane;
+      p.ep.bias = a.bias != nullptr ? a.bias + v0 : nullptr;
+      p.ep.labels = a.labels;
+      p.ep.ignore_index = a.ignore_index;
+      p.ep.lse = lse;
+      p.ep.dloss = dloss;
+      p.ep.dz_scale = l.scale;
+      p.ep.smoothing = a.smoothing;
+      p.ep.v0 = v0;
+      p.ep.V = a.V;
+      p.ep.col_part = dbias != nullptr ? l.colp : nullptr;
+      p.ep.ld_col = l.piece;
+      JEPA_TRY_CUDA(gemm(a.dtype, false, false, tg::CE_BWD, p, a.num_sms, s));
+    }
+    if (dbias != nullptr)
+      JEPA_TRY_CUDA(part_sum(ColSums{{l.colp, nullptr}, {dbias + v0, nullptr}}, 1, l.piece, ceil_div(a.M, 32), n, unscale, s));
+    if (dx != nullptr) {
+      Params p = base_params(a.M, a.D, tg::kBN, a.status);
+      set_k(p, n, 1, l.dx.splits);
+      if (sp) p.kb_chunk = 1;
+      JEPA_TRY_CUDA(map_k(&p.a[0], dz));
+      JEPA_TRY_CUDA(map_mn(&p.b[0], w, v0));
+      p.a_plane = l.dz_plane;
+      p.b_plane = (int)l.w.plane_rows;
+      p.ep.scale = unscale;
+      // the first piece has the most splits: a narrower last piece adds into the first slabs
+      if (v0 == 0) dx_slabs = p.splits;
+      int epi;
+      JEPA_TRY_CUDA(reduce_output(a.dtype, l.dx, p, 0, dx, l.dx.slab, v0 != 0, &epi));
+      JEPA_TRY_CUDA(gemm(a.dtype, false, true, epi, p, a.num_sms, s));
+    }
+    if (dw != nullptr) {
+      uint8_t* out = static_cast<uint8_t*>(dw) + elem(a.dtype) * (size_t)v0 * a.D;
+      Params p = base_params(n, a.D, tg::kBN, a.status);
+      set_k(p, a.M, 1, l.dw.splits);
+      if (sp) p.kb_chunk = 1;
+      JEPA_TRY_CUDA(map_mn(&p.a[0], dz));
+      JEPA_TRY_CUDA(map_mn(&p.b[0], l.x));
+      p.a_plane = l.dz_plane;
+      p.b_plane = (int)l.x.plane_rows;
+      p.ep.scale = unscale;
+      int epi;
+      JEPA_TRY_CUDA(reduce_output(a.dtype, l.dw, p, 0, out, l.dw.slab, false, &epi));
+      JEPA_TRY_CUDA(gemm(a.dtype, true, true, epi, p, a.num_sms, s));
+      if (!l.dw.direct) JEPA_TRY_CUDA(slab_sum(a.dtype, l.dw, p.splits, p.slab_rows, out, n, a.D, unscale, s));
+    }
+  }
+  if (dx != nullptr && !l.dx.direct)
+    JEPA_TRY_CUDA(slab_sum(a.dtype, l.dx, dx_slabs, l.dx.mp, dx, a.M, a.D, unscale, s));
   return cudaSuccess;
 }
 
 // ----------------------------------------------------------------------------- gated feed-forward
-// Workspace: the piece's two projections, and (backward, 16-bit) the fp32 sum
-// of dx over the pieces.
-size_t gated_ffn_workspace(int M, int D, int F, int dtype, bool backward) {
-  size_t b = 2 * align256(sizeof(float) * (size_t)M * piece_cols(M, F, 2));
-  if (backward && dtype != DTYPE_F32) b += align256(sizeof(float) * (size_t)M * D);
-  return dtype != DTYPE_F32 && D % 8 == 0 && F % 8 == 0 ? larger(b, gated_ffn_tc_workspace(M, D, F, backward)) : b;
-}
-
 namespace {
 
-struct FfnPiece {
-  float *g, *u;
-  int pc;
+struct FfnFwd {
+  Mat x, wg, wu;
+  size_t bytes;
 };
-FfnPiece ffn_buffers(const FfnArgs& a, void* ws) {
-  FfnPiece p;
-  p.pc = piece_cols(a.M, a.F, 2);
-  p.g = static_cast<float*>(ws);
-  p.u = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(sizeof(float) * (size_t)a.M * p.pc));
-  return p;
+FfnFwd ffn_fwd_layout(const FfnArgs& a, Carver& cv) {
+  FfnFwd l;
+  l.x = operand(a.dtype, a.x, a.M, a.D, cv);
+  l.wg = operand(a.dtype, a.wg, a.F, a.D, cv);
+  l.wu = operand(a.dtype, a.wu, a.F, a.D, cv);
+  l.bytes = cv.used;
+  return l;
 }
-cudaError_t ffn_project(const FfnArgs& a, const FfnPiece& p, int f0, int n, cudaStream_t s) {
-  const size_t off = elem(a.dtype) * (size_t)f0 * a.D;
-  const AnyMat x = rows_k(a.x, a.dtype, a.D);
-  JEPA_TRY_CUDA(gemm_any(x, rows_k(static_cast<const uint8_t*>(a.wg) + off, a.dtype, a.D), p.g, DTYPE_F32, p.pc, a.M, n,
-                         a.D, a.bg ? a.bg + f0 : nullptr, false, s));
-  return gemm_any(x, rows_k(static_cast<const uint8_t*>(a.wu) + off, a.dtype, a.D), p.u, DTYPE_F32, p.pc, a.M, n, a.D,
-                  a.bu ? a.bu + f0 : nullptr, false, s);
+// dg and du are [M, fp], in planes for fp32.
+struct FfnBwd {
+  FfnFwd in;
+  int fp, d_plane;
+  uint8_t* d[2];
+  float* colp[2];
+  Reduce dx, dw;
+  float* dw_slab[2];
+  size_t bytes;
+};
+FfnBwd ffn_bwd_layout(const FfnArgs& a, void* ws) {
+  Carver cv{static_cast<uint8_t*>(ws)};
+  FfnBwd l;
+  l.in = ffn_fwd_layout(a, cv);
+  l.fp = (int)round_up(a.F, 64);
+  l.d_plane = split(a.dtype) ? (int)round_up(a.M, 256) : 0;
+  const long rows = split(a.dtype) ? 3 * (long)l.d_plane : a.M;
+  for (int k = 0; k < 2; ++k) l.d[k] = cv.take<uint8_t>((size_t)rows * l.fp * 2);
+  for (int k = 0; k < 2; ++k) l.colp[k] = cv.take<float>((size_t)ceil_div(a.M, 32) * l.fp * 4);
+  l.dx = plan_reduce(a.dtype, a.M, a.D, 1, 2 * ceil_div(a.F, tg::kBK), false, cv);
+  l.dw = plan_reduce(a.dtype, a.F, a.D, 2, ceil_div(a.M, tg::kBK), false, cv);
+  l.dw_slab[0] = l.dw.slab;
+  l.dw_slab[1] = l.dw.direct ? nullptr : cv.take<float>((size_t)l.dw.splits * l.dw.mp * l.dw.np * 4);
+  l.bytes = cv.used;
+  return l;
+}
+cudaError_t ffn_product(const FfnArgs& a, const FfnFwd& l, Params& p, cudaStream_t s) {
+  JEPA_TRY_CUDA(fill(a.dtype, a.x, l.x, s));
+  JEPA_TRY_CUDA(fill(a.dtype, a.wg, l.wg, s));
+  JEPA_TRY_CUDA(fill(a.dtype, a.wu, l.wu, s));
+  p = base_params(a.M, a.F, tg::kBN / 2, a.status);
+  set_k(p, a.D, 1, 1);
+  if (split(a.dtype)) p.kb_chunk = 1;
+  JEPA_TRY_CUDA(map_k(&p.a[0], l.x));
+  JEPA_TRY_CUDA(map_k(&p.b[0], l.wg));
+  JEPA_TRY_CUDA(map_k(&p.b[1], l.wu));
+  p.a_plane = (int)l.x.plane_rows;
+  p.b_plane = (int)l.wg.plane_rows;
+  p.ep.bias = a.bg;
+  p.ep.bias2 = a.bu;
+  p.ep.act = a.act;
+  return cudaSuccess;
 }
 
 }  // namespace
 
+size_t gated_ffn_workspace(int M, int D, int F, int dtype, bool backward) {
+  if (M == 0) return 0;
+  FfnArgs a{};
+  a.M = M;
+  a.D = D;
+  a.F = F;
+  a.dtype = dtype;
+  if (backward) return ffn_bwd_layout(a, nullptr).bytes;
+  Carver cv{nullptr};
+  return ffn_fwd_layout(a, cv).bytes;
+}
+
 cudaError_t gated_ffn_fwd(const FfnArgs& a, void* h, void* ws, cudaStream_t s) {
   if (a.M == 0) return cudaSuccess;
-  if (gated_ffn_tc_ok(a, h, nullptr, nullptr, nullptr)) return gated_ffn_fwd_tc(a, h, s);
-  const FfnPiece p = ffn_buffers(a, ws);
-  for (int f0 = 0; f0 < a.F; f0 += p.pc) {
-    const int n = a.F - f0 < p.pc ? a.F - f0 : p.pc;
-    JEPA_TRY_CUDA(ffn_project(a, p, f0, n, s));
-    const unsigned b = blocks_for((long)a.M * n, kBlock);
-    if (a.dtype == DTYPE_F32)
-      gate_fwd_kernel<float><<<b, kBlock, 0, s>>>(p.g, p.u, p.pc, a.M, n, a.act, (float*)h + f0, a.F);
-    else if (a.dtype == DTYPE_F16)
-      gate_fwd_kernel<__half><<<b, kBlock, 0, s>>>(p.g, p.u, p.pc, a.M, n, a.act, (__half*)h + f0, a.F);
-    else
-      gate_fwd_kernel<__nv_bfloat16><<<b, kBlock, 0, s>>>(p.g, p.u, p.pc, a.M, n, a.act, (__nv_bfloat16*)h + f0, a.F);
-    JEPA_TRY_CUDA(cudaGetLastError());
+  Carver cv{static_cast<uint8_t*>(ws)};
+  const FfnFwd l = ffn_fwd_layout(a, cv);
+  Params p;
+  JEPA_TRY_CUDA(ffn_product(a, l, p, s));
+  if ((a.F * elem(a.dtype)) % 16 != 0) {
+    p.plain = h;
+    p.plain_ld = a.F;
+  } else if (split(a.dtype)) {
+    JEPA_TRY_CUDA(map_out32(&p.c[0], h, a.M, a.F, a.F));
+  } else {
+    JEPA_TRY_CUDA(map_out16(&p.c[0], h, a.M, a.F, a.F));
   }
-  return cudaSuccess;
+  return gemm(a.dtype, false, false, tg::GATE_FWD, p, a.num_sms, s);
 }
 
 cudaError_t gated_ffn_bwd(const FfnArgs& a, const void* dh, void* dx, void* dwg, void* dwu, float* dbg, float* dbu,
                           void* ws, cudaStream_t s) {
-  const size_t es = elem(a.dtype);
   if (a.M == 0) {
-    JEPA_TRY_CUDA(zero(dwg, es * (size_t)a.F * a.D, s));
-    JEPA_TRY_CUDA(zero(dwu, es * (size_t)a.F * a.D, s));
-    JEPA_TRY_CUDA(zero(dbg, sizeof(float) * (size_t)a.F, s));
-    return zero(dbu, sizeof(float) * (size_t)a.F, s);
+    for (void* dw : {dwg, dwu}) JEPA_TRY_CUDA(zero(dw, elem(a.dtype) * (size_t)a.F * a.D, s));
+    for (float* db : {dbg, dbu}) JEPA_TRY_CUDA(zero(db, sizeof(float) * (size_t)a.F, s));
+    return cudaSuccess;
   }
-  if (gated_ffn_tc_ok(a, dh, dx, dwg, dwu)) return gated_ffn_bwd_tc(a, dh, dx, dwg, dwu, dbg, dbu, ws, s);
-  const FfnPiece p = ffn_buffers(a, ws);
-  float* dxa = a.dtype == DTYPE_F32
-                   ? static_cast<float*>(dx)
-                   : reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 2 * align256(sizeof(float) * (size_t)a.M * p.pc));
-  for (int f0 = 0; f0 < a.F; f0 += p.pc) {
-    const int n = a.F - f0 < p.pc ? a.F - f0 : p.pc;
-    JEPA_TRY_CUDA(ffn_project(a, p, f0, n, s));
-    const unsigned b = blocks_for((long)a.M * n, kBlock);
-    if (a.dtype == DTYPE_F32)
-      gate_bwd_kernel<float><<<b, kBlock, 0, s>>>(p.g, p.u, p.pc, a.M, n, a.act, (const float*)dh + f0, a.F);
-    else if (a.dtype == DTYPE_F16)
-      gate_bwd_kernel<__half><<<b, kBlock, 0, s>>>(p.g, p.u, p.pc, a.M, n, a.act, (const __half*)dh + f0, a.F);
-    else
-      gate_bwd_kernel<__nv_bfloat16><<<b, kBlock, 0, s>>>(p.g, p.u, p.pc, a.M, n, a.act, (const __nv_bfloat16*)dh + f0, a.F);
-    JEPA_TRY_CUDA(cudaGetLastError());
-    const size_t off = es * (size_t)f0 * a.D;
-    for (int k = 0; k < 2; ++k) {
-      const float* d = k == 0 ? p.g : p.u;
-      const uint8_t* w = static_cast<const uint8_t*>(k == 0 ? a.wg : a.wu) + off;
-      void* dw = k == 0 ? dwg : dwu;
-      float* db = k == 0 ? dbg : dbu;
-      if (dx != nullptr)
-        JEPA_TRY_CUDA(gemm_any(rows_k(d, DTYPE_F32, p.pc), k_rows(w, a.dtype, a.D), dxa, DTYPE_F32, a.D, a.M, a.D, n,
-                               nullptr, f0 != 0 || k != 0, s));
-      if (dw != nullptr)
-        JEPA_TRY_CUDA(gemm_any(k_rows(d, DTYPE_F32, p.pc), k_rows(a.x, a.dtype, a.D), static_cast<uint8_t*>(dw) + off,
-                               a.dtype, a.D, n, a.D, a.M, nullptr, false, s));
-      if (db != nullptr) JEPA_TRY_CUDA(col_sum(d, DTYPE_F32, p.pc, a.M, n, db + f0, s));
+  const FfnBwd l = ffn_bwd_layout(a, ws);
+  const bool sp = split(a.dtype);
+  Mat d[2];
+  for (int k = 0; k < 2; ++k) {
+    d[k].p = l.d[k];
+    d[k].rows = a.M;
+    d[k].cols = a.F;
+    d[k].ld = l.fp;
+    d[k].plane_rows = l.d_plane;
+  }
+  {
+    Params p;
+    JEPA_TRY_CUDA(ffn_product(a, l.in, p, s));
+    for (int k = 0; k < 2; ++k)
+      JEPA_TRY_CUDA(map_out16(&p.c[k], l.d[k], sp ? 3 * (long)l.d_plane : a.M, l.fp, l.fp));
+    if (!sp && (dbg != nullptr || dbu != nullptr)) p.kb_chunk = chunk_blocks(p, true);
+    p.c_plane = l.d_plane;
+    p.ep.dh = dh;
+    p.ep.dh_vec = (a.F * elem(a.dtype)) % 16 == 0;
+    p.ep.col_part = dbg != nullptr ? l.colp[0] : nullptr;
+    p.ep.col_part2 = dbu != nullptr ? l.colp[1] : nullptr;
+    p.ep.ld_col = l.fp;
+    JEPA_TRY_CUDA(gemm(a.dtype, false, false, tg::GATE_BWD, p, a.num_sms, s));
+  }
+  ColSums cs{};
+  int sums = 0;
+  for (int k = 0; k < 2; ++k)
+    if ((k == 0 ? dbg : dbu) != nullptr) {
+      cs.a[sums] = l.colp[k];
+      cs.out[sums++] = k == 0 ? dbg : dbu;
     }
+  if (sums > 0) JEPA_TRY_CUDA(part_sum(cs, sums, l.fp, ceil_div(a.M, 32), a.F, nullptr, s));
+  if (dx != nullptr) {
+    Params p = base_params(a.M, a.D, tg::kBN, a.status);
+    set_k(p, a.F, 2, l.dx.splits);
+    if (sp) p.kb_chunk = 1;
+    for (int k = 0; k < 2; ++k) {
+      JEPA_TRY_CUDA(map_k(&p.a[k], d[k]));
+      JEPA_TRY_CUDA(map_mn(&p.b[k], k == 0 ? l.in.wg : l.in.wu));
+    }
+    p.a_plane = l.d_plane;
+    p.b_plane = (int)l.in.wg.plane_rows;
+    int epi;
+    JEPA_TRY_CUDA(reduce_output(a.dtype, l.dx, p, 0, dx, l.dx.slab, false, &epi));
+    JEPA_TRY_CUDA(gemm(a.dtype, false, true, epi, p, a.num_sms, s));
+    if (!l.dx.direct) JEPA_TRY_CUDA(slab_sum(a.dtype, l.dx, p.splits, p.slab_rows, dx, a.M, a.D, nullptr, s));
   }
-  if (dx != nullptr && a.dtype != DTYPE_F32) JEPA_TRY_CUDA(cast_to(dxa, a.dtype, dx, (long)a.M * a.D, s));
+  void* dw[2] = {dwg, dwu};
+  if (dwg == nullptr && dwu == nullptr) return cudaSuccess;
+  // the weight gradients that are wanted are one launch
+  Params p = base_params(a.F, a.D, tg::kBN, a.status);
+  set_k(p, a.M, 1, l.dw.splits);
+  if (sp) p.kb_chunk = 1;
+  JEPA_TRY_CUDA(map_mn(&p.b[0], l.in.x));
+  p.a_plane = l.d_plane;
+  p.b_plane = (int)l.in.x.plane_rows;
+  int nz = 0, epi = 0;
+  for (int k = 0; k < 2; ++k) {
+    if (dw[k] == nullptr) continue;
+    JEPA_TRY_CUDA(map_mn(&p.a[nz], d[k]));
+    JEPA_TRY_CUDA(reduce_output(a.dtype, l.dw, p, nz, dw[k], l.dw_slab[k], false, &epi));
+    ++nz;
+  }
+  p.nz = nz;
+  JEPA_TRY_CUDA(gemm(a.dtype, true, true, epi, p, a.num_sms, s));
+  if (!l.dw.direct)
+    for (int k = 0; k < 2; ++k) {
+      if (dw[k] == nullptr) continue;
+      Reduce r = l.dw;
+      r.slab = l.dw_slab[k];
+      JEPA_TRY_CUDA(slab_sum(a.dtype, r, p.splits, p.slab_rows, dw[k], a.F, a.D, nullptr, s));
+    }
   return cudaSuccess;
 }
 
 // ----------------------------------------------------------------------------- linear layer backward
+namespace {
+
+struct LinBwd {
+  Mat d, A, W;
+  Reduce dA, dW;
+  float* colp;
+  size_t bytes;
+};
+LinBwd lin_bwd_layout(int dtype, const void* dout, const void* A, const void* W, int M, int N, int K, void* ws) {
+  Carver cv{static_cast<uint8_t*>(ws)};
+  LinBwd l;
+  l.d = operand(dtype, dout, M, N, cv);
+  l.A = operand(dtype, A, M, K, cv);
+  l.W = operand(dtype, W, N, K, cv);
+  l.dA = plan_reduce(dtype, M, K, 1, ceil_div(N, tg::kBK), false, cv);
+  l.dW = plan_reduce(dtype, N, K, 1, ceil_div(M, tg::kBK), false, cv);
+  l.colp = cv.take<float>((size_t)col_strips(M, N) * N * 4);
+  l.bytes = cv.used;
+  return l;
+}
+
+}  // namespace
+
 size_t linear_bwd_workspace(int M, int N, int K, int dtype) {
-  return dtype != DTYPE_F32 && N % 8 == 0 && K % 8 == 0 ? linear_bwd_tc_workspace(M, N, K) : 0;
+  return M == 0 ? 0 : lin_bwd_layout(dtype, nullptr, nullptr, nullptr, M, N, K, nullptr).bytes;
 }
 
 cudaError_t linear_bwd(int dtype, const void* dout, const void* A, const void* W, void* dA, void* dW, float* dbias,
@@ -420,14 +872,32 @@ cudaError_t linear_bwd(int dtype, const void* dout, const void* A, const void* W
     JEPA_TRY_CUDA(zero(dW, elem(dtype) * (size_t)N * K, s));
     return zero(dbias, sizeof(float) * (size_t)N, s);
   }
-  if (linear_bwd_tc_ok(dtype, dout, A, W, dA, dW, N, K))
-    return linear_bwd_tc(dtype, dout, A, W, dA, dW, dbias, M, N, K, ws, status, num_sms, s);
-  if (dA != nullptr)
-    JEPA_TRY_CUDA(gemm_any(rows_k(dout, dtype, N), k_rows(W, dtype, K), dA, dtype, K, M, K, N, nullptr, false, s));
-  if (dW != nullptr)
-    JEPA_TRY_CUDA(gemm_any(k_rows(dout, dtype, N), k_rows(A, dtype, K), dW, dtype, K, N, K, M, nullptr, false, s));
-  if (dbias != nullptr) JEPA_TRY_CUDA(col_sum(dout, dtype, N, M, N, dbias, s));
-  return cudaSuccess;
+  const LinBwd l = lin_bwd_layout(dtype, dout, A, W, M, N, K, ws);
+  if (dA != nullptr || dW != nullptr) JEPA_TRY_CUDA(fill(dtype, dout, l.d, s));
+  for (int k = 0; k < 2; ++k) {
+    // dA = dout W, then dW = dout^T A
+    void* out = k == 0 ? dA : dW;
+    if (out == nullptr) continue;
+    const Mat& b = k == 0 ? l.W : l.A;
+    const Reduce& rd = k == 0 ? l.dA : l.dW;
+    const int rows = k == 0 ? M : N;
+    JEPA_TRY_CUDA(fill(dtype, k == 0 ? W : A, b, s));
+    Params p = base_params(rows, K, tg::kBN, status);
+    set_k(p, k == 0 ? N : M, 1, rd.splits);
+    if (split(dtype)) p.kb_chunk = 1;
+    JEPA_TRY_CUDA(k == 0 ? map_k(&p.a[0], l.d) : map_mn(&p.a[0], l.d));
+    JEPA_TRY_CUDA(map_mn(&p.b[0], b));
+    p.a_plane = (int)l.d.plane_rows;
+    p.b_plane = (int)b.plane_rows;
+    int epi;
+    JEPA_TRY_CUDA(reduce_output(dtype, rd, p, 0, out, rd.slab, false, &epi));
+    JEPA_TRY_CUDA(gemm(dtype, k != 0, true, epi, p, num_sms, s));
+    if (!rd.direct) JEPA_TRY_CUDA(slab_sum(dtype, rd, p.splits, p.slab_rows, out, rows, K, nullptr, s));
+  }
+  if (dbias == nullptr) return cudaSuccess;
+  if (dtype == DTYPE_F32) return col_sum_t<float>(dout, M, N, l.colp, dbias, s);
+  if (dtype == DTYPE_F16) return col_sum_t<__half>(dout, M, N, l.colp, dbias, s);
+  return col_sum_t<__nv_bfloat16>(dout, M, N, l.colp, dbias, s);
 }
 
 }  // namespace jepa

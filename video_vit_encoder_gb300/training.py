@@ -13,21 +13,26 @@ not asked for (``needs``) are returned as None.
 """
 from __future__ import annotations
 
-import ctypes as C
+import functools
 
 import torch
 
 from . import _lib
 from ._lib import check, load
-from .binding import DTYPE_CODE, _ptr
+from .binding import DTYPE_CODE
 
 _CODE = {torch.float32: DTYPE_CODE["f32"], torch.float16: DTYPE_CODE["f16"], torch.bfloat16: DTYPE_CODE["bf16"]}
+# the handle of a device's current stream (a call a fifth as long as through torch.cuda.current_stream)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_empty = torch.empty
+_f32 = torch.float32
 _ACT = {"silu": _lib.GATE_SILU, "gelu": _lib.GATE_GELU}
 
 
 def _expect(name, t, shape, dtype, device):
     """t is None or a contiguous tensor of this shape, dtype and device."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
         return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -35,8 +40,7 @@ def _expect(name, t, shape, dtype, device):
         raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _matrix(name, t):
@@ -46,41 +50,42 @@ def _matrix(name, t):
 
 
 def _code(name, dtype):
-    if dtype not in _CODE:
+    code = _CODE.get(dtype)
+    if code is None:
         raise ValueError(f"{name} is {dtype}: float32, float16 or bfloat16")
-    return _CODE[dtype]
+    return code
 
 
-class _Launch:
-    """The device and stream of one call: current while it allocates and launches."""
+def _p(t):
+    return None if t is None else t.data_ptr()
 
-    def __init__(self, t, stream):
-        if t.device.type != "cuda":
-            raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
-        self.device = t.device
-        if stream is not None and stream.device != t.device:
-            raise ValueError(f"stream is on {stream.device}, tensors are on {t.device}")
-        self.stream = stream
 
-    def __enter__(self):
-        self._dev = torch.cuda.device(self.device)
-        self._dev.__enter__()
-        self._ctx = torch.cuda.stream(self.stream) if self.stream is not None else None
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        self.handle = C.c_void_p(torch.cuda.current_stream().cuda_stream)
-        return self
+def _a16(t):
+    """The matrix, or a copy of one that does not start on 16 bytes (a view
+    into another tensor can start anywhere)."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
 
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-        self._dev.__exit__(*exc)
 
-    def empty(self, shape, dtype, wanted=True):
-        return torch.empty(shape, dtype=dtype, device=self.device) if wanted else None
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(query, *sizes):
+    return getattr(load(), query)(*sizes)
 
-    def workspace(self, nbytes):
-        return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+
+def _run(t, stream, body):
+    """body(device, stream handle) with t's device and the stream current, so
+    that what it allocates belongs to the stream that uses it."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return body(t.device, _raw_stream(index))
+        with torch.cuda.device(index):
+            return body(t.device, _raw_stream(index))
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, tensors are on {t.device}")
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        return body(t.device, stream.cuda_stream)
 
 
 def layernorm_fwd(x, w, b, eps, out_dtype=None, stream=None):
@@ -88,19 +93,23 @@ def layernorm_fwd(x, w, b, eps, out_dtype=None, stream=None):
     [dim].  y has out_dtype (default x's; another one needs float32 x), mean
     and rstd are float32 of x's leading shape."""
     lib = load()
-    dim = x.shape[-1]
-    out_dtype = out_dtype or x.dtype
-    xc, yc = _code("x", x.dtype), _code("out_dtype", out_dtype)
-    _expect("x", x, x.shape, x.dtype, x.device)
-    _expect("w", w, (dim,), torch.float32, x.device)
-    _expect("b", b, (dim,), torch.float32, x.device)
-    rows = x.numel() // dim if dim else 0
-    with _Launch(x, stream) as la:
-        y = la.empty(x.shape, out_dtype)
-        mean, rstd = la.empty(x.shape[:-1], torch.float32), la.empty(x.shape[:-1], torch.float32)
-        check(lib.jepa_layernorm_fwd(_ptr(x), _ptr(w), _ptr(b), _ptr(y), _ptr(mean), _ptr(rstd), rows, dim, xc, yc,
-                                     eps, la.handle))
-    return y, mean, rstd
+    shape, dt = x.shape, x.dtype
+    dim = shape[-1]
+    out_dtype = out_dtype or dt
+    xc, yc = _code("x", dt), _code("out_dtype", out_dtype)
+    dev = x.device
+    _expect("x", x, shape, dt, dev)
+    _expect("w", w, (dim,), _f32, dev)
+    _expect("b", b, (dim,), _f32, dev)
+
+    def body(dev, handle):
+        lead = shape[:-1]
+        rows = lead.numel()
+        y = _empty(shape, dtype=out_dtype, device=dev)
+        mean, rstd = _empty(lead, dtype=_f32, device=dev), _empty(lead, dtype=_f32, device=dev)
+        check(lib.jepa_layernorm_fwd(_p(x), _p(w), _p(b), _p(y), _p(mean), _p(rstd), rows, dim, xc, yc, eps, handle))
+        return y, mean, rstd
+    return _run(x, stream, body)
 
 
 def layernorm_bwd(dy, x, w, mean, rstd, residual=None, needs=(True, True), stream=None):
@@ -108,33 +117,40 @@ def layernorm_bwd(dy, x, w, mean, rstd, residual=None, needs=(True, True), strea
     mean and rstd.  residual: x's shape and dtype, added to dx.  needs: (dw,
     db)."""
     lib = load()
-    dim = x.shape[-1]
-    xc, yc = _code("x", x.dtype), _code("dy", dy.dtype)
-    dev = x.device
-    for name, t, shape, dt in (("x", x, x.shape, x.dtype), ("dy", dy, x.shape, dy.dtype),
-                               ("w", w, (dim,), torch.float32), ("mean", mean, x.shape[:-1], torch.float32),
-                               ("rstd", rstd, x.shape[:-1], torch.float32), ("residual", residual, x.shape, x.dtype)):
-        _expect(name, t, shape, dt, dev)
-    rows = x.numel() // dim if dim else 0
-    with _Launch(x, stream) as la:
-        dx = la.empty(x.shape, x.dtype)
-        dw, db = la.empty((dim,), torch.float32, needs[0]), la.empty((dim,), torch.float32, needs[1])
-        ws = la.workspace(lib.jepa_layernorm_bwd_workspace_bytes(rows, dim))
-        check(lib.jepa_layernorm_bwd(_ptr(dy), _ptr(x), _ptr(w), _ptr(mean), _ptr(rstd), _ptr(residual), _ptr(dx),
-                                     _ptr(dw), _ptr(db), rows, dim, xc, yc, _ptr(ws), ws.numel(), la.handle))
-    return dx, dw, db
+    shape, dt, dev = x.shape, x.dtype, x.device
+    dim, lead = shape[-1], shape[:-1]
+    xc, yc = _code("x", dt), _code("dy", dy.dtype)
+    _expect("x", x, shape, dt, dev)
+    _expect("dy", dy, shape, dy.dtype, dev)
+    _expect("w", w, (dim,), _f32, dev)
+    _expect("mean", mean, lead, _f32, dev)
+    _expect("rstd", rstd, lead, _f32, dev)
+    _expect("residual", residual, shape, dt, dev)
+
+    def body(dev, handle):
+        rows = lead.numel()
+        dx = _empty(shape, dtype=dt, device=dev)
+        dw = _empty(dim, dtype=_f32, device=dev) if needs[0] else None
+        db = _empty(dim, dtype=_f32, device=dev) if needs[1] else None
+        n = _workspace_bytes("jepa_layernorm_bwd_workspace_bytes", rows, dim)
+        ws = _empty(n, dtype=torch.uint8, device=dev)
+        check(lib.jepa_layernorm_bwd(_p(dy), _p(x), _p(w), _p(mean), _p(rstd), _p(residual), _p(dx), _p(dw), _p(db),
+                                     rows, dim, xc, yc, _p(ws), n, handle))
+        return dx, dw, db
+    return _run(x, stream, body)
 
 
 def _ce_args(x, W, bias, labels):
     M, D = _matrix("x", x)
     V = _matrix("W", W)[0]
-    code = _code("x", x.dtype)
-    for name, t, shape, dt in (("x", x, x.shape, x.dtype), ("W", W, (V, D), x.dtype),
-                               ("bias", bias, (V,), torch.float32)):
-        _expect(name, t, shape, dt, x.device)
+    dt, dev = x.dtype, x.device
+    code = _code("x", dt)
+    _expect("x", x, (M, D), dt, dev)
+    _expect("W", W, (V, D), dt, dev)
+    _expect("bias", bias, (V,), _f32, dev)
     if labels.dtype not in (torch.int32, torch.int64):
         raise ValueError(f"labels are {labels.dtype}: int64 or int32")
-    _expect("labels", labels, (M,), labels.dtype, x.device)
+    _expect("labels", labels, (M,), labels.dtype, dev)
     return M, D, V, code
 
 
@@ -144,13 +160,16 @@ def linear_ce_fwd(x, W, bias, labels, ignore_index=-100, smoothing=0.0, stream=N
     Rows with label ignore_index have loss 0."""
     lib = load()
     M, D, V, code = _ce_args(x, W, bias, labels)
-    with _Launch(x, stream) as la:
-        labels = labels.long()
-        loss, lse = la.empty((M,), torch.float32), la.empty((M,), torch.float32)
-        ws = la.workspace(lib.jepa_linear_ce_workspace_bytes(M, D, V, code, 0))
-        check(lib.jepa_linear_ce_fwd(_ptr(x), _ptr(W), _ptr(bias), _ptr(labels), _ptr(loss), _ptr(lse), M, D, V, code,
-                                     ignore_index, smoothing, _ptr(ws), ws.numel(), la.handle))
-    return loss, lse
+
+    def body(dev, handle):
+        lab, xx, ww = labels.long(), _a16(x), _a16(W)
+        loss, lse = _empty(M, dtype=_f32, device=dev), _empty(M, dtype=_f32, device=dev)
+        n = _workspace_bytes("jepa_linear_ce_workspace_bytes", M, D, V, code, 0)
+        ws = _empty(n, dtype=torch.uint8, device=dev)
+        check(lib.jepa_linear_ce_fwd(_p(xx), _p(ww), _p(bias), _p(lab), _p(loss), _p(lse), M, D, V, code, ignore_index,
+                                     smoothing, _p(ws), n, handle))
+        return loss, lse
+    return _run(x, stream, body)
 
 
 def linear_ce_bwd(dloss, x, W, bias, labels, lse, ignore_index=-100, smoothing=0.0, needs=(True, True, True),
@@ -160,30 +179,36 @@ def linear_ce_bwd(dloss, x, W, bias, labels, lse, ignore_index=-100, smoothing=0
     pass's lse.  needs: (dx, dW, dbias)."""
     lib = load()
     M, D, V, code = _ce_args(x, W, bias, labels)
-    _expect("lse", lse, (M,), torch.float32, x.device)
-    with _Launch(x, stream) as la:
-        labels = labels.long()
-        if not torch.is_tensor(dloss):
-            dloss = torch.full((M,), float(dloss), device=x.device)
-        elif dloss.dim() == 0:
-            dloss = dloss.to(device=x.device, dtype=torch.float32).expand(M).contiguous()
-        _expect("dloss", dloss, (M,), torch.float32, x.device)
-        dx, dW = la.empty((M, D), x.dtype, needs[0]), la.empty((V, D), x.dtype, needs[1])
-        dbias = la.empty((V,), torch.float32, needs[2])
-        ws = la.workspace(lib.jepa_linear_ce_workspace_bytes(M, D, V, code, 1))
-        check(lib.jepa_linear_ce_bwd(_ptr(x), _ptr(W), _ptr(bias), _ptr(labels), _ptr(lse), _ptr(dloss), _ptr(dx),
-                                     _ptr(dW), _ptr(dbias), M, D, V, code, ignore_index, smoothing, _ptr(ws),
-                                     ws.numel(), la.handle))
-    return dx, dW, dbias
+    _expect("lse", lse, (M,), _f32, x.device)
+
+    def body(dev, handle):
+        lab, dl, dt, xx, ww = labels.long(), dloss, x.dtype, _a16(x), _a16(W)
+        if not torch.is_tensor(dl):
+            dl = torch.full((M,), float(dl), device=dev)
+        elif dl.dim() == 0:
+            dl = dl.to(device=dev, dtype=_f32).expand(M).contiguous()
+        _expect("dloss", dl, (M,), _f32, dev)
+        dx = _empty((M, D), dtype=dt, device=dev) if needs[0] else None
+        dW = _empty((V, D), dtype=dt, device=dev) if needs[1] else None
+        db = _empty(V, dtype=_f32, device=dev) if needs[2] else None
+        n = _workspace_bytes("jepa_linear_ce_workspace_bytes", M, D, V, code, 1)
+        ws = _empty(n, dtype=torch.uint8, device=dev)
+        check(lib.jepa_linear_ce_bwd(_p(xx), _p(ww), _p(bias), _p(lab), _p(lse), _p(dl), _p(dx), _p(dW), _p(db), M, D, V,
+                                     code, ignore_index, smoothing, _p(ws), n, handle))
+        return dx, dW, db
+    return _run(x, stream, body)
 
 
 def _ffn_args(x, Wg, Wu, bg, bu, act):
     M, D = _matrix("x", x)
     F = _matrix("Wg", Wg)[0]
-    code = _code("x", x.dtype)
-    for name, t, shape, dt in (("x", x, x.shape, x.dtype), ("Wg", Wg, (F, D), x.dtype), ("Wu", Wu, (F, D), x.dtype),
-                               ("bg", bg, (F,), torch.float32), ("bu", bu, (F,), torch.float32)):
-        _expect(name, t, shape, dt, x.device)
+    dt, dev = x.dtype, x.device
+    code = _code("x", dt)
+    _expect("x", x, (M, D), dt, dev)
+    _expect("Wg", Wg, (F, D), dt, dev)
+    _expect("Wu", Wu, (F, D), dt, dev)
+    _expect("bg", bg, (F,), _f32, dev)
+    _expect("bu", bu, (F,), _f32, dev)
     if act not in _ACT:
         raise ValueError(f"act {act!r}: 'silu' or 'gelu'")
     return M, D, F, code, _ACT[act]
@@ -194,12 +219,15 @@ def gated_ffn_fwd(x, Wg, Wu, bg=None, bu=None, act="silu", stream=None):
     Wg, Wu [F, D]; bg, bu float [F] or None; act 'silu' or 'gelu' (erf)."""
     lib = load()
     M, D, F, code, a = _ffn_args(x, Wg, Wu, bg, bu, act)
-    with _Launch(x, stream) as la:
-        h = la.empty((M, F), x.dtype)
-        ws = la.workspace(lib.jepa_gated_ffn_workspace_bytes(M, D, F, code, 0))
-        check(lib.jepa_gated_ffn_fwd(_ptr(x), _ptr(Wg), _ptr(Wu), _ptr(bg), _ptr(bu), _ptr(h), M, D, F, code, a,
-                                     _ptr(ws), ws.numel(), la.handle))
-    return h
+
+    def body(dev, handle):
+        xx, wg, wu = _a16(x), _a16(Wg), _a16(Wu)
+        h = _empty((M, F), dtype=x.dtype, device=dev)
+        n = _workspace_bytes("jepa_gated_ffn_workspace_bytes", M, D, F, code, 0)
+        ws = _empty(n, dtype=torch.uint8, device=dev) if n else None
+        check(lib.jepa_gated_ffn_fwd(_p(xx), _p(wg), _p(wu), _p(bg), _p(bu), _p(h), M, D, F, code, a, _p(ws), n, handle))
+        return h
+    return _run(x, stream, body)
 
 
 def gated_ffn_bwd(dh, x, Wg, Wu, bg=None, bu=None, act="silu", needs=(True, True, True, True, True), stream=None):
@@ -208,15 +236,20 @@ def gated_ffn_bwd(dh, x, Wg, Wu, bg=None, bu=None, act="silu", needs=(True, True
     lib = load()
     M, D, F, code, a = _ffn_args(x, Wg, Wu, bg, bu, act)
     _expect("dh", dh, (M, F), x.dtype, x.device)
-    with _Launch(x, stream) as la:
-        dx = la.empty((M, D), x.dtype, needs[0])
-        dWg, dWu = la.empty((F, D), x.dtype, needs[1]), la.empty((F, D), x.dtype, needs[2])
-        dbg, dbu = la.empty((F,), torch.float32, needs[3]), la.empty((F,), torch.float32, needs[4])
-        ws = la.workspace(lib.jepa_gated_ffn_workspace_bytes(M, D, F, code, 1))
-        check(lib.jepa_gated_ffn_bwd(_ptr(dh), _ptr(x), _ptr(Wg), _ptr(Wu), _ptr(bg), _ptr(bu), _ptr(dx), _ptr(dWg),
-                                     _ptr(dWu), _ptr(dbg), _ptr(dbu), M, D, F, code, a, _ptr(ws), ws.numel(),
-                                     la.handle))
-    return dx, dWg, dWu, dbg, dbu
+
+    def body(dev, handle):
+        dt, d, xx, wg, wu = x.dtype, _a16(dh), _a16(x), _a16(Wg), _a16(Wu)
+        dx = _empty((M, D), dtype=dt, device=dev) if needs[0] else None
+        dWg = _empty((F, D), dtype=dt, device=dev) if needs[1] else None
+        dWu = _empty((F, D), dtype=dt, device=dev) if needs[2] else None
+        dbg = _empty(F, dtype=_f32, device=dev) if needs[3] else None
+        dbu = _empty(F, dtype=_f32, device=dev) if needs[4] else None
+        n = _workspace_bytes("jepa_gated_ffn_workspace_bytes", M, D, F, code, 1)
+        ws = _empty(n, dtype=torch.uint8, device=dev)
+        check(lib.jepa_gated_ffn_bwd(_p(d), _p(xx), _p(wg), _p(wu), _p(bg), _p(bu), _p(dx), _p(dWg), _p(dWu), _p(dbg),
+                                     _p(dbu), M, D, F, code, a, _p(ws), n, handle))
+        return dx, dWg, dWu, dbg, dbu
+    return _run(x, stream, body)
 
 
 def linear_bwd(dout, A, W, bias=True, needs=(True, True), stream=None):
@@ -226,13 +259,19 @@ def linear_bwd(dout, A, W, bias=True, needs=(True, True), stream=None):
     lib = load()
     M, K = _matrix("A", A)
     N = _matrix("W", W)[0]
-    code = _code("A", A.dtype)
-    for name, t, shape in (("A", A, A.shape), ("W", W, (N, K)), ("dout", dout, (M, N))):
-        _expect(name, t, shape, A.dtype, A.device)
-    with _Launch(A, stream) as la:
-        dA, dW = la.empty((M, K), A.dtype, needs[0]), la.empty((N, K), A.dtype, needs[1])
-        dbias = la.empty((N,), torch.float32, bias)
-        ws = la.workspace(lib.jepa_linear_bwd_workspace_bytes(M, N, K, code))
-        check(lib.jepa_linear_bwd(_ptr(dout), _ptr(A), _ptr(W), _ptr(dA), _ptr(dW), _ptr(dbias), M, N, K, code,
-                                  _ptr(ws), ws.numel(), la.handle))
-    return dA, dW, dbias
+    dt, dev = A.dtype, A.device
+    code = _code("A", dt)
+    _expect("A", A, (M, K), dt, dev)
+    _expect("W", W, (N, K), dt, dev)
+    _expect("dout", dout, (M, N), dt, dev)
+
+    def body(dev, handle):
+        d, a, w = _a16(dout), _a16(A), _a16(W)
+        dA = _empty((M, K), dtype=dt, device=dev) if needs[0] else None
+        dW = _empty((N, K), dtype=dt, device=dev) if needs[1] else None
+        db = _empty(N, dtype=_f32, device=dev) if bias else None
+        n = _workspace_bytes("jepa_linear_bwd_workspace_bytes", M, N, K, code)
+        ws = _empty(n, dtype=torch.uint8, device=dev) if n else None
+        check(lib.jepa_linear_bwd(_p(d), _p(a), _p(w), _p(dA), _p(dW), _p(db), M, N, K, code, _p(ws), n, handle))
+        return dA, dW, db
+    return _run(A, stream, body)
