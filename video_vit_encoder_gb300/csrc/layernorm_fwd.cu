@@ -12,55 +12,27 @@ namespace {
 
 constexpr int kBlock = 256;
 
-template <typename TX, typename TY, int V, int NV, int TPR, bool SHIFT>
+// Rows that are multiples of their vector: a warp a row, or a block.
+template <typename TX, typename TY, int V, int NV, int TPR>
 __global__ void __launch_bounds__(kBlock) ln_fwd_kernel(const TX* __restrict__ x, const float* __restrict__ w,
                                                         const float* __restrict__ b, TY* __restrict__ y,
                                                         float* __restrict__ mean, float* __restrict__ rstd, long rows,
                                                         int dim, float eps) {
   __shared__ float red[kBlock / 32];
-  extern __shared__ __align__(16) float table[];   // SHIFT: w, then b, in the threads' columns: [NV * V / 4][thread] float4
   constexpr int kRows = kBlock / TPR;   // rows a block works on at a time
-  constexpr int kTable = NV * V * kBlock;
-  const int tid = threadIdx.x, t = tid % TPR;
-  const long first = (long)blockIdx.x * kRows + tid / TPR;
+  const int t = threadIdx.x % TPR;
   const long stride = (long)gridDim.x * kRows;
-  const long total = rows * dim;
-  const int o = SHIFT ? (int)((first * dim) % V) : 0;
   const float inv = 1.0f / (float)dim;
-  if constexpr (SHIFT) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int c = (t + i * TPR) * V - o + j;
-        const int k = ((i * V + j) / 4 * kBlock + tid) * 4 + j % 4;
-        table[k] = c >= 0 && c < dim ? __ldg(w + c) : 0.f;
-        table[kTable + k] = c >= 0 && c < dim ? __ldg(b + c) : 0.f;
-      }
-  }
-  for (long row = first; row < rows; row += stride) {
+  for (long row = (long)blockIdx.x * kRows + threadIdx.x / TPR; row < rows; row += stride) {
+    const TX* xr = x + row * dim;
     float v[NV][V];
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c0 = (t + i * TPR) * V - o;
-      const long at = row * dim + c0;
+      const int c = (t + i * TPR) * V;
 #pragma unroll
       for (int j = 0; j < V; ++j) v[i][j] = 0.f;
-      if (c0 < dim) {
-        if (!SHIFT || at + V <= total) {
-          ln_load<TX, V>(x + at, v[i]);
-        } else {   // the last row's last vector ends with the operand
-#pragma unroll
-          for (int j = 0; j < V; ++j)
-            if (at + j < total) v[i][j] = DT<TX>::to(x[at + j]);
-        }
-        if (SHIFT && !ln_whole<V>(c0, dim)) {   // the neighbouring rows' values
-#pragma unroll
-          for (int j = 0; j < V; ++j)
-            if (c0 + j < 0 || c0 + j >= dim) v[i][j] = 0.f;
-        }
-      }
+      if (c < dim) ln_load<TX, V>(xr + c, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -70,20 +42,139 @@ __global__ void __launch_bounds__(kBlock) ln_fwd_kernel(const TX* __restrict__ x
     const float mu = s[0] * inv;
     float q[1] = {0.f};
 #pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((t + i * TPR) * V < dim) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          v[i][j] -= mu;
+          q[0] = fmaf(v[i][j], v[i][j], q[0]);
+        }
+      }
+    ln_row_sum<TPR, 1>(q, red);
+    const float rs = 1.0f / sqrtf(q[0] * inv + eps);
+    if (t == 0) {
+      if (mean != nullptr) mean[row] = mu;
+      if (rstd != nullptr) rstd[row] = rs;
+    }
+    TY* yr = y + row * dim;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (t + i * TPR) * V;
+      if (c < dim) {
+        float ww[V], bb[V], out[V];
+        ln_load<float, V>(w + c, ww);
+        ln_load<float, V>(b + c, bb);
+#pragma unroll
+        for (int j = 0; j < V; ++j) out[j] = v[i][j] * rs * ww[j] + bb[j];
+        ln_store<TY, V>(yr + c, out);
+      }
+    }
+  }
+}
+
+// Rows that start anywhere (SHIFT): one block of 16 warps per SM, rows through
+// an asynchronous ring as in the backward pass, w and b in the threads' columns
+// in shared memory.
+constexpr int kShiftThreads = 512;
+constexpr int kMostSmem = 232448;
+template <typename TX, int V, int NV, int TPR>
+struct ShiftShape {
+  static constexpr int kRows = kShiftThreads / TPR;
+  using Table = LnTable<V, NV, TPR, kRows>;
+  static constexpr int kRowVec = NV * V * sizeof(TX);
+  static constexpr size_t kHead = 32 * sizeof(float);
+  static constexpr int kFit = (int)((kMostSmem - kHead - 2 * Table::kBytes) / (kShiftThreads * kRowVec));
+  static constexpr int kDepth = kFit > 4 ? 4 : kFit;
+  static_assert(kDepth >= 1, "a row must fit");
+  static constexpr size_t kRing = (size_t)kDepth * kShiftThreads * kRowVec;
+  static constexpr size_t kSmem = kHead + kRing + 2 * Table::kBytes;
+};
+
+template <typename TX, typename TY, int V, int NV, int TPR>
+__global__ void __launch_bounds__(kShiftThreads, 1)
+    ln_fwd_shift_kernel(const TX* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b,
+                        TY* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, long rows, int dim,
+                        float eps) {
+  using S = ShiftShape<TX, V, NV, TPR>;
+  constexpr int kBX = V * sizeof(TX);
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* red = reinterpret_cast<float*>(smem);
+  uint8_t* ring = smem + S::kHead;
+  float* tw = reinterpret_cast<float*>(ring + S::kRing);
+  float* tb = tw + S::Table::kBytes / sizeof(float);
+  const int tid = threadIdx.x, t = tid % TPR;
+  const long first = (long)blockIdx.x * S::kRows + tid / TPR;
+  const long stride = (long)gridDim.x * S::kRows;
+  const int o = (int)((first * dim) % V);
+  const int head = t == 0 ? o : 0;   // elements of this thread's vector 0 that are the previous row's
+  const float inv = 1.0f / (float)dim;
+  S::Table::fill(tw, w, dim, o);
+  S::Table::fill(tb, b, dim, o);
+  __syncthreads();
+  auto fetch = [&](long row, int d) {
+    if (row < rows) {
+      uint8_t* slot = ring + (size_t)d * kShiftThreads * S::kRowVec;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c0 = (t + i * TPR) * V - o;
+        if (c0 < dim)   // the last vector ends with the row (zeros follow)
+          ln_copy_async<kBX>(slot + (size_t)(i * kShiftThreads + tid) * kBX, x + row * dim + c0,
+                             min(V, dim - c0) * (int)sizeof(TX));
+      }
+    }
+    ln_copy_commit();
+  };
+#pragma unroll
+  for (int d = 0; d < S::kDepth; ++d) fetch(first + d * stride, d);
+  int d = 0;
+  for (long row = first; row < rows; row += stride) {
+    ln_copy_wait<S::kDepth - 1>();
+    const uint8_t* slot = ring + (size_t)d * kShiftThreads * S::kRowVec;
+    float v[NV][V];
+    float sa[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c0 = (t + i * TPR) * V - o;
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[i][j] = 0.f;
+      if (c0 < dim) {
+        ln_load<TX, V>(reinterpret_cast<const TX*>(slot + (size_t)(i * kShiftThreads + tid) * kBX), v[i]);
+        if (i == 0) {
+#pragma unroll
+          for (int j = 0; j < V - 1; ++j) v[i][j] = j < head ? 0.f : v[i][j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < V; j += 2) add2f(sa[0], sa[1], v[i][j], v[i][j + 1]);
+    }
+    fetch(row + S::kDepth * stride, d);   // the slot has been read
+    if (++d == S::kDepth) d = 0;
+    float s[1] = {sa[0] + sa[1]};
+    ln_row_sum<TPR, 1>(s, red);
+    const float mu = s[0] * inv;
+    float qa[2] = {0.f, 0.f};
+#pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c0 = (t + i * TPR) * V - o;
       if (c0 < dim) {
+        float dv[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[i][j] -= mu;
-        if (SHIFT && !ln_whole<V>(c0, dim)) {
+        for (int j = 0; j < V; j += 2) add2f(v[i][j], v[i][j + 1], -mu, -mu);
 #pragma unroll
-          for (int j = 0; j < V; ++j)
-            if (c0 + j < 0 || c0 + j >= dim) v[i][j] = 0.f;
+        for (int j = 0; j < V; ++j) dv[j] = v[i][j];
+        if (c0 + V > dim) {   // zeros that follow the row
+#pragma unroll
+          for (int j = 1; j < V; ++j) dv[j] = c0 + j < dim ? dv[j] : 0.f;
+        }
+        if (i == 0) {
+#pragma unroll
+          for (int j = 0; j < V - 1; ++j) dv[j] = j < head ? 0.f : dv[j];
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j) q[0] = fmaf(v[i][j], v[i][j], q[0]);
+        for (int j = 0; j < V; j += 2) ln_fma2(qa[0], qa[1], dv[j], dv[j + 1], dv[j], dv[j + 1]);
       }
     }
+    float q[1] = {qa[0] + qa[1]};
     ln_row_sum<TPR, 1>(q, red);
     const float rs = 1.0f / sqrtf(q[0] * inv + eps);
     if (t == 0) {
@@ -95,26 +186,19 @@ __global__ void __launch_bounds__(kBlock) ln_fwd_kernel(const TX* __restrict__ x
     for (int i = 0; i < NV; ++i) {
       const int c0 = (t + i * TPR) * V - o;
       if (c0 < dim) {
-        float ww[V], bb[V], out[V];
-        if constexpr (SHIFT) {
+        float ww[V], out[V];
+        S::Table::load(tw, i, ww);
+        S::Table::load(tb, i, out);
 #pragma unroll
-          for (int j = 0; j < V; j += 4) {
-            const float4 qw = *reinterpret_cast<const float4*>(table + ((i * V + j) / 4 * kBlock + tid) * 4);
-            const float4 qb = *reinterpret_cast<const float4*>(table + kTable + ((i * V + j) / 4 * kBlock + tid) * 4);
-            ww[j] = qw.x; ww[j + 1] = qw.y; ww[j + 2] = qw.z; ww[j + 3] = qw.w;
-            bb[j] = qb.x; bb[j + 1] = qb.y; bb[j + 2] = qb.z; bb[j + 3] = qb.w;
-          }
-        } else {
-          ln_load<float, V>(w + c0, ww);
-          ln_load<float, V>(b + c0, bb);
+        for (int j = 0; j < V; j += 2) {
+          ln_mul2(v[i][j], v[i][j + 1], rs, rs);
+          ln_fma2(out[j], out[j + 1], v[i][j], v[i][j + 1], ww[j], ww[j + 1]);
         }
-#pragma unroll
-        for (int j = 0; j < V; ++j) out[j] = v[i][j] * rs * ww[j] + bb[j];
-        if constexpr (SHIFT) ln_store_part<TY, V>(yr, c0, dim, out);
-        else ln_store<TY, V>(yr + c0, out);
+        ln_store_part<TY, V>(yr, c0, dim, out);
       }
     }
   }
+  ln_copy_wait<0>();
 }
 
 // Rows wider than a block's registers, and operands that do not start on their
@@ -155,33 +239,48 @@ int blocks_of(long rows, int per_row) {
   return (int)(need < kMostBlocks ? need : kMostBlocks);
 }
 
-template <typename TX, typename TY, int V, int NV, int TPR, bool SHIFT>
-cudaError_t launch_rows(const TX* x, const float* w, const float* b, TY* y, float* mean, float* rstd, long rows,
-                        int dim, float eps, cudaStream_t s) {
-  auto kern = ln_fwd_kernel<TX, TY, V, NV, TPR, SHIFT>;
-  constexpr size_t kSmem = SHIFT ? sizeof(float) * 2 * NV * V * kBlock : 0;
-  if constexpr (kSmem > 48 * 1024) {
-    static DeviceOnce setup;
-    const cudaError_t e = setup.run([&](int) {
-      return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    });
-    if (e != cudaSuccess) return e;
-  }
-  // a thread's rows have to be a multiple of V apart where its columns depend on them: 8 rows a block, or
-  // a full grid of one-row blocks (a multiple of 8), or one row a block
-  kern<<<blocks_of(rows, kBlock / TPR), kBlock, kSmem, s>>>(x, w, b, y, mean, rstd, rows, dim, eps);
+template <typename TX, typename TY, int V>
+cudaError_t fwd_rows(const TX* x, const float* w, const float* b, TY* y, float* mean, float* rstd, long rows, int dim,
+                     float eps, cudaStream_t s) {
+#define JEPA_LN_FWD(NVE, TPR)                                                                                   \
+  ln_fwd_kernel<TX, TY, V, (NVE) / V, TPR><<<blocks_of(rows, kBlock / TPR), kBlock, 0, s>>>(x, w, b, y, mean, rstd, \
+                                                                                            rows, dim, eps)
+  if (dim <= 256) JEPA_LN_FWD(8, 32);
+  else if (dim <= 512) JEPA_LN_FWD(16, 32);
+  else if (dim <= 1024) JEPA_LN_FWD(32, 32);
+  else if (dim <= 2048) JEPA_LN_FWD(32, 64);
+  else if (dim <= 4096) JEPA_LN_FWD(32, 128);
+  else JEPA_LN_FWD(32, 256);
+#undef JEPA_LN_FWD
   return cudaGetLastError();
 }
 
-template <typename TX, typename TY, int V, bool SHIFT>
-cudaError_t fwd_v(const TX* x, const float* w, const float* b, TY* y, float* mean, float* rstd, long rows, int dim,
-                  float eps, cudaStream_t s) {
-  const int n = dim + (SHIFT ? V - 1 : 0);   // columns that the vectors cover
-  if (n <= 256) return launch_rows<TX, TY, V, 8 / V, 32, SHIFT>(x, w, b, y, mean, rstd, rows, dim, eps, s);
-  if (n <= 512) return launch_rows<TX, TY, V, 16 / V, 32, SHIFT>(x, w, b, y, mean, rstd, rows, dim, eps, s);
-  if (n <= 1024) return launch_rows<TX, TY, V, 32 / V, 32, SHIFT>(x, w, b, y, mean, rstd, rows, dim, eps, s);
-  if (n <= 4096) return launch_rows<TX, TY, V, 16 / V, 256, SHIFT>(x, w, b, y, mean, rstd, rows, dim, eps, s);
-  return launch_rows<TX, TY, V, 32 / V, 256, SHIFT>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+template <typename TX, typename TY, int V, int NV, int TPR>
+cudaError_t launch_shift(const TX* x, const float* w, const float* b, TY* y, float* mean, float* rstd, long rows,
+                         int dim, float eps, cudaStream_t s) {
+  using S = ShiftShape<TX, V, NV, TPR>;
+  auto kern = ln_fwd_shift_kernel<TX, TY, V, NV, TPR>;
+  static DeviceOnce setup;
+  const cudaError_t e = setup.run([&](int) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  // a thread's rows are a multiple of 8 apart (152 blocks), or it has one row
+  const long need = (rows + S::kRows - 1) / S::kRows;
+  kern<<<(int)(need < 152 ? need : 152), kShiftThreads, S::kSmem, s>>>(x, w, b, y, mean, rstd, rows, dim, eps);
+  return cudaGetLastError();
+}
+
+template <typename TX, typename TY, int V>
+cudaError_t fwd_shift(const TX* x, const float* w, const float* b, TY* y, float* mean, float* rstd, long rows, int dim,
+                      float eps, cudaStream_t s) {
+  const int n = dim + V - 1;   // columns that the vectors cover
+  if (n <= 256) return launch_shift<TX, TY, V, 8 / V, 32>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+  if (n <= 512) return launch_shift<TX, TY, V, 16 / V, 32>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+  if (n <= 1024) return launch_shift<TX, TY, V, 32 / V, 32>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+  if (n <= 2048) return launch_shift<TX, TY, V, 32 / V, 64>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+  if (n <= 4096) return launch_shift<TX, TY, V, 32 / V, 128>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+  return launch_shift<TX, TY, V, 32 / V, 256>(x, w, b, y, mean, rstd, rows, dim, eps, s);
 }
 
 constexpr int kLongest = 8192;   // columns that a block's registers hold
@@ -194,8 +293,8 @@ cudaError_t fwd_t(const void* x_, const float* w, const float* b, void* y_, floa
   TY* y = static_cast<TY*>(y_);
   const bool vec = ln_aligned(x, V * sizeof(TX)) && ln_aligned(y, V * sizeof(TY));
   if (vec && dim % V == 0 && dim <= kLongest && ln_aligned(w, 16) && ln_aligned(b, 16))
-    return fwd_v<TX, TY, V, false>(x, w, b, y, mean, rstd, rows, dim, eps, s);
-  if (vec && dim + V - 1 <= kLongest) return fwd_v<TX, TY, V, true>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+    return fwd_rows<TX, TY, V>(x, w, b, y, mean, rstd, rows, dim, eps, s);
+  if (vec && dim + V - 1 <= kLongest) return fwd_shift<TX, TY, V>(x, w, b, y, mean, rstd, rows, dim, eps, s);
   ln_fwd_wide_kernel<TX, TY><<<blocks_of(rows, 1), kBlock, 0, s>>>(x, w, b, y, mean, rstd, rows, dim, eps);
   return cudaGetLastError();
 }

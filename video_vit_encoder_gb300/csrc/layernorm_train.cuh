@@ -1,15 +1,15 @@
 // Row access shared by the layer norm's forward and backward kernels.
 //
-// A row of `dim` values is held in registers by TPR threads (one warp, or a
-// whole block), each owning NV vectors of V consecutive columns (16 bytes of
-// the widest operand).  Where dim is a multiple of V, vector i of thread t
-// starts at column (t + i * TPR) * V.  Where it is not, rows start at any
-// element, so the vectors are laid on the aligned memory under the row: they
-// start at column (t + i * TPR) * V - o with o = (row * dim) mod V, and the
-// first and last one share their memory with the neighbouring rows.  A
-// thread's rows are a multiple of V apart, so o, and with it the columns a
-// thread owns, are the same for all its rows.  Operands that do not start on
-// their vector take V = 1.
+// A row of `dim` values is the work of TPR threads (one warp to a block), each
+// owning NV vectors of V consecutive columns (16 bytes of the widest operand).
+// Where dim is a multiple of V, vector i of thread t starts at column
+// (t + i * TPR) * V.  Where it is not (SHIFT), rows start at any element, so
+// the vectors are laid on the aligned memory under the row: they start at
+// column (t + i * TPR) * V - o with o = (row * dim) mod V, and the first and
+// last one share their memory with the neighbouring rows.  A thread's rows are
+// a multiple of V apart, so o, and with it the columns a thread owns, are the
+// same for all its rows.  Operands that do not start on their vector, and rows
+// of more than 8192 columns, have kernels of their own.
 #pragma once
 #include "train.h"
 
@@ -60,6 +60,23 @@ __device__ __forceinline__ void ln_store(T* p, const float (&v)[V]) {
   }
 }
 
+// Packed arithmetic on two neighbouring values: (a, b) *= (x, y), (a, b) += (x, y) (p, q).
+__device__ __forceinline__ void ln_mul2(float& a, float& b, float x, float y) {
+  uint64_t v, k;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(k) : "f"(x), "f"(y));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(k));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ void ln_fma2(float& a, float& b, float x, float y, float p, float q) {
+  uint64_t v, k, l;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(k) : "f"(x), "f"(y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(l) : "f"(p), "f"(q));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(v) : "l"(k), "l"(l));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+
 __device__ __forceinline__ float ln_warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -67,21 +84,22 @@ __device__ __forceinline__ float ln_warp_sum(float v) {
 }
 
 // Sums of N values over the TPR threads of a row; every thread gets them.
-// With TPR > 32 the row is the block's: red holds N x (TPR / 32) floats and
-// every thread of the block calls this.
+// With TPR > 32 red holds N x (TPR / 32) floats for each group of TPR threads
+// of the block, and the group's warps meet at a barrier of their own.
 template <int TPR, int N>
 __device__ __forceinline__ void ln_row_sum(float (&v)[N], float* red) {
 #pragma unroll
   for (int j = 0; j < N; ++j) v[j] = ln_warp_sum(v[j]);
   if constexpr (TPR > 32) {
     constexpr int W = TPR / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __syncthreads();   // the previous sum has been read
+    const int group = threadIdx.x / TPR, warp = (threadIdx.x % TPR) >> 5, lane = threadIdx.x & 31;
+    red += group * N * W;
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");   // the previous sum has been read
     if (lane == 0) {
 #pragma unroll
       for (int j = 0; j < N; ++j) red[j * W + warp] = v[j];
     }
-    __syncthreads();
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       float s = 0.f;
@@ -107,6 +125,36 @@ template <int N>
 __device__ __forceinline__ void ln_copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+
+// A vector of float parameters per column, in the columns that a thread's
+// vectors cover, shared by the groups of a block whose o is the same (they are
+// V apart): [class][NV * V / 4][thread of the row] float4.
+template <int V, int NV, int TPR, int GROUPS>
+struct LnTable {
+  static constexpr int kClasses = GROUPS < V ? GROUPS : V;
+  static constexpr size_t kBytes = sizeof(float) * kClasses * TPR * NV * V;
+  // Filled by the first groups of the block; the block meets before it is read.
+  static __device__ __forceinline__ void fill(float* table, const float* src, int dim, int o) {
+    const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
+    if (g < kClasses) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int c = (t + i * TPR) * V - o + j;
+          table[((g * (NV * V / 4) + (i * V + j) / 4) * TPR + t) * 4 + j % 4] = c >= 0 && c < dim ? __ldg(src + c) : 0.f;
+        }
+    }
+  }
+  static __device__ __forceinline__ void load(const float* table, int i, float (&v)[V]) {
+    const int g = threadIdx.x / TPR % kClasses, t = threadIdx.x % TPR;
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(table + ((g * (NV * V / 4) + (i * V + j) / 4) * TPR + t) * 4);
+      v[j] = q.x; v[j + 1] = q.y; v[j + 2] = q.z; v[j + 3] = q.w;
+    }
+  }
+};
 
 // Whether a vector whose first column is c0 lies inside the row as a whole.
 template <int V>

@@ -11,9 +11,20 @@ namespace jepa {
 cudaError_t layernorm_fwd(int x_dtype, int y_dtype, const void* x, const float* w, const float* b, void* y, float* mean,
                           float* rstd, long rows, int dim, float eps, cudaStream_t s);
 size_t layernorm_bwd_workspace(long rows, int dim);
-cudaError_t layernorm_bwd(int x_dtype, int y_dtype, const void* dy, const void* x, const float* w, const float* mean,
-                          const float* rstd, const void* res, void* dx, float* dw, float* db, long rows, int dim,
-                          float* ws, cudaStream_t s);
+struct LnBwdArgs {
+  const void *dy, *x, *res;       // res or null
+  const float *w, *mean, *rstd;
+  void* dx;
+  float *dw, *db, *ws;            // dw, db or null
+  long rows;
+  int dim;
+};
+cudaError_t layernorm_bwd(int x_dtype, int y_dtype, const LnBwdArgs& a, cudaStream_t s);
+cudaError_t layernorm_bwd_f32(const LnBwdArgs& a, cudaStream_t s);
+cudaError_t layernorm_bwd_f32_f16(const LnBwdArgs& a, cudaStream_t s);
+cudaError_t layernorm_bwd_f32_bf16(const LnBwdArgs& a, cudaStream_t s);
+cudaError_t layernorm_bwd_f16(const LnBwdArgs& a, cudaStream_t s);
+cudaError_t layernorm_bwd_bf16(const LnBwdArgs& a, cudaStream_t s);
 
 // ----------------------------------------------------------------------------- operators (train_ops.cu)
 enum GateAct : int { ACT_SILU = 0, ACT_GELU = 1 };

@@ -114,9 +114,8 @@ jepa_status jepa_layernorm_bwd(const void* dy, const void* x, const float* w, co
       misaligned(mean, 4) || misaligned(rstd, 4) || misaligned(dw, 4) || misaligned(db, 4))
     return api_fail(JEPA_ERR_ARG, "a buffer is not aligned to its element");
   ARG_TRY(check_ws(workspace, workspace_bytes, layernorm_bwd_workspace(rows, dim)));
-  return cuda_result(layernorm_bwd(x_dtype, y_dtype, dy, x, w, mean, rstd, residual, dx, dw, db, rows, dim,
-                                   (float*)workspace, (cudaStream_t)stream),
-                     "layernorm_bwd");
+  const LnBwdArgs a{dy, x, residual, w, mean, rstd, dx, dw, db, (float*)workspace, rows, dim};
+  return cuda_result(layernorm_bwd(x_dtype, y_dtype, a, (cudaStream_t)stream), "layernorm_bwd");
 }
 
 // ============================================================================= softmax cross entropy
