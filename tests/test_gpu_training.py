@@ -134,7 +134,8 @@ def test_layernorm_nan_row_stays_in_its_row(jg):
 
 # ----------------------------------------------------------------------------- softmax cross entropy
 CE_SHAPES = [(1, 8, 1, 0), (1, 64, 2, 0), (8, 1024, 174, 0), (129, 72, 257, 0), (300, 768, 1000, 0), (257, 65, 513, 0),
-             (64, 128, 4097, 0), (33, 40, 30, 1), (600, 64, 300, 0), (5, 8, 9000, 0)]
+             (64, 128, 4097, 0), (33, 40, 30, 1), (600, 64, 300, 0), (5, 8, 9000, 0), (16, 200, 5000, 0), (9, 1032, 40, 0),
+             (17, 512, 300, 0)]
 
 
 def _ce_case(M, D, V, dtype, shift, key, ignore=0.2):
@@ -262,7 +263,8 @@ def test_linear_ce_nan_rows(jg, dtype, D):
 
 # ----------------------------------------------------------------------------- gated feed-forward
 FFN_SHAPES = [(1, 64, 8, 0), (1, 8, 1, 0), (8, 1024, 256, 0), (129, 72, 136, 0), (300, 256, 520, 0), (257, 128, 1000, 0),
-              (5, 33, 17, 0), (200, 65, 300, 0), (40, 64, 64, 1), (700, 128, 256, 0)]
+              (5, 33, 17, 0), (200, 65, 300, 0), (40, 64, 64, 1), (700, 128, 256, 0), (16, 200, 72, 0), (12, 1032, 520, 0),
+              (17, 512, 77, 0), (2, 4, 3, 0)]
 
 
 def _ffn_case(M, D, F, dtype, shift, bias, key):

@@ -60,6 +60,13 @@ cudaError_t gated_ffn_fwd(const FfnArgs& a, void* h, void* ws, cudaStream_t s);
 cudaError_t gated_ffn_bwd(const FfnArgs& a, const void* dh, void* dx, void* dwg, void* dwu, float* dbg, float* dbu,
                           void* ws, cudaStream_t s);
 
+// The forward passes for a few rows (few_rows.cu): at most 16, of 16-byte pieces.
+bool few_rows_ok(int dtype, int M, int D);
+cudaError_t few_rows_gate(const FfnArgs& a, void* h, cudaStream_t s);
+// Statistics of each row in parts [few_rows_ce_parts(V)][M], as the tiles leave them.
+int few_rows_ce_parts(int V);
+cudaError_t few_rows_ce(const CeArgs& a, float2* ms, float* sums, float* zy, cudaStream_t s);
+
 size_t linear_bwd_workspace(int M, int N, int K, int dtype);
 cudaError_t linear_bwd(int dtype, const void* dout, const void* A, const void* W, void* dA, void* dW, float* dbias,
                        int M, int N, int K, void* ws, int* status, int num_sms, cudaStream_t s);

@@ -409,8 +409,9 @@ cudaError_t zero(void* p, size_t bytes, cudaStream_t s) {
 }
 
 // ----------------------------------------------------------------------------- softmax cross entropy
-// Joins the (max, sum of 2^(z - max)) of a row's parts; 32 rows a block, the
-// block's 8 warps take every eighth part.
+// Joins the (max, sum of 2^(z - max)) of a row's parts, in a fixed order: a
+// block takes 32 rows, its 8 warps every eighth part each, or with ONE a single
+// row, its threads every 256th part each (many parts of few rows).
 struct Ms {
   float m, s, sum;
 };
@@ -421,6 +422,7 @@ __device__ __forceinline__ void ms_join(Ms& a, float m, float s, float sum) {
   a.m = mm;
   a.sum += sum;
 }
+template <bool ONE>
 __global__ void __launch_bounds__(kBlock) ce_join_kernel(const float2* __restrict__ ms, const float* __restrict__ sums,
                                                          const float* __restrict__ zy, int parts, int M, int V,
                                                          const int64_t* __restrict__ labels, long ignore_index,
@@ -428,18 +430,25 @@ __global__ void __launch_bounds__(kBlock) ce_join_kernel(const float2* __restric
                                                          float* __restrict__ lse_out, int* status) {
   __shared__ Ms sm[8][33];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int row = blockIdx.x * 32 + lane;
+  const int row = ONE ? (int)blockIdx.x : (int)blockIdx.x * 32 + lane;
   Ms a{-INFINITY, 0.f, 0.f};
   if (row < M) {
 #pragma unroll 4
-    for (int k = g; k < parts; k += 8) {
+    for (int k = ONE ? threadIdx.x : g; k < parts; k += ONE ? kBlock : 8) {
       const float2 q = __ldg(ms + (size_t)k * M + row);
       ms_join(a, q.x, q.y, sums != nullptr ? __ldg(sums + (size_t)k * M + row) : 0.f);
     }
   }
+  if constexpr (ONE) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float m = __shfl_xor_sync(0xffffffffu, a.m, o), v = __shfl_xor_sync(0xffffffffu, a.s, o);
+      ms_join(a, m, v, __shfl_xor_sync(0xffffffffu, a.sum, o));
+    }
+  }
   sm[g][lane] = a;
   __syncthreads();
-  if (g != 0 || row >= M) return;
+  if (g != 0 || row >= M || (ONE && lane != 0)) return;
   for (int k = 1; k < 8; ++k) ms_join(a, sm[k][lane].m, sm[k][lane].s, sm[k][lane].sum);
   // lse = ln(2^m s)
   const float lse = (a.m + log2f(a.s)) * 0.69314718055994531f;
@@ -456,6 +465,16 @@ __global__ void __launch_bounds__(kBlock) ce_join_kernel(const float2* __restric
   }
   if (loss != nullptr) loss[row] = l;
   lse_out[row] = lse;
+}
+cudaError_t ce_join(const CeArgs& a, const float2* ms, const float* sums, const float* zy, int parts, float* loss,
+                    float* lse, cudaStream_t s) {
+  if (a.M <= 16)
+    ce_join_kernel<true><<<a.M, kBlock, 0, s>>>(ms, sums, zy, parts, a.M, a.V, a.labels, a.ignore_index, a.smoothing,
+                                                loss, lse, a.status);
+  else
+    ce_join_kernel<false><<<blocks_for(a.M, 32), kBlock, 0, s>>>(ms, sums, zy, parts, a.M, a.V, a.labels,
+                                                                 a.ignore_index, a.smoothing, loss, lse, a.status);
+  return cudaGetLastError();
 }
 
 // What dz is held in units of: scale[0] = max |dloss| (1 if that is 0 or not
@@ -497,10 +516,14 @@ struct CeFwd {
 CeFwd ce_fwd_layout(const CeArgs& a, void* ws) {
   Carver cv{static_cast<uint8_t*>(ws)};
   CeFwd l;
-  l.x = operand(a.dtype, a.x, a.M, a.D, cv);
-  l.w = operand(a.dtype, a.w, a.V, a.D, cv);
-  l.run = ce_run(a.M, a.V);
-  l.parts = 2 * ceil_div(ceil_div(a.V, 256), l.run);
+  if (few_rows_ok(a.dtype, a.M, a.D)) {
+    l.parts = few_rows_ce_parts(a.V);
+  } else {
+    l.x = operand(a.dtype, a.x, a.M, a.D, cv);
+    l.w = operand(a.dtype, a.w, a.V, a.D, cv);
+    l.run = ce_run(a.M, a.V);
+    l.parts = 2 * ceil_div(ceil_div(a.V, 256), l.run);
+  }
   const size_t n = (size_t)l.parts * a.M;
   l.ms = cv.take<float2>(n * 8);
   l.sums = a.smoothing > 0.f ? cv.take<float>(n * 4) : nullptr;
@@ -557,6 +580,10 @@ size_t linear_ce_workspace(int M, int D, int V, int dtype, bool backward) {
 cudaError_t linear_ce_fwd(const CeArgs& a, float* loss, float* lse, void* ws, cudaStream_t s) {
   if (a.M == 0) return cudaSuccess;
   const CeFwd l = ce_fwd_layout(a, ws);
+  if (few_rows_ok(a.dtype, a.M, a.D)) {
+    JEPA_TRY_CUDA(few_rows_ce(a, l.ms, l.sums, l.zy, s));
+    return ce_join(a, l.ms, l.sums, l.zy, l.parts, loss, lse, s);
+  }
   JEPA_TRY_CUDA(fill(a.dtype, a.x, l.x, s));
   JEPA_TRY_CUDA(fill(a.dtype, a.w, l.w, s));
   Params p = base_params(a.M, a.V, tg::kBN, a.status);
@@ -574,9 +601,7 @@ cudaError_t linear_ce_fwd(const CeArgs& a, float* loss, float* lse, void* ws, cu
   p.ep.part_sum = l.sums;
   p.ep.zy = l.zy;
   JEPA_TRY_CUDA(gemm(a.dtype, false, false, tg::CE_FWD, p, a.num_sms, s));
-  ce_join_kernel<<<blocks_for(a.M, 32), kBlock, 0, s>>>(l.ms, l.sums, l.zy, l.parts, a.M, a.V, a.labels, a.ignore_index,
-                                                        a.smoothing, loss, lse, a.status);
-  return cudaGetLastError();
+  return ce_join(a, l.ms, l.sums, l.zy, l.parts, loss, lse, s);
 }
 
 cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss, void* dx, void* dw, float* dbias,
@@ -735,12 +760,14 @@ size_t gated_ffn_workspace(int M, int D, int F, int dtype, bool backward) {
   a.F = F;
   a.dtype = dtype;
   if (backward) return ffn_bwd_layout(a, nullptr).bytes;
+  if (few_rows_ok(dtype, M, D)) return 0;
   Carver cv{nullptr};
   return ffn_fwd_layout(a, cv).bytes;
 }
 
 cudaError_t gated_ffn_fwd(const FfnArgs& a, void* h, void* ws, cudaStream_t s) {
   if (a.M == 0) return cudaSuccess;
+  if (few_rows_ok(a.dtype, a.M, a.D)) return few_rows_gate(a, h, s);
   Carver cv{static_cast<uint8_t*>(ws)};
   const FfnFwd l = ffn_fwd_layout(a, cv);
   Params p;

@@ -13,6 +13,7 @@ not asked for (``needs``) are returned as None.
 """
 from __future__ import annotations
 
+import contextlib
 import functools
 
 import torch
@@ -26,7 +27,7 @@ _CODE = {torch.float32: DTYPE_CODE["f32"], torch.float16: DTYPE_CODE["f16"], tor
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 _empty = torch.empty
-_f32 = torch.float32
+_f32, _u8 = torch.float32, torch.uint8
 _ACT = {"silu": _lib.GATE_SILU, "gelu": _lib.GATE_GELU}
 
 
@@ -63,7 +64,7 @@ def _p(t):
 def _a16(t):
     """The matrix, or a copy of one that does not start on 16 bytes (a view
     into another tensor can start anywhere)."""
-    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 @functools.lru_cache(maxsize=4096)
@@ -71,52 +72,49 @@ def _workspace_bytes(query, *sizes):
     return getattr(load(), query)(*sizes)
 
 
-def _run(t, stream, body):
-    """body(device, stream handle) with t's device and the stream current, so
-    that what it allocates belongs to the stream that uses it."""
-    index = t.get_device()
-    if index < 0:
+@contextlib.contextmanager
+def _place(t, stream):
+    """t's device and the stream current, so that what a call allocates
+    belongs to the stream that uses it."""
+    if t.get_device() < 0:
         raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
-    if stream is None:
-        if index == torch.cuda.current_device():
-            return body(t.device, _raw_stream(index))
-        with torch.cuda.device(index):
-            return body(t.device, _raw_stream(index))
-    if stream.device != t.device:
+    if stream is not None and stream.device != t.device:
         raise ValueError(f"stream is on {stream.device}, tensors are on {t.device}")
-    with torch.cuda.device(index), torch.cuda.stream(stream):
-        return body(t.device, stream.cuda_stream)
+    with torch.cuda.device(t.device), torch.cuda.stream(stream):
+        yield
+
+
+def _elsewhere(t, stream):
+    """Whether a call on t has to be made under _place (which refuses CPU tensors)."""
+    index = t.get_device()
+    return stream is not None or index < 0 or index != torch.cuda.current_device()
 
 
 def layernorm_fwd(x, w, b, eps, out_dtype=None, stream=None):
     """(y, mean, rstd) of x [..., dim] over its last dimension; w, b float
     [dim].  y has out_dtype (default x's; another one needs float32 x), mean
     and rstd are float32 of x's leading shape."""
-    lib = load()
-    shape, dt = x.shape, x.dtype
-    dim = shape[-1]
+    shape, dt, dev = x.shape, x.dtype, x.device
+    dim, lead = shape[-1], shape[:-1]
     out_dtype = out_dtype or dt
     xc, yc = _code("x", dt), _code("out_dtype", out_dtype)
-    dev = x.device
     _expect("x", x, shape, dt, dev)
     _expect("w", w, (dim,), _f32, dev)
     _expect("b", b, (dim,), _f32, dev)
-
-    def body(dev, handle):
-        lead = shape[:-1]
-        rows = lead.numel()
-        y = _empty(shape, dtype=out_dtype, device=dev)
-        mean, rstd = _empty(lead, dtype=_f32, device=dev), _empty(lead, dtype=_f32, device=dev)
-        check(lib.jepa_layernorm_fwd(_p(x), _p(w), _p(b), _p(y), _p(mean), _p(rstd), rows, dim, xc, yc, eps, handle))
-        return y, mean, rstd
-    return _run(x, stream, body)
+    if _elsewhere(x, stream):
+        with _place(x, stream):
+            return layernorm_fwd(x, w, b, eps, out_dtype)
+    y = _empty(shape, dtype=out_dtype, device=dev)
+    mean, rstd = _empty(lead, dtype=_f32, device=dev), _empty(lead, dtype=_f32, device=dev)
+    check(load().jepa_layernorm_fwd(x.data_ptr(), w.data_ptr(), b.data_ptr(), y.data_ptr(), mean.data_ptr(),
+                                    rstd.data_ptr(), lead.numel(), dim, xc, yc, eps, _raw_stream(dev.index)))
+    return y, mean, rstd
 
 
 def layernorm_bwd(dy, x, w, mean, rstd, residual=None, needs=(True, True), stream=None):
     """(dx, dw, db) from dy (y's shape and dtype), x, w and the forward pass's
     mean and rstd.  residual: x's shape and dtype, added to dx.  needs: (dw,
     db)."""
-    lib = load()
     shape, dt, dev = x.shape, x.dtype, x.device
     dim, lead = shape[-1], shape[:-1]
     xc, yc = _code("x", dt), _code("dy", dy.dtype)
@@ -126,18 +124,19 @@ def layernorm_bwd(dy, x, w, mean, rstd, residual=None, needs=(True, True), strea
     _expect("mean", mean, lead, _f32, dev)
     _expect("rstd", rstd, lead, _f32, dev)
     _expect("residual", residual, shape, dt, dev)
-
-    def body(dev, handle):
-        rows = lead.numel()
-        dx = _empty(shape, dtype=dt, device=dev)
-        dw = _empty(dim, dtype=_f32, device=dev) if needs[0] else None
-        db = _empty(dim, dtype=_f32, device=dev) if needs[1] else None
-        n = _workspace_bytes("jepa_layernorm_bwd_workspace_bytes", rows, dim)
-        ws = _empty(n, dtype=torch.uint8, device=dev)
-        check(lib.jepa_layernorm_bwd(_p(dy), _p(x), _p(w), _p(mean), _p(rstd), _p(residual), _p(dx), _p(dw), _p(db),
-                                     rows, dim, xc, yc, _p(ws), n, handle))
-        return dx, dw, db
-    return _run(x, stream, body)
+    if _elsewhere(x, stream):
+        with _place(x, stream):
+            return layernorm_bwd(dy, x, w, mean, rstd, residual, needs)
+    rows = lead.numel()
+    dx = _empty(shape, dtype=dt, device=dev)
+    dw = _empty(dim, dtype=_f32, device=dev) if needs[0] else None
+    db = _empty(dim, dtype=_f32, device=dev) if needs[1] else None
+    n = _workspace_bytes("jepa_layernorm_bwd_workspace_bytes", rows, dim)
+    ws = _empty(n, dtype=_u8, device=dev)
+    check(load().jepa_layernorm_bwd(dy.data_ptr(), x.data_ptr(), w.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                    _p(residual), dx.data_ptr(), _p(dw), _p(db), rows, dim, xc, yc, ws.data_ptr(), n,
+                                    _raw_stream(dev.index)))
+    return dx, dw, db
 
 
 def _ce_args(x, W, bias, labels):
@@ -158,18 +157,19 @@ def linear_ce_fwd(x, W, bias, labels, ignore_index=-100, smoothing=0.0, stream=N
     """(loss, lse), float [M], of the classifier x W^T + bias: x [M, D], W
     [V, D] in one dtype, bias float [V] or None, labels int64 (or int32) [M].
     Rows with label ignore_index have loss 0."""
-    lib = load()
     M, D, V, code = _ce_args(x, W, bias, labels)
-
-    def body(dev, handle):
-        lab, xx, ww = labels.long(), _a16(x), _a16(W)
-        loss, lse = _empty(M, dtype=_f32, device=dev), _empty(M, dtype=_f32, device=dev)
-        n = _workspace_bytes("jepa_linear_ce_workspace_bytes", M, D, V, code, 0)
-        ws = _empty(n, dtype=torch.uint8, device=dev)
-        check(lib.jepa_linear_ce_fwd(_p(xx), _p(ww), _p(bias), _p(lab), _p(loss), _p(lse), M, D, V, code, ignore_index,
-                                     smoothing, _p(ws), n, handle))
-        return loss, lse
-    return _run(x, stream, body)
+    if _elsewhere(x, stream):
+        with _place(x, stream):
+            return linear_ce_fwd(x, W, bias, labels, ignore_index, smoothing)
+    dev = x.device
+    lab, x, W = labels.long(), _a16(x), _a16(W)
+    loss, lse = _empty(M, dtype=_f32, device=dev), _empty(M, dtype=_f32, device=dev)
+    n = _workspace_bytes("jepa_linear_ce_workspace_bytes", M, D, V, code, 0)
+    ws = _empty(n, dtype=_u8, device=dev)
+    check(load().jepa_linear_ce_fwd(x.data_ptr(), W.data_ptr(), _p(bias), lab.data_ptr(), loss.data_ptr(),
+                                    lse.data_ptr(), M, D, V, code, ignore_index, smoothing, ws.data_ptr(), n,
+                                    _raw_stream(dev.index)))
+    return loss, lse
 
 
 def linear_ce_bwd(dloss, x, W, bias, labels, lse, ignore_index=-100, smoothing=0.0, needs=(True, True, True),
@@ -177,26 +177,27 @@ def linear_ce_bwd(dloss, x, W, bias, labels, lse, ignore_index=-100, smoothing=0
     """(dx, dW, dbias) from dloss, the gradient of each row's loss (float [M],
     or one number for all rows: 1 / n for the mean of n rows), and the forward
     pass's lse.  needs: (dx, dW, dbias)."""
-    lib = load()
     M, D, V, code = _ce_args(x, W, bias, labels)
     _expect("lse", lse, (M,), _f32, x.device)
-
-    def body(dev, handle):
-        lab, dl, dt, xx, ww = labels.long(), dloss, x.dtype, _a16(x), _a16(W)
-        if not torch.is_tensor(dl):
-            dl = torch.full((M,), float(dl), device=dev)
-        elif dl.dim() == 0:
-            dl = dl.to(device=dev, dtype=_f32).expand(M).contiguous()
-        _expect("dloss", dl, (M,), _f32, dev)
-        dx = _empty((M, D), dtype=dt, device=dev) if needs[0] else None
-        dW = _empty((V, D), dtype=dt, device=dev) if needs[1] else None
-        db = _empty(V, dtype=_f32, device=dev) if needs[2] else None
-        n = _workspace_bytes("jepa_linear_ce_workspace_bytes", M, D, V, code, 1)
-        ws = _empty(n, dtype=torch.uint8, device=dev)
-        check(lib.jepa_linear_ce_bwd(_p(xx), _p(ww), _p(bias), _p(lab), _p(lse), _p(dl), _p(dx), _p(dW), _p(db), M, D, V,
-                                     code, ignore_index, smoothing, _p(ws), n, handle))
-        return dx, dW, db
-    return _run(x, stream, body)
+    if _elsewhere(x, stream):
+        with _place(x, stream):
+            return linear_ce_bwd(dloss, x, W, bias, labels, lse, ignore_index, smoothing, needs)
+    dt, dev = x.dtype, x.device
+    if not torch.is_tensor(dloss):
+        dloss = torch.full((M,), float(dloss), device=dev)
+    elif dloss.dim() == 0:
+        dloss = dloss.to(device=dev, dtype=_f32).expand(M).contiguous()
+    _expect("dloss", dloss, (M,), _f32, dev)
+    lab, x, W = labels.long(), _a16(x), _a16(W)
+    dx = _empty((M, D), dtype=dt, device=dev) if needs[0] else None
+    dW = _empty((V, D), dtype=dt, device=dev) if needs[1] else None
+    db = _empty(V, dtype=_f32, device=dev) if needs[2] else None
+    n = _workspace_bytes("jepa_linear_ce_workspace_bytes", M, D, V, code, 1)
+    ws = _empty(n, dtype=_u8, device=dev)
+    check(load().jepa_linear_ce_bwd(x.data_ptr(), W.data_ptr(), _p(bias), lab.data_ptr(), lse.data_ptr(),
+                                    dloss.data_ptr(), _p(dx), _p(dW), _p(db), M, D, V, code, ignore_index, smoothing,
+                                    ws.data_ptr(), n, _raw_stream(dev.index)))
+    return dx, dW, db
 
 
 def _ffn_args(x, Wg, Wu, bg, bu, act):
@@ -217,46 +218,47 @@ def _ffn_args(x, Wg, Wu, bg, bu, act):
 def gated_ffn_fwd(x, Wg, Wu, bg=None, bu=None, act="silu", stream=None):
     """h = act(x Wg^T + bg) * (x Wu^T + bu), [M, F] in x's dtype: x [M, D],
     Wg, Wu [F, D]; bg, bu float [F] or None; act 'silu' or 'gelu' (erf)."""
-    lib = load()
     M, D, F, code, a = _ffn_args(x, Wg, Wu, bg, bu, act)
-
-    def body(dev, handle):
-        xx, wg, wu = _a16(x), _a16(Wg), _a16(Wu)
-        h = _empty((M, F), dtype=x.dtype, device=dev)
-        n = _workspace_bytes("jepa_gated_ffn_workspace_bytes", M, D, F, code, 0)
-        ws = _empty(n, dtype=torch.uint8, device=dev) if n else None
-        check(lib.jepa_gated_ffn_fwd(_p(xx), _p(wg), _p(wu), _p(bg), _p(bu), _p(h), M, D, F, code, a, _p(ws), n, handle))
-        return h
-    return _run(x, stream, body)
+    if _elsewhere(x, stream):
+        with _place(x, stream):
+            return gated_ffn_fwd(x, Wg, Wu, bg, bu, act)
+    dev = x.device
+    x, Wg, Wu = _a16(x), _a16(Wg), _a16(Wu)
+    h = _empty((M, F), dtype=x.dtype, device=dev)
+    n = _workspace_bytes("jepa_gated_ffn_workspace_bytes", M, D, F, code, 0)
+    ws = _empty(n, dtype=_u8, device=dev) if n else None
+    check(load().jepa_gated_ffn_fwd(x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), _p(bg), _p(bu), h.data_ptr(), M, D, F,
+                                    code, a, _p(ws), n, _raw_stream(dev.index)))
+    return h
 
 
 def gated_ffn_bwd(dh, x, Wg, Wu, bg=None, bu=None, act="silu", needs=(True, True, True, True, True), stream=None):
     """(dx, dWg, dWu, dbg, dbu) from dh [M, F]; the projections are computed
     again from x.  needs: one flag for each."""
-    lib = load()
     M, D, F, code, a = _ffn_args(x, Wg, Wu, bg, bu, act)
     _expect("dh", dh, (M, F), x.dtype, x.device)
-
-    def body(dev, handle):
-        dt, d, xx, wg, wu = x.dtype, _a16(dh), _a16(x), _a16(Wg), _a16(Wu)
-        dx = _empty((M, D), dtype=dt, device=dev) if needs[0] else None
-        dWg = _empty((F, D), dtype=dt, device=dev) if needs[1] else None
-        dWu = _empty((F, D), dtype=dt, device=dev) if needs[2] else None
-        dbg = _empty(F, dtype=_f32, device=dev) if needs[3] else None
-        dbu = _empty(F, dtype=_f32, device=dev) if needs[4] else None
-        n = _workspace_bytes("jepa_gated_ffn_workspace_bytes", M, D, F, code, 1)
-        ws = _empty(n, dtype=torch.uint8, device=dev)
-        check(lib.jepa_gated_ffn_bwd(_p(d), _p(xx), _p(wg), _p(wu), _p(bg), _p(bu), _p(dx), _p(dWg), _p(dWu), _p(dbg),
-                                     _p(dbu), M, D, F, code, a, _p(ws), n, handle))
-        return dx, dWg, dWu, dbg, dbu
-    return _run(x, stream, body)
+    if _elsewhere(x, stream):
+        with _place(x, stream):
+            return gated_ffn_bwd(dh, x, Wg, Wu, bg, bu, act, needs)
+    dt, dev = x.dtype, x.device
+    dh, x, Wg, Wu = _a16(dh), _a16(x), _a16(Wg), _a16(Wu)
+    dx = _empty((M, D), dtype=dt, device=dev) if needs[0] else None
+    dWg = _empty((F, D), dtype=dt, device=dev) if needs[1] else None
+    dWu = _empty((F, D), dtype=dt, device=dev) if needs[2] else None
+    dbg = _empty(F, dtype=_f32, device=dev) if needs[3] else None
+    dbu = _empty(F, dtype=_f32, device=dev) if needs[4] else None
+    n = _workspace_bytes("jepa_gated_ffn_workspace_bytes", M, D, F, code, 1)
+    ws = _empty(n, dtype=_u8, device=dev)
+    check(load().jepa_gated_ffn_bwd(dh.data_ptr(), x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), _p(bg), _p(bu), _p(dx),
+                                    _p(dWg), _p(dWu), _p(dbg), _p(dbu), M, D, F, code, a, ws.data_ptr(), n,
+                                    _raw_stream(dev.index)))
+    return dx, dWg, dWu, dbg, dbu
 
 
 def linear_bwd(dout, A, W, bias=True, needs=(True, True), stream=None):
     """(dA, dW, dbias) of out = A W^T + bias from dout [M, N]: A [M, K], W
     [N, K] and dout in one dtype.  needs: (dA, dW); bias: whether dbias (float
     [N]) is wanted."""
-    lib = load()
     M, K = _matrix("A", A)
     N = _matrix("W", W)[0]
     dt, dev = A.dtype, A.device
@@ -264,14 +266,15 @@ def linear_bwd(dout, A, W, bias=True, needs=(True, True), stream=None):
     _expect("A", A, (M, K), dt, dev)
     _expect("W", W, (N, K), dt, dev)
     _expect("dout", dout, (M, N), dt, dev)
-
-    def body(dev, handle):
-        d, a, w = _a16(dout), _a16(A), _a16(W)
-        dA = _empty((M, K), dtype=dt, device=dev) if needs[0] else None
-        dW = _empty((N, K), dtype=dt, device=dev) if needs[1] else None
-        db = _empty(N, dtype=_f32, device=dev) if bias else None
-        n = _workspace_bytes("jepa_linear_bwd_workspace_bytes", M, N, K, code)
-        ws = _empty(n, dtype=torch.uint8, device=dev) if n else None
-        check(lib.jepa_linear_bwd(_p(d), _p(a), _p(w), _p(dA), _p(dW), _p(db), M, N, K, code, _p(ws), n, handle))
-        return dA, dW, db
-    return _run(A, stream, body)
+    if _elsewhere(A, stream):
+        with _place(A, stream):
+            return linear_bwd(dout, A, W, bias, needs)
+    dout, A, W = _a16(dout), _a16(A), _a16(W)
+    dA = _empty((M, K), dtype=dt, device=dev) if needs[0] else None
+    dW = _empty((N, K), dtype=dt, device=dev) if needs[1] else None
+    db = _empty(N, dtype=_f32, device=dev) if bias else None
+    n = _workspace_bytes("jepa_linear_bwd_workspace_bytes", M, N, K, code)
+    ws = _empty(n, dtype=_u8, device=dev) if n else None
+    check(load().jepa_linear_bwd(dout.data_ptr(), A.data_ptr(), W.data_ptr(), _p(dA), _p(dW), _p(db), M, N, K, code,
+                                 _p(ws), n, _raw_stream(dev.index)))
+    return dA, dW, db
