@@ -23,10 +23,12 @@
 // first, whose steps then truncate a small accumulator.
 //
 // Work units are runs of tiles: the cross entropy carries its row statistics
-// over a run of column tiles, everything else has runs of one.  K may consist
-// of two segments with their own operands (dx = dg Wg + du Wu is one product),
-// and may be split between units, each writing its own fp32 slab, which a
-// second kernel adds in a fixed order.
+// over a run of column tiles, everything else has runs of one.  The reducing
+// products of a backward pass (dx and dW) are two jobs of one launch, so that
+// the units of one fill the last round of the other.  K may consist of two
+// segments with their own operands (dx = dg Wg + du Wu is one product), and may
+// be split between units, each writing its own fp32 slab, which a second kernel
+// adds in a fixed order.
 //
 // Warp roles: warp 0 loads, warp 1 issues the MMAs (the even CTA's, for the
 // pair), eight warps run the epilogue, two per 32 TMEM lanes, each half the
@@ -58,17 +60,19 @@ constexpr size_t kSmemBytes = 1024 + kBarOffset + 256;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 enum Epi : int {
+  REDUCE = 0,    // C per job: see Out
+  CE_FWD = 1,    // row statistics of z = acc + bias
+  CE_BWD = 2,    // dz (T, or planes) from z = acc + bias
+  GATE_FWD = 3,  // h (T, or fp32); columns 0-127 of the tile are gates, 128-255 the same columns' ups
+  GATE_BWD = 4   // dg, du (T, or planes)
+};
+enum Out : int {
   STORE = 0,     // C (T) = acc * scale
   F32 = 1,       // slab, or C in fp32 = acc
-  F32_ADD = 2,   // slab, or C in fp32 += acc
-  CE_FWD = 3,    // row statistics of z = acc + bias
-  CE_BWD = 4,    // dz (T, or planes) from z = acc + bias
-  GATE_FWD = 5,  // h (T, or fp32); columns 0-127 of the tile are gates, 128-255 the same columns' ups
-  GATE_BWD = 6   // dg, du (T, or planes)
+  F32_ADD = 2    // slab, or C in fp32 += acc
 };
 
 struct EpiArgs {
-  const float* scale;      // STORE: factor on the device, or null
   const float* bias;       // CE: [N], GATE: gate's [N]
   const float* bias2;      // GATE: up's [N]
   // cross entropy (columns are v0 .. v0 + N of V)
@@ -90,47 +94,89 @@ struct EpiArgs {
   int act;
 };
 
-struct Params {
-  CUtensorMap a[2], b[2], c[2];
+// One product, or nz products that share B.
+struct Job {
+  CUtensorMap a[2], b[2], c[2];   // a[segment + z], b[segment] (gates: gate, up), c[z]
   int M, N;              // extents of the output
   int num_m, num_n;      // pair tiles
-  int run;               // column tiles per unit
   int kb_seg, nseg;      // K blocks per segment, segments
-  int nz;                // products that share B (a[z], c[z])
+  int nz;
   int splits, kb_split;  // K splits, blocks per split
+  int a_plane, b_plane;  // SPLIT: rows from one plane to the next
+  int a_mn;              // REDUCE: A is MN-major (B always is); else both are K-major
+  int out;               // REDUCE
+  int slab_rows;         // REDUCE: rows of a slab
+  const float* scale;    // REDUCE, STORE: factor on the device, or null
+};
+
+struct Params {
+  Job j[2];
+  int units[2];          // of each job
+  int extra;             // units of job 1 that a pair takes while others do their last of job 0
+  int run;               // column tiles per unit
   int kb_chunk;          // blocks accumulated in tensor memory before the epilogue takes them
-  int a_plane, b_plane, c_plane;  // SPLIT: rows from one plane to the next
-  int slab_rows;         // rows of a slab (F32, F32_ADD)
+  int c_plane;           // SPLIT: rows from one plane of C to the next
   void* plain;           // C where TMA cannot store it (rows not multiples of 16 bytes), else null
   long plain_ld;
   EpiArgs ep;
   int* status;
 };
 
+// The units of one CTA pair.  Job 0 has the longer units and goes first, round
+// robin; in its last, partial round the pairs without a unit of it take `extra`
+// units of job 1 each; what is left of job 1 goes round robin, beginning with
+// those pairs.
+struct Walk {
+  int cid, nc, full, part;   // pair, pairs, whole rounds of job 0, pairs in its last one
+  __device__ __forceinline__ Walk(const Params& p, int cid_, int nc_) : cid(cid_), nc(nc_) {
+    full = p.units[0] / nc;
+    part = p.units[0] - full * nc;
+  }
+  // The i-th unit, counted over both jobs, or -1.
+  __device__ __forceinline__ int at(const Params& p, int i) const {
+    if (i < full || (i == full && cid < part)) return i * nc + cid;
+    if (p.units[1] == 0) return -1;
+    i -= full + (cid < part ? 1 : 0);
+    int base = 0;
+    if (part != 0) {
+      base = min(p.units[1], (nc - part) * p.extra);
+      if (cid >= part) {
+        if (i < p.extra) {
+          const int k = cid - part + i * (nc - part);
+          return k < p.units[1] ? p.units[0] + k : -1;
+        }
+        i -= p.extra;
+      }
+    }
+    const int k = base + i * nc + (cid >= part ? cid - part : cid - part + nc);
+    return k < p.units[1] ? p.units[0] + k : -1;
+  }
+};
+
 // One unit: row tile m, columns tiles n0 .. n0 + nr, product z, K blocks kb0 .. kb1.
 struct Unit {
-  int m, n0, nr, run_index, z, split, kb0, kb1;
+  int job, m, n0, nr, run_index, z, split, kb0, kb1;
 };
-__host__ __device__ __forceinline__ int unit_count(const Params& p) {
-  return p.num_m * ((p.num_n + p.run - 1) / p.run) * p.nz * p.splits;
-}
 __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
   Unit t;
-  const int runs = (p.num_n + p.run - 1) / p.run;
-  const int tiles = p.num_m * runs;
+  t.job = u >= p.units[0] ? 1 : 0;
+  if (t.job) u -= p.units[0];
+  const Job& j = p.j[t.job];
+  const int runs = (j.num_n + p.run - 1) / p.run;
+  const int tiles = j.num_m * runs;
   const int q = u / tiles;
   const int r = u - q * tiles;
-  t.split = q / p.nz;
-  t.z = q - t.split * p.nz;
+  t.split = q / j.nz;
+  t.z = q - t.split * j.nz;
   const int group = kGroupM * runs;
   const int gi = r / group, w = r - gi * group;
-  const int gm = min(p.num_m - gi * kGroupM, kGroupM);
+  const int gm = min(j.num_m - gi * kGroupM, kGroupM);
   t.run_index = w / gm;
   t.m = gi * kGroupM + (w - t.run_index * gm);
   t.n0 = t.run_index * p.run;
-  t.nr = min(p.run, p.num_n - t.n0);
-  t.kb0 = t.split * p.kb_split;
-  t.kb1 = min(t.kb0 + p.kb_split, p.kb_seg * p.nseg);
+  t.nr = min(p.run, j.num_n - t.n0);
+  t.kb0 = t.split * j.kb_split;
+  t.kb1 = min(t.kb0 + j.kb_split, j.kb_seg * j.nseg);
   return t;
 }
 
@@ -338,22 +384,22 @@ __device__ __forceinline__ void ce_fwd_tile(const Params& p, float (&v)[128], in
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const int col = col0 + c * 32;
-    if (col >= p.N) continue;
+    if (col >= p.j[0].N) continue;
     float* w = v + c * 32;
     if (ep.bias != nullptr) {
-      add_bias(ep.bias, col, p.N, -INFINITY, w);
-    } else if (col + 32 > p.N) {
+      add_bias(ep.bias, col, p.j[0].N, -INFINITY, w);
+    } else if (col + 32 > p.j[0].N) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) w[j] = col + j < p.N ? w[j] : -INFINITY;
+      for (int j = 0; j < 32; ++j) w[j] = col + j < p.j[0].N ? w[j] : -INFINITY;
     }
     if constexpr (SUM) {
       float s = 0.f;
-      if (col + 32 <= p.N) {
+      if (col + 32 <= p.j[0].N) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) s += w[j];
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s += col + j < p.N ? w[j] : 0.f;
+        for (int j = 0; j < 32; ++j) s += col + j < p.j[0].N ? w[j] : 0.f;
       }
       st.sum += s;
     }
@@ -389,7 +435,7 @@ template <bool SPLIT>
 __device__ __forceinline__ RowGrad ce_bwd_row(const Params& p, int row, bool report) {
   const EpiArgs& ep = p.ep;
   RowGrad r{false, -1, 0.f, 0.f};
-  if (row < p.M) {
+  if (row < p.j[0].M) {
     const long y = __ldg(reinterpret_cast<const long long*>(ep.labels) + row);
     const float lse = __ldg(ep.lse + row), dl = __ldg(ep.dloss + row);
     r.part = y != ep.ignore_index && y >= 0 && y < ep.V;
@@ -422,9 +468,9 @@ __device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], co
   for (int c = 0; c < 4; ++c) {
     const int cc = col0 + c * 32;
     float* w = v + c * 32;
-    if (cc >= p.N) continue;
+    if (cc >= p.j[0].N) continue;
     // columns past N keep finite values: nothing reads them
-    if (ep.bias != nullptr) add_bias(ep.bias, cc, p.N, 0.f, w);
+    if (ep.bias != nullptr) add_bias(ep.bias, cc, p.j[0].N, 0.f, w);
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
       fma2(w[j], w[j + 1], kLog2e, -l2);
@@ -452,14 +498,14 @@ __device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], co
     if (lane == 0) bulk_wait_read_all();
     __syncwarp();
     float* to = ep.col_part + (size_t)(y >> 5) * ep.ld_col + col0;
-    const int n = y < p.M ? p.N - col0 : 0;
+    const int n = y < p.j[0].M ? p.j[0].N - col0 : 0;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      if (col0 + c * 32 < p.N) col_sum32(v + c * 32, buf, lane, to + c * 32, n - c * 32);
+      if (col0 + c * 32 < p.j[0].N) col_sum32(v + c * 32, buf, lane, to + c * 32, n - c * 32);
   }
 #pragma unroll
   for (int c = 0; c < 2; ++c)
-    if (col0 + c * 64 < p.N) emit_operand<T, SPLIT>(p, &p.c[0], v, c * 64, buf, lane, col0 + c * 64, y);
+    if (col0 + c * 64 < p.j[0].N) emit_operand<T, SPLIT>(p, &p.j[0].c[0], v, c * 64, buf, lane, col0 + c * 64, y);
 }
 
 // Copies this warp's 32 x 64 block of dh into the staging buffer (swizzled as
@@ -473,8 +519,8 @@ __device__ __forceinline__ void fetch_dh(const Params& p, uint8_t* buf, int lane
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = i * 4 + (lane >> 3);
-    const bool in = row0 + r < p.M && col + 8 * k < p.N;
-    const T* src = static_cast<const T*>(p.ep.dh) + (in ? (size_t)(row0 + r) * p.N + col + 8 * k : 0);
+    const bool in = row0 + r < p.j[0].M && col + 8 * k < p.j[0].N;
+    const T* src = static_cast<const T*>(p.ep.dh) + (in ? (size_t)(row0 + r) * p.j[0].N + col + 8 * k : 0);
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(buf + r * 128 + ((k ^ (r & 7)) << 4))),
                  "l"(src), "r"(in ? 16 : 0)
                  : "memory");
@@ -491,14 +537,14 @@ __device__ __forceinline__ void gate_tile(const Params& p, float (&v)[128], int 
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();
   }
-  if (col >= p.N) return;
+  if (col >= p.j[0].N) return;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int cc = col + h * 32;
     float* g = v + h * 32;
     float* u = v + 64 + h * 32;
-    if (ep.bias != nullptr) add_bias(ep.bias, cc, p.N, 0.f, g);
-    if (ep.bias2 != nullptr) add_bias(ep.bias2, cc, p.N, 0.f, u);
+    if (ep.bias != nullptr) add_bias(ep.bias, cc, p.j[0].N, 0.f, g);
+    if (ep.bias2 != nullptr) add_bias(ep.bias2, cc, p.j[0].N, 0.f, u);
     if constexpr (!BWD) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
@@ -508,7 +554,7 @@ __device__ __forceinline__ void gate_tile(const Params& p, float (&v)[128], int 
       }
     } else {
       constexpr int kPer = 16 / sizeof(TD);   // values of dh in 16 bytes
-      const TD* dh = static_cast<const TD*>(ep.dh) + (size_t)row * p.N + cc;
+      const TD* dh = static_cast<const TD*>(ep.dh) + (size_t)row * p.j[0].N + cc;
 #pragma unroll
       for (int j = 0; j < 32; j += kPer) {
         TD d[kPer];
@@ -517,11 +563,11 @@ __device__ __forceinline__ void gate_tile(const Params& p, float (&v)[128], int 
           if constexpr (!SPLIT)   // fetch_dh has put it into the staging buffer
             q = *reinterpret_cast<const uint4*>(buf + lane * 128 + (((h * 4 + j / 8) ^ (lane & 7)) << 4));
           else   // rows are multiples of 16 bytes: a piece is inside or outside as a whole
-            q = row < p.M && cc + j < p.N ? __ldg(reinterpret_cast<const uint4*>(dh + j)) : make_uint4(0, 0, 0, 0);
+            q = row < p.j[0].M && cc + j < p.j[0].N ? __ldg(reinterpret_cast<const uint4*>(dh + j)) : make_uint4(0, 0, 0, 0);
           memcpy(d, &q, 16);
         } else {
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) d[i] = row < p.M && cc + j + i < p.N ? dh[j + i] : DT<TD>::from(0.f);
+          for (int i = 0; i < kPer; ++i) d[i] = row < p.j[0].M && cc + j + i < p.j[0].N ? dh[j + i] : DT<TD>::from(0.f);
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -545,20 +591,20 @@ __device__ __forceinline__ void gate_tile(const Params& p, float (&v)[128], int 
         float* part = k == 0 ? ep.col_part : ep.col_part2;
         if (part == nullptr) continue;
         float* to = part + (size_t)(y >> 5) * ep.ld_col + col;
-        const int n = y < p.M ? p.N - col : 0;
+        const int n = y < p.j[0].M ? p.j[0].N - col : 0;
         col_sum32(v + k * 64, buf, lane, to, n);
         col_sum32(v + k * 64 + 32, buf, lane, to + 32, n - 32);
       }
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) emit_operand<T, SPLIT>(p, &p.c[k], v, k * 64, buf, lane, col, y);
+    for (int k = 0; k < 2; ++k) emit_operand<T, SPLIT>(p, &p.j[0].c[k], v, k * 64, buf, lane, col, y);
   } else if constexpr (!SPLIT) {
     auto put = [&](int k) {
       const float* q = v + 8 * k;
       return make_uint4(pack2<T>(q[0], q[1]), pack2<T>(q[2], q[3]), pack2<T>(q[4], q[5]), pack2<T>(q[6], q[7]));
     };
-    if (p.plain == nullptr) emit(&p.c[0], buf, lane, col, row - lane, false, put);
-    else emit_plain(static_cast<T*>(p.plain), p.plain_ld, p.M, p.N, buf, lane, col, row - lane, put);
+    if (p.plain == nullptr) emit(&p.j[0].c[0], buf, lane, col, row - lane, false, put);
+    else emit_plain(static_cast<T*>(p.plain), p.plain_ld, p.j[0].M, p.j[0].N, buf, lane, col, row - lane, put);
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -567,18 +613,18 @@ __device__ __forceinline__ void gate_tile(const Params& p, float (&v)[128], int 
         return make_uint4(__float_as_uint(q[0]), __float_as_uint(q[1]), __float_as_uint(q[2]), __float_as_uint(q[3]));
       };
       const int cc = col + h * 32;
-      if (cc >= p.N) break;
-      if (p.plain == nullptr) emit(&p.c[0], buf, lane, cc, row - lane, false, put);
-      else emit_plain(static_cast<float*>(p.plain), p.plain_ld, p.M, p.N, buf, lane, cc, row - lane, put);
+      if (cc >= p.j[0].N) break;
+      if (p.plain == nullptr) emit(&p.j[0].c[0], buf, lane, cc, row - lane, false, put);
+      else emit_plain(static_cast<float*>(p.plain), p.plain_ld, p.j[0].M, p.j[0].N, buf, lane, cc, row - lane, put);
     }
   }
 }
 
 // 128 columns of a 16-bit C straight from tensor memory.
 template <typename T>
-__device__ __forceinline__ void store_tile(const Params& p, const CUtensorMap* c, uint32_t taddr, int row0, int col0,
+__device__ __forceinline__ void store_tile(const Job& p, const CUtensorMap* c, uint32_t taddr, int row0, int col0,
                                            uint8_t* buf, int lane) {
-  const float sc = p.ep.scale != nullptr ? __ldg(p.ep.scale) : 1.0f;
+  const float sc = p.scale != nullptr ? __ldg(p.scale) : 1.0f;
 #pragma unroll 1
   for (int c0 = 0; c0 < kBN / 2; c0 += 64) {
     if (col0 + c0 >= p.N) break;
@@ -595,7 +641,7 @@ __device__ __forceinline__ void store_tile(const Params& p, const CUtensorMap* c
   }
 }
 // 128 columns of an fp32 C: straight from tensor memory, or the register sums.
-__device__ __forceinline__ void slab_tile(const Params& p, const CUtensorMap* c, uint32_t taddr, int row0, int col0,
+__device__ __forceinline__ void slab_tile(const Job& p, const CUtensorMap* c, uint32_t taddr, int row0, int col0,
                                           uint8_t* buf, int lane, bool add) {
 #pragma unroll 1
   for (int c0 = 0; c0 < kBN / 2; c0 += 32) {
@@ -607,7 +653,7 @@ __device__ __forceinline__ void slab_tile(const Params& p, const CUtensorMap* c,
          [&](int k) { return make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]); });
   }
 }
-__device__ __forceinline__ void slab_regs(const Params& p, const CUtensorMap* c, const float (&v)[128], int row0,
+__device__ __forceinline__ void slab_regs(const Job& p, const CUtensorMap* c, const float (&v)[128], int row0,
                                           int col0, uint8_t* buf, int lane, bool add) {
 #pragma unroll
   for (int c0 = 0; c0 < 128; c0 += 32) {
@@ -627,12 +673,12 @@ struct Shape {
   static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 };
 
-template <typename T, bool SPLIT, bool AMN, bool BMN, int EPI>
+template <typename T, bool SPLIT, int EPI>
 __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_kernel(const __grid_constant__ Params p) {
   constexpr bool kGate = EPI == GATE_FWD || EPI == GATE_BWD;
   constexpr int kPlanes = SPLIT ? 3 : 1;
   static_assert(kStages % kPlanes == 0, "the planes of a block take consecutive stages");
-  static_assert(!SPLIT || EPI != STORE, "a split product has fp32 results");
+  constexpr bool BMN = EPI == REDUCE;
   constexpr bool kRegs = Shape<SPLIT, EPI>::kRegs;
   constexpr int kFirstEpi = Shape<SPLIT, EPI>::kFirstEpi;
   constexpr bool kStageDh = EPI == GATE_BWD && !SPLIT;   // 64 columns of 16 bits are a row of the staging buffer
@@ -652,8 +698,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   const bool leader = rank == 0;
-  const int num_units = unit_count(p);
-  const int first = (int)cluster_id_x(), stride = (int)cluster_count_x();
+  const Walk walk(p, (int)cluster_id_x(), (int)cluster_count_x());
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -667,8 +712,8 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&p.a[0]);
-    tma_prefetch_desc(&p.b[0]);
+    tma_prefetch_desc(&p.j[0].a[0]);
+    tma_prefetch_desc(&p.j[0].b[0]);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -689,8 +734,10 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
         uint32_t phase = 0;
         long issued = 0;
         bool stop = false;
-        for (int u = first; u < num_units && !stop; u += stride) {
+        for (int i = 0, u; !stop && (u = walk.at(p, i)) >= 0; ++i) {
           const Unit t = unit_of(p, u);
+          const Job& job = p.j[t.job];
+          const bool amn = BMN && job.a_mn != 0;
           const int ra = (t.m * 2 + rank) * kBM;
           for (int r = 0; r < t.nr && !stop; ++r) {
             const int rb = kGate ? (t.n0 + r) * (kBN / 2) : (t.n0 + r) * kBN + rank * (kBN / 2);
@@ -702,17 +749,17 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
                 break;
               }
               const int kb = SPLIT ? q / 3 : q, plane = SPLIT ? q - 3 * kb : 0;
-              const int seg = kb >= p.kb_seg ? 1 : 0;
-              const int k = (kb - seg * p.kb_seg) * kBK;
-              const CUtensorMap* ma = &p.a[seg + t.z];
-              const CUtensorMap* mb = &p.b[kGate ? rank : seg];
+              const int seg = kb >= job.kb_seg ? 1 : 0;
+              const int k = (kb - seg * job.kb_seg) * kBK;
+              const CUtensorMap* ma = &job.a[seg + t.z];
+              const CUtensorMap* mb = &job.b[kGate ? rank : seg];
               if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
               const uint32_t bar = full0 + 8 * stage;
               uint8_t* da = sA + stage * kABytes;
               uint8_t* db = sB + stage * kBBytes;
               // the planes lie one after another along the stored matrix's rows
-              const int pa = plane * p.a_plane, pb = plane * p.b_plane;
-              if constexpr (AMN) {
+              const int pa = plane * job.a_plane, pb = plane * job.b_plane;
+              if (amn) {
                 tma_load_2d_pair(da, ma, bar, ra, k + pa);
                 tma_load_2d_pair(da + 8192, ma, bar, ra + 64, k + pa);
               } else {
@@ -748,14 +795,15 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer (the even CTA)
       if (leader) {
-        constexpr uint32_t idesc =
-            idesc_f16<T, 2 * kBM, kBN>() | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
         int stage = 0;
         uint32_t phase = 0;
         int acc = 0;
         bool ok = true;
-        for (int u = first; u < num_units && ok; u += stride) {
+        for (int i = 0, u; ok && (u = walk.at(p, i)) >= 0; ++i) {
           const Unit t = unit_of(p, u);
+          const bool amn = BMN && p.j[t.job].a_mn != 0;
+          const uint32_t idesc = idesc_f16<T, 2 * kBM, kBN>() | (amn ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
+          const uint32_t step = amn ? 128 : 2;   // 16 k on in A's descriptor
           for (int r = 0; r < t.nr && ok; ++r) {
             for (int c0 = t.kb0; c0 < t.kb1 && ok; c0 += p.kb_chunk, ++acc) {
               if (__any_sync(0xffffffffu, *abort_flag)) {
@@ -780,18 +828,18 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
 #pragma unroll
                 for (int pl = 0; pl < kPlanes; ++pl) {
                   const uint32_t aa = smem_u32(sA + (stage + pl) * kABytes), bb = smem_u32(sB + (stage + pl) * kBBytes);
-                  da[pl] = AMN ? smem_desc_mnmajor(aa) : smem_desc_kmajor<128>(aa);
+                  da[pl] = amn ? smem_desc_mnmajor(aa) : smem_desc_kmajor<128>(aa);
                   db[pl] = BMN ? smem_desc_mnmajor(bb) : smem_desc_kmajor<128>(bb);
                 }
                 // planes (i, j) with i + j = 2, then 1, then 0: the small products first
 #pragma unroll
                 for (int order = kPlanes - 1; order >= 0; --order)
 #pragma unroll
-                  for (int i = 0; i <= order; ++i)
+                  for (int pa = 0; pa <= order; ++pa)
 #pragma unroll
                     for (int k = 0; k < kBK / 16; ++k)
-                      umma_f16_ss_pair_warp(d, da[i] + k * (AMN ? 128 : 2), db[order - i] + k * (BMN ? 128 : 2), idesc,
-                                            kb != c0 || order != kPlanes - 1 || i != 0 || k != 0);
+                      umma_f16_ss_pair_warp(d, da[pa] + k * step, db[order - pa] + k * (BMN ? 128 : 2), idesc,
+                                            kb != c0 || order != kPlanes - 1 || pa != 0 || k != 0);
 #pragma unroll
                 for (int pl = 0; pl < kPlanes; ++pl) umma_commit_pair_warp(&empty[stage + pl], (uint16_t)0x3);
                 stage += kPlanes;
@@ -820,15 +868,16 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
     uint8_t* buf_s = sEpi + (warp - kFirstEpi) * kEpiStage;
     int acc = 0;
     bool stop = false;
-    for (int u = first; u < num_units && !stop; u += stride) {
+    for (int i = 0, u; !stop && (u = walk.at(p, i)) >= 0; ++i) {
       const Unit t = unit_of(p, u);
+      const Job& job = p.j[t.job];
       const int row = (t.m * 2 + rank) * kBM + quarter * 32 + lane;
       RowStats st{-INFINITY, 0.f, 0.f};
       RowGrad rg{};
       if constexpr (EPI == CE_BWD) rg = ce_bwd_row<SPLIT>(p, row, t.n0 == 0 && half == 0);
       int label = -1;
       if constexpr (EPI == CE_FWD) {
-        if (row < p.M) {
+        if (row < job.M) {
           const long y = p.ep.labels[row];
           label = y >= 0 && y < p.ep.V ? (int)y : -1;
         }
@@ -863,7 +912,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
         float warm = 0.f;
         if constexpr (EPI >= CE_FWD) {
           const int c = kGate ? (t.n0 + r) * (kBN / 2) + half * 64 + lane * 2 : col + lane * 4;
-          const int at = min(c, p.N - 1);
+          const int at = min(c, job.N - 1);
           if (p.ep.bias != nullptr) warm = __ldg(p.ep.bias + at);
           if (kGate && p.ep.bias2 != nullptr) warm += __ldg(p.ep.bias2 + at);
         }
@@ -909,11 +958,11 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
         } else {
           const int buf = acc & 1;
           const uint32_t tb = tl + buf * kBN;
-          if constexpr (EPI == STORE)
-            store_tile<T>(p, &p.c[t.z], tb + half * (kBN / 2), row - lane, col, buf_s, lane);
+          if (job.out == STORE)
+            store_tile<T>(job, &job.c[t.z], tb + half * (kBN / 2), row - lane, col, buf_s, lane);
           else
-            slab_tile(p, &p.c[t.z], tb + half * (kBN / 2), row - lane + t.split * p.slab_rows, col, buf_s, lane,
-                      EPI == F32_ADD);
+            slab_tile(job, &job.c[t.z], tb + half * (kBN / 2), row - lane + t.split * job.slab_rows, col, buf_s, lane,
+                      job.out == F32_ADD);
           chunk_taken(buf);
         }
         if constexpr (kRegs) {
@@ -928,13 +977,13 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
             if (p.ep.act == ACT_SILU) gate_tile<T, SPLIT, ACT_SILU, EPI == GATE_BWD>(p, v, row, oc, buf_s, lane);
             else gate_tile<T, SPLIT, ACT_GELU, EPI == GATE_BWD>(p, v, row, oc, buf_s, lane);
           } else {
-            slab_regs(p, &p.c[t.z], v, row - lane + t.split * p.slab_rows, col, buf_s, lane, EPI == F32_ADD);
+            slab_regs(job, &job.c[t.z], v, row - lane + t.split * job.slab_rows, col, buf_s, lane, job.out == F32_ADD);
           }
         }
       }
       if constexpr (EPI == CE_FWD) {
-        if (!stop && row < p.M) {
-          const size_t i = (size_t)(t.run_index * 2 + half) * p.M + row;
+        if (!stop && row < job.M) {
+          const size_t i = (size_t)(t.run_index * 2 + half) * job.M + row;
           p.ep.part_ms[i] = make_float2(st.m, st.s);
           if (p.ep.part_sum != nullptr) p.ep.part_sum[i] = st.sum;
         }
@@ -953,9 +1002,9 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
 }
 
 // Launches over the resident CTA pairs of the current device.
-template <typename T, bool SPLIT, bool AMN, bool BMN, int EPI>
+template <typename T, bool SPLIT, int EPI>
 cudaError_t launch(const Params& p, int num_sms, cudaStream_t s) {
-  auto kern = train_gemm_kernel<T, SPLIT, AMN, BMN, EPI>;
+  auto kern = train_gemm_kernel<T, SPLIT, EPI>;
   using S = Shape<SPLIT, EPI>;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(S::kThreads);
@@ -989,8 +1038,8 @@ cudaError_t launch(const Params& p, int num_sms, cudaStream_t s) {
     return cudaSuccess;
   }, &dev);
   if (e != cudaSuccess) return e;
-  const long units = (long)p.num_m * ((p.num_n + p.run - 1) / p.run) * p.nz * p.splits;
-  if (units < 1 || units > 0x7fffffffl - 4096) return cudaErrorInvalidValue;
+  const long units = (long)p.units[0] + p.units[1];
+  if (p.units[0] < 1 || p.units[1] < 0 || units > 0x7fffffffl - 4096) return cudaErrorInvalidValue;
   const int clusters = units < resident_on[dev] ? (int)units : resident_on[dev];
   cfg.gridDim = dim3(2 * clusters);
   return cudaLaunchKernelEx(&cfg, kern, p);
@@ -1000,26 +1049,18 @@ cudaError_t launch(const Params& p, int num_sms, cudaStream_t s) {
 }  // namespace jepa
 
 // The instantiations for one operand type; each has its own translation unit.
-#define JEPA_TRAIN_GEMM_INSTANCES(T, SPLIT, NAME)                                                           \
-  namespace jepa {                                                                                          \
-  namespace tg {                                                                                            \
-  cudaError_t NAME(bool amn, bool bmn, int epi, const Params& p, int num_sms, cudaStream_t s) {             \
-    if (!amn && !bmn) {                                                                                     \
-      if (epi == CE_FWD) return launch<T, SPLIT, false, false, CE_FWD>(p, num_sms, s);                      \
-      if (epi == CE_BWD) return launch<T, SPLIT, false, false, CE_BWD>(p, num_sms, s);                      \
-      if (epi == GATE_FWD) return launch<T, SPLIT, false, false, GATE_FWD>(p, num_sms, s);                  \
-      if (epi == GATE_BWD) return launch<T, SPLIT, false, false, GATE_BWD>(p, num_sms, s);                  \
-    } else if (!amn) {                                                                                      \
-      if constexpr (!SPLIT)                                                                                 \
-        if (epi == STORE) return launch<T, SPLIT, false, true, STORE>(p, num_sms, s);                       \
-      if (epi == F32) return launch<T, SPLIT, false, true, F32>(p, num_sms, s);                             \
-      if (epi == F32_ADD) return launch<T, SPLIT, false, true, F32_ADD>(p, num_sms, s);                     \
-    } else if (bmn) {                                                                                       \
-      if constexpr (!SPLIT)                                                                                 \
-        if (epi == STORE) return launch<T, SPLIT, true, true, STORE>(p, num_sms, s);                        \
-      if (epi == F32) return launch<T, SPLIT, true, true, F32>(p, num_sms, s);                              \
-    }                                                                                                       \
-    return cudaErrorInvalidValue;                                                                           \
-  }                                                                                                         \
-  }                                                                                                         \
+#define JEPA_TRAIN_GEMM_INSTANCES(T, SPLIT, NAME)                              \
+  namespace jepa {                                                             \
+  namespace tg {                                                               \
+  cudaError_t NAME(int epi, const Params& p, int num_sms, cudaStream_t s) {    \
+    switch (epi) {                                                             \
+      case REDUCE: return launch<T, SPLIT, REDUCE>(p, num_sms, s);             \
+      case CE_FWD: return launch<T, SPLIT, CE_FWD>(p, num_sms, s);             \
+      case CE_BWD: return launch<T, SPLIT, CE_BWD>(p, num_sms, s);             \
+      case GATE_FWD: return launch<T, SPLIT, GATE_FWD>(p, num_sms, s);         \
+      case GATE_BWD: return launch<T, SPLIT, GATE_BWD>(p, num_sms, s);         \
+    }                                                                          \
+    return cudaErrorInvalidValue;                                              \
+  }                                                                            \
+  }                                                                            \
   }

@@ -9,13 +9,14 @@
 namespace jepa {
 
 namespace tg {
-cudaError_t gemm_bf16(bool amn, bool bmn, int epi, const Params& p, int num_sms, cudaStream_t s);
-cudaError_t gemm_f16(bool amn, bool bmn, int epi, const Params& p, int num_sms, cudaStream_t s);
-cudaError_t gemm_f32(bool amn, bool bmn, int epi, const Params& p, int num_sms, cudaStream_t s);
+cudaError_t gemm_bf16(int epi, const Params& p, int num_sms, cudaStream_t s);
+cudaError_t gemm_f16(int epi, const Params& p, int num_sms, cudaStream_t s);
+cudaError_t gemm_f32(int epi, const Params& p, int num_sms, cudaStream_t s);
 }  // namespace tg
 
 namespace {
 
+using tg::Job;
 using tg::Params;
 
 constexpr int kBlock = 256;
@@ -167,46 +168,164 @@ cudaError_t fill(int dtype, const void* src, const Mat& m, cudaStream_t s) {
 }
 
 // ----------------------------------------------------------------------------- products
-Params base_params(long M, long N, int cols_per_tile, int* status) {
+Job base_job(long M, long N, int cols_per_tile) {
+  Job j{};
+  j.M = (int)M;
+  j.N = (int)N;
+  j.num_m = ceil_div(M, 2 * tg::kBM);
+  j.num_n = ceil_div(N, cols_per_tile);
+  j.nseg = j.nz = j.splits = 1;
+  return j;
+}
+void set_k(Job& j, long k_per_seg, int nseg, int splits) {
+  j.kb_seg = ceil_div(k_per_seg, tg::kBK);
+  j.nseg = nseg;
+  const int total = j.kb_seg * nseg;
+  j.kb_split = ceil_div(total, splits);
+  j.splits = ceil_div(total, j.kb_split);
+}
+// A launch of one K-major product (the cross entropy's and the gates').
+Params forward_params(const Job& j, int run, int* status) {
   Params p{};
-  p.M = (int)M;
-  p.N = (int)N;
-  p.num_m = ceil_div(M, 2 * tg::kBM);
-  p.num_n = ceil_div(N, cols_per_tile);
-  p.run = p.nseg = p.nz = p.splits = 1;
+  p.j[0] = j;
+  p.run = run;
+  const long units = (long)j.num_m * ceil_div(j.num_n, run);
+  p.units[0] = units > 0x7fffffffl ? -1 : (int)units;   // launch refuses what it cannot count
   p.kb_chunk = kWhole;
   p.status = status;
   return p;
 }
-void set_k(Params& p, long k_per_seg, int nseg, int splits) {
-  p.kb_seg = ceil_div(k_per_seg, tg::kBK);
-  p.nseg = nseg;
-  const int total = p.kb_seg * nseg;
-  p.kb_split = ceil_div(total, splits);
-  p.splits = ceil_div(total, p.kb_split);
-}
 
-// K splits of a product of nz outputs M x N over kb blocks, from the time of
-// the schedule: rounds of the 76 pairs, each a unit's blocks (0.27 us a block,
-// 6 times that for planes) plus about 1.6 us to fill and drain, and, when
-// split, writing the fp32 slabs and adding them (5 TB/s, and 2 us to launch).
-int plan_splits(int dtype, long M, long N, int nz, int kb) {
-  const long tiles = (long)ceil_div(M, 256) * ceil_div(N, 256) * nz;
-  const double block = split(dtype) ? 1.6 : 0.27;
-  const int least = split(dtype) ? 1 : 4;
-  int best = 1;
-  double best_t = 1e300;
-  for (int s = 1; s <= 16 && (s == 1 || kb / s >= least); ++s) {
-    const int per = ceil_div(kb, s);
-    const int real = ceil_div(kb, per);
-    double t = (double)ceil_div(tiles * real, kPairs) * (per * block + 1.6);
-    if (real > 1) t += 2.0 + 2.0 * real * nz * (double)M * N * 4.0 / 5e6;
-    if (t < best_t) {
-      best_t = t;
-      best = real;
+// The reducing products of a backward pass: outputs M x N of the operator's
+// type, `nz` of them, each a sum over kb blocks of K (dx, and dW).
+struct Product {
+  long M, N;
+  int nz, kb;
+};
+// How they are scheduled: the splits of K of each, which goes first, and the
+// units of the second that fill the first one's last round.
+struct PairPlan {
+  int splits[2], first, extra;
+};
+
+// Time of one unit over `per` blocks in us: 0.27 us a block (256 x 256 x 64 on a
+// CTA pair; 1.6 for planes), but at least an epilogue's, and a little to change
+// over.
+double unit_us(bool sp, int per) {
+  const double t = per * (sp ? 1.6 : 0.27), epilogue = sp ? 2.5 : 2.0;
+  return (t > epilogue ? t : epilogue) + 0.3;
+}
+// Rounds of the 76 pairs for n[0] units of c[0] us, then n[1] of c[1] (Walk's order).
+double rounds_us(const long (&n)[2], const double (&c)[2], int* extra) {
+  const long full = n[0] / kPairs, part = n[0] % kPairs, idle = kPairs - part;
+  double best = 1e300;
+  const int most = part == 0 ? 0 : (int)(c[0] / c[1]) + 1;
+  for (int e = 0; e <= most; ++e) {
+    const long taken = part == 0 ? 0 : (idle * e < n[1] ? idle * e : n[1]);
+    const long rest = n[1] - taken;
+    double t = full * c[0] + (taken + idle - 1) / idle * c[1] + (rest + kPairs - 1) / kPairs * c[1];
+    if (part != 0) {
+      const long busy = rest > idle ? (rest - idle + kPairs - 1) / kPairs : 0;
+      const double u = (full + 1) * c[0] + busy * c[1];
+      if (u > t) t = u;
+    }
+    if (t < best) {
+      best = t;
+      *extra = e;
     }
   }
   return best;
+}
+PairPlan search_plan(bool sp, const Product (&pr)[2]) {
+  static const int kTry[] = {1, 2, 3, 4, 6, 8, 12, 16};
+  const int least = sp ? 1 : 4;   // blocks of a split
+  long tiles[2];
+  for (int k = 0; k < 2; ++k) tiles[k] = (long)ceil_div(pr[k].M, 256) * ceil_div(pr[k].N, 256) * pr[k].nz;
+  PairPlan best{};
+  double best_t = 1e300;
+  for (int s0 : kTry) {
+    if (s0 > 1 && (pr[0].kb / s0 < least || tiles[0] > 4 * kPairs)) break;
+    for (int s1 : kTry) {
+      if (s1 > 1 && (pr[1].kb / s1 < least || tiles[1] > 4 * kPairs)) break;
+      const int want[2] = {s0, s1};
+      int real[2];
+      long n[2];
+      double c[2], slabs = 0.0;
+      for (int k = 0; k < 2; ++k) {
+        const int per = ceil_div(pr[k].kb, want[k]);
+        real[k] = ceil_div(pr[k].kb, per);
+        n[k] = tiles[k] * real[k];
+        c[k] = unit_us(sp, per);
+        // fp32 slabs written and added at 5 TB/s
+        if (real[k] > 1) slabs += 2.0 * real[k] * pr[k].nz * (double)pr[k].M * pr[k].N * 4.0 / 5e6;
+      }
+      if (slabs > 0.0) slabs += 2.0;
+      const int first = c[1] > c[0] ? 1 : 0;
+      const long no[2] = {n[first], n[1 - first]};
+      const double co[2] = {c[first], c[1 - first]};
+      int extra = 0;
+      const double t = rounds_us(no, co, &extra) + slabs;
+      if (t < best_t) {
+        best_t = t;
+        best = PairPlan{{real[0], real[1]}, first, extra};
+      }
+    }
+  }
+  return best;
+}
+// The search takes a few us, so a thread keeps the plans of the shapes it has seen.
+PairPlan plan_pair(int dtype, const Product& a, const Product& b) {
+  struct Entry {
+    Product pr[2];
+    bool sp, used;
+    PairPlan plan;
+  };
+  static thread_local Entry cache[64];
+  const bool sp = split(dtype);
+  size_t h = sp;
+  for (const Product* p : {&a, &b})
+    for (long v : {p->M, p->N, (long)p->nz, (long)p->kb}) h = h * 1000003u + (size_t)v;
+  Entry& e = cache[h % 64];
+  auto same = [](const Product& x, const Product& y) {
+    return x.M == y.M && x.N == y.N && x.nz == y.nz && x.kb == y.kb;
+  };
+  if (!e.used || e.sp != sp || !same(e.pr[0], a) || !same(e.pr[1], b)) {
+    const Product pr[2] = {a, b};
+    e = Entry{{a, b}, sp, true, search_plan(sp, pr)};
+  }
+  return e.plan;
+}
+
+// How a product's C of the operator's type comes about: written by the
+// product, or through fp32 slabs, one per split (and z).
+struct Reduce {
+  int splits = 1;
+  bool direct = false;
+  long np = 0, mp = 0;    // a slab's columns and rows
+  float* slab[2] = {nullptr, nullptr};
+};
+Reduce plan_reduce(int dtype, const Product& pr, int splits, bool add, Carver& cv) {
+  Reduce r;
+  r.splits = splits;
+  // fp32 adds pieces in place; 16-bit pieces add up in fp32
+  r.direct = splits == 1 && (split(dtype) ? pr.N % 4 == 0 : pr.N % 8 == 0 && !add);
+  r.np = round_up(pr.N, 8);
+  r.mp = round_up(pr.M, 256);
+  if (!r.direct)
+    for (int z = 0; z < pr.nz; ++z) r.slab[z] = cv.take<float>((size_t)splits * r.mp * r.np * 4);
+  return r;
+}
+// Sets j's output z; with slabs, slab_sum is still to come.
+cudaError_t reduce_output(int dtype, const Reduce& rd, Job& j, int z, void* out, float* slab, bool add) {
+  const long rows = j.M, N = j.N;
+  j.out = add ? tg::F32_ADD : tg::F32;
+  if (rd.direct) {
+    if (split(dtype)) return map_out32(&j.c[z], out, rows, N, N);
+    j.out = tg::STORE;
+    return map_out16(&j.c[z], out, rows, N, N);
+  }
+  j.slab_rows = (int)round_up(rows, 256);
+  return map_out32(&j.c[z], slab, (long)j.slab_rows * j.splits, rd.np, rd.np);
 }
 
 // K blocks between the register sums of a 16-bit product with fp32 results.
@@ -215,51 +334,71 @@ int plan_splits(int dtype, long M, long N, int nz, int kb) {
 // blocks 0.62, with 2 blocks 0.65).  Column sums (dbias) over few classes
 // cancel, so that the truncation shows: at 1789 x 448 x 12 they are 4.9e-6 off
 // with 8 blocks.  Such products have few tiles, and few blocks are affordable.
-int chunk_blocks(const Params& p, bool column_sums) {
-  const long tiles = (long)p.num_m * p.num_n;
+int chunk_blocks(const Job& j, bool column_sums) {
+  const long tiles = (long)j.num_m * j.num_n;
   return !column_sums || tiles > 4 * kPairs ? 8 : (tiles > kPairs ? 4 : 2);
 }
 
-cudaError_t gemm(int dtype, bool amn, bool bmn, int epi, const Params& p, int num_sms, cudaStream_t s) {
-  if (dtype == DTYPE_F32) return tg::gemm_f32(amn, bmn, epi, p, num_sms, s);
-  return dtype == DTYPE_BF16 ? tg::gemm_bf16(amn, bmn, epi, p, num_sms, s) : tg::gemm_f16(amn, bmn, epi, p, num_sms, s);
+cudaError_t gemm(int dtype, int epi, const Params& p, int num_sms, cudaStream_t s) {
+  if (dtype == DTYPE_F32) return tg::gemm_f32(epi, p, num_sms, s);
+  return dtype == DTYPE_BF16 ? tg::gemm_bf16(epi, p, num_sms, s) : tg::gemm_f16(epi, p, num_sms, s);
+}
+// The wanted ones of two reducing jobs in one launch, planned as `plan`.
+cudaError_t gemm_reduce(int dtype, const Job* a, const Job* b, const PairPlan& plan, int* status, int num_sms,
+                        cudaStream_t s) {
+  const Job* jobs[2] = {a, b};
+  if (plan.first == 1) {
+    jobs[0] = b;
+    jobs[1] = a;
+  }
+  if (jobs[0] == nullptr) {
+    jobs[0] = jobs[1];
+    jobs[1] = nullptr;
+  }
+  if (jobs[0] == nullptr) return cudaSuccess;
+  Params p{};
+  p.run = 1;
+  p.kb_chunk = split(dtype) ? 1 : kWhole;
+  p.extra = plan.extra;
+  p.status = status;
+  for (int k = 0; k < 2; ++k)
+    if (jobs[k] != nullptr) {
+      p.j[k] = *jobs[k];
+      const long units = (long)p.j[k].num_m * p.j[k].num_n * p.j[k].nz * p.j[k].splits;
+      p.units[k] = units > 0x7fffffffl ? -1 : (int)units;
+    }
+  return gemm(dtype, tg::REDUCE, p, num_sms, s);
 }
 
-// How a reducing product's C [M, N] of the operator's type comes about:
-// written by the product, or through fp32 slabs, one per split.
-struct Reduce {
-  int splits = 1;
-  bool direct = false;
-  long np = 0, mp = 0;    // a slab's columns and rows
-  float* slab = nullptr;
+// out[r, c] = scale * sum over the slabs, in slab order, for up to three outputs
+// at once (grid.y).  VEC: N is the slabs' row length, 8 values a thread; else
+// one.
+struct SlabSums {
+  const float* slab[3];
+  long stride[3];      // from slab to slab
+  int slabs[3];
+  void* out[3];
+  long rows[3];
+  int N, np;           // columns of the outputs and of the slabs
+  int count;
 };
-Reduce plan_reduce(int dtype, long M, long N, int nz, int kb, bool add, Carver& cv) {
-  Reduce r;
-  r.splits = plan_splits(dtype, M, N, nz, kb);
-  // fp32 adds pieces in place; 16-bit pieces add up in fp32
-  r.direct = r.splits == 1 && (split(dtype) ? N % 4 == 0 : N % 8 == 0 && !add);
-  r.np = round_up(N, 8);
-  r.mp = round_up(M, 256);
-  if (!r.direct) r.slab = cv.take<float>((size_t)r.splits * r.mp * r.np * 4);
-  return r;
-}
-
-// out[r, c] = scale * sum over the slabs, in slab order.  VEC: N is the slabs'
-// row length, 8 values a thread; else one.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kBlock) slab_sum_kernel(const float* __restrict__ slab, long stride, int n_slabs,
-                                                          T* __restrict__ out, long rows, int N, int np,
+__global__ void __launch_bounds__(kBlock) slab_sum_kernel(const __grid_constant__ SlabSums q,
                                                           const float* __restrict__ scale) {
+  const int y = blockIdx.y;
   const long i = (long)blockIdx.x * kBlock + threadIdx.x;
   const float sc = scale != nullptr ? __ldg(scale) : 1.f;
+  T* out = static_cast<T*>(q.out[y]);
+  const int n_slabs = q.slabs[y];
+  const long stride = q.stride[y];
   if constexpr (VEC) {
-    if (i * 8 >= rows * N) return;
+    if (i * 8 >= q.rows[y] * q.N) return;
     float v[8] = {};
-    const float4* a = reinterpret_cast<const float4*>(slab) + 2 * i;
+    const float4* a = reinterpret_cast<const float4*>(q.slab[y]) + 2 * i;
 #pragma unroll 4
     for (int k = 0; k < n_slabs; ++k, a += stride / 4) {
-      const float4 x = __ldg(a), y = __ldg(a + 1);
-      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w; v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      const float4 x = __ldg(a), w = __ldg(a + 1);
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w; v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= sc;
@@ -271,46 +410,41 @@ __global__ void __launch_bounds__(kBlock) slab_sum_kernel(const float* __restric
       reinterpret_cast<float4*>(out)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
     }
   } else {
-    const long r = i / N;
-    if (r >= rows) return;
-    const float* a = slab + r * np + (i - r * N);
+    const long r = i / q.N;
+    if (r >= q.rows[y]) return;
+    const float* a = q.slab[y] + r * q.np + (i - r * q.N);
     float v = 0.f;
 #pragma unroll 4
     for (int k = 0; k < n_slabs; ++k, a += stride) v += __ldg(a);
     out[i] = DT<T>::from(v * sc);
   }
 }
+// Adds an output of j that went through slabs.
+void add_slab_sum(SlabSums& q, const Reduce& rd, int z, int slabs, long slab_rows, void* out, long rows, long N) {
+  if (rd.direct || out == nullptr) return;
+  const int k = q.count++;
+  q.slab[k] = rd.slab[z];
+  q.stride[k] = slab_rows * rd.np;
+  q.slabs[k] = slabs;
+  q.out[k] = out;
+  q.rows[k] = rows;
+  q.N = (int)N;
+  q.np = (int)rd.np;
+}
 template <typename T>
-cudaError_t slab_sum_t(const Reduce& rd, int n_slabs, long slab_rows, void* out, long rows, long N, const float* scale,
-                       cudaStream_t s) {
-  const long stride = slab_rows * rd.np;
-  if (N % 8 == 0)
-    slab_sum_kernel<T, true><<<blocks_for(rows * N / 8, kBlock), kBlock, 0, s>>>(rd.slab, stride, n_slabs, (T*)out, rows,
-                                                                                 (int)N, (int)rd.np, scale);
+cudaError_t slab_sum_t(const SlabSums& q, const float* scale, cudaStream_t s) {
+  long most = 0;
+  for (int k = 0; k < q.count; ++k) most = q.rows[k] > most ? q.rows[k] : most;
+  if (q.N % 8 == 0)
+    slab_sum_kernel<T, true><<<dim3(blocks_for(most * q.N / 8, kBlock), q.count), kBlock, 0, s>>>(q, scale);
   else
-    slab_sum_kernel<T, false><<<blocks_for(rows * N, kBlock), kBlock, 0, s>>>(rd.slab, stride, n_slabs, (T*)out, rows,
-                                                                              (int)N, (int)rd.np, scale);
+    slab_sum_kernel<T, false><<<dim3(blocks_for(most * q.N, kBlock), q.count), kBlock, 0, s>>>(q, scale);
   return cudaGetLastError();
 }
-cudaError_t slab_sum(int dtype, const Reduce& rd, int n_slabs, long slab_rows, void* out, long rows, long N,
-                     const float* scale, cudaStream_t s) {
-  if (dtype == DTYPE_F32) return slab_sum_t<float>(rd, n_slabs, slab_rows, out, rows, N, scale, s);
-  if (dtype == DTYPE_F16) return slab_sum_t<__half>(rd, n_slabs, slab_rows, out, rows, N, scale, s);
-  return slab_sum_t<__nv_bfloat16>(rd, n_slabs, slab_rows, out, rows, N, scale, s);
-}
-
-// Sets p's output z for a reducing product of `rows` rows and returns its
-// epilogue; with slabs, slab_sum is still to come.
-cudaError_t reduce_output(int dtype, const Reduce& rd, Params& p, int z, void* out, float* slab, bool add, int* epi) {
-  const long rows = p.M, N = p.N;
-  *epi = add ? tg::F32_ADD : tg::F32;
-  if (rd.direct) {
-    if (split(dtype)) return map_out32(&p.c[z], out, rows, N, N);
-    *epi = tg::STORE;
-    return map_out16(&p.c[z], out, rows, N, N);
-  }
-  p.slab_rows = (int)round_up(rows, 256);
-  return map_out32(&p.c[z], slab, (long)p.slab_rows * p.splits, rd.np, rd.np);
+cudaError_t slab_sum(int dtype, const SlabSums& q, const float* scale, cudaStream_t s) {
+  if (q.count == 0) return cudaSuccess;
+  if (dtype == DTYPE_F32) return slab_sum_t<float>(q, scale, s);
+  return dtype == DTYPE_F16 ? slab_sum_t<__half>(q, scale, s) : slab_sum_t<__nv_bfloat16>(q, scale, s);
 }
 
 // ----------------------------------------------------------------------------- column sums
@@ -539,6 +673,7 @@ struct CeBwd {
   int piece, dz_plane;
   uint8_t* dz;
   float *scale, *colp;
+  PairPlan plan;
   Reduce dx, dw;
   size_t bytes;
 };
@@ -558,8 +693,10 @@ CeBwd ce_bwd_layout(const CeArgs& a, void* ws) {
   l.scale = cv.take<float>(3 * sizeof(float));
   l.colp = cv.take<float>((size_t)ceil_div(a.M, 32) * l.piece * 4);
   const int n = a.V < l.piece ? a.V : l.piece;
-  l.dx = plan_reduce(a.dtype, a.M, a.D, 1, ceil_div(n, tg::kBK), pieces > 1, cv);
-  l.dw = plan_reduce(a.dtype, n, a.D, 1, ceil_div(a.M, tg::kBK), false, cv);
+  const Product dx{a.M, a.D, 1, ceil_div(n, tg::kBK)}, dw{n, a.D, 1, ceil_div(a.M, tg::kBK)};
+  l.plan = plan_pair(a.dtype, dx, dw);
+  l.dx = plan_reduce(a.dtype, dx, l.plan.splits[0], pieces > 1, cv);
+  l.dw = plan_reduce(a.dtype, dw, l.plan.splits[1], false, cv);
   l.bytes = cv.used;
   return l;
 }
@@ -586,21 +723,21 @@ cudaError_t linear_ce_fwd(const CeArgs& a, float* loss, float* lse, void* ws, cu
   }
   JEPA_TRY_CUDA(fill(a.dtype, a.x, l.x, s));
   JEPA_TRY_CUDA(fill(a.dtype, a.w, l.w, s));
-  Params p = base_params(a.M, a.V, tg::kBN, a.status);
-  p.run = l.run;
-  set_k(p, a.D, 1, 1);
-  p.kb_chunk = split(a.dtype) ? 1 : chunk_blocks(p, false);
-  JEPA_TRY_CUDA(map_k(&p.a[0], l.x));
-  JEPA_TRY_CUDA(map_k(&p.b[0], l.w));
-  p.a_plane = (int)l.x.plane_rows;
-  p.b_plane = (int)l.w.plane_rows;
+  Job j = base_job(a.M, a.V, tg::kBN);
+  set_k(j, a.D, 1, 1);
+  JEPA_TRY_CUDA(map_k(&j.a[0], l.x));
+  JEPA_TRY_CUDA(map_k(&j.b[0], l.w));
+  j.a_plane = (int)l.x.plane_rows;
+  j.b_plane = (int)l.w.plane_rows;
+  Params p = forward_params(j, l.run, a.status);
+  p.kb_chunk = split(a.dtype) ? 1 : chunk_blocks(j, false);
   p.ep.bias = a.bias;
   p.ep.labels = a.labels;
   p.ep.V = a.V;
   p.ep.part_ms = l.ms;
   p.ep.part_sum = l.sums;
   p.ep.zy = l.zy;
-  JEPA_TRY_CUDA(gemm(a.dtype, false, false, tg::CE_FWD, p, a.num_sms, s));
+  JEPA_TRY_CUDA(gemm(a.dtype, tg::CE_FWD, p, a.num_sms, s));
   return ce_join(a, l.ms, l.sums, l.zy, l.parts, loss, lse, s);
 }
 
@@ -631,14 +768,15 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
     dz.ld = l.piece;
     dz.plane_rows = l.dz_plane;
     {
-      Params p = base_params(a.M, n, tg::kBN, a.status);
-      set_k(p, a.D, 1, 1);
-      p.kb_chunk = sp ? 1 : (dbias != nullptr ? chunk_blocks(p, true) : kWhole);
-      JEPA_TRY_CUDA(map_k(&p.a[0], l.x));
-      JEPA_TRY_CUDA(map_k(&p.b[0], w, v0));
-      JEPA_TRY_CUDA(map_out16(&p.c[0], l.dz, sp ? 3 * (long)l.dz_plane : a.M, l.piece, l.piece));
-      p.a_plane = (int)l.x.plane_rows;
-      p.b_plane = (int)l.w.plane_rows;
+      Job j = base_job(a.M, n, tg::kBN);
+      set_k(j, a.D, 1, 1);
+      JEPA_TRY_CUDA(map_k(&j.a[0], l.x));
+      JEPA_TRY_CUDA(map_k(&j.b[0], w, v0));
+      JEPA_TRY_CUDA(map_out16(&j.c[0], l.dz, sp ? 3 * (long)l.dz_plane : a.M, l.piece, l.piece));
+      j.a_plane = (int)l.x.plane_rows;
+      j.b_plane = (int)l.w.plane_rows;
+      Params p = forward_params(j, 1, a.status);
+      p.kb_chunk = sp ? 1 : (dbias != nullptr ? chunk_blocks(j, true) : kWhole);
       p.c_plane = l.dz_plane;
       p.ep.bias = a.bias != nullptr ? a.bias + v0 : nullptr;
       p.ep.labels = a.labels;
@@ -651,43 +789,40 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
       p.ep.V = a.V;
       p.ep.col_part = dbias != nullptr ? l.colp : nullptr;
       p.ep.ld_col = l.piece;
-      JEPA_TRY_CUDA(gemm(a.dtype, false, false, tg::CE_BWD, p, a.num_sms, s));
+      JEPA_TRY_CUDA(gemm(a.dtype, tg::CE_BWD, p, a.num_sms, s));
     }
     if (dbias != nullptr)
       JEPA_TRY_CUDA(part_sum(ColSums{{l.colp, nullptr}, {dbias + v0, nullptr}}, 1, l.piece, ceil_div(a.M, 32), n, unscale, s));
+    Job jx = base_job(a.M, a.D, tg::kBN), jw = base_job(n, a.D, tg::kBN);
+    uint8_t* dw_out = dw != nullptr ? static_cast<uint8_t*>(dw) + elem(a.dtype) * (size_t)v0 * a.D : nullptr;
     if (dx != nullptr) {
-      Params p = base_params(a.M, a.D, tg::kBN, a.status);
-      set_k(p, n, 1, l.dx.splits);
-      if (sp) p.kb_chunk = 1;
-      JEPA_TRY_CUDA(map_k(&p.a[0], dz));
-      JEPA_TRY_CUDA(map_mn(&p.b[0], w, v0));
-      p.a_plane = l.dz_plane;
-      p.b_plane = (int)l.w.plane_rows;
-      p.ep.scale = unscale;
+      set_k(jx, n, 1, l.dx.splits);
+      JEPA_TRY_CUDA(map_k(&jx.a[0], dz));
+      JEPA_TRY_CUDA(map_mn(&jx.b[0], w, v0));
+      jx.a_plane = l.dz_plane;
+      jx.b_plane = (int)l.w.plane_rows;
+      jx.scale = unscale;
       // the first piece has the most splits: a narrower last piece adds into the first slabs
-      if (v0 == 0) dx_slabs = p.splits;
-      int epi;
-      JEPA_TRY_CUDA(reduce_output(a.dtype, l.dx, p, 0, dx, l.dx.slab, v0 != 0, &epi));
-      JEPA_TRY_CUDA(gemm(a.dtype, false, true, epi, p, a.num_sms, s));
+      if (v0 == 0) dx_slabs = jx.splits;
+      JEPA_TRY_CUDA(reduce_output(a.dtype, l.dx, jx, 0, dx, l.dx.slab[0], v0 != 0));
     }
     if (dw != nullptr) {
-      uint8_t* out = static_cast<uint8_t*>(dw) + elem(a.dtype) * (size_t)v0 * a.D;
-      Params p = base_params(n, a.D, tg::kBN, a.status);
-      set_k(p, a.M, 1, l.dw.splits);
-      if (sp) p.kb_chunk = 1;
-      JEPA_TRY_CUDA(map_mn(&p.a[0], dz));
-      JEPA_TRY_CUDA(map_mn(&p.b[0], l.x));
-      p.a_plane = l.dz_plane;
-      p.b_plane = (int)l.x.plane_rows;
-      p.ep.scale = unscale;
-      int epi;
-      JEPA_TRY_CUDA(reduce_output(a.dtype, l.dw, p, 0, out, l.dw.slab, false, &epi));
-      JEPA_TRY_CUDA(gemm(a.dtype, true, true, epi, p, a.num_sms, s));
-      if (!l.dw.direct) JEPA_TRY_CUDA(slab_sum(a.dtype, l.dw, p.splits, p.slab_rows, out, n, a.D, unscale, s));
+      set_k(jw, a.M, 1, l.dw.splits);
+      JEPA_TRY_CUDA(map_mn(&jw.a[0], dz));
+      JEPA_TRY_CUDA(map_mn(&jw.b[0], l.x));
+      jw.a_mn = 1;
+      jw.a_plane = l.dz_plane;
+      jw.b_plane = (int)l.x.plane_rows;
+      jw.scale = unscale;
+      JEPA_TRY_CUDA(reduce_output(a.dtype, l.dw, jw, 0, dw_out, l.dw.slab[0], false));
     }
+    JEPA_TRY_CUDA(gemm_reduce(a.dtype, dx != nullptr ? &jx : nullptr, dw != nullptr ? &jw : nullptr, l.plan, a.status,
+                              a.num_sms, s));
+    SlabSums q{};
+    add_slab_sum(q, l.dw, 0, jw.splits, jw.slab_rows, dw_out, n, a.D);
+    if (v0 + n == a.V) add_slab_sum(q, l.dx, 0, dx_slabs, l.dx.mp, dx, a.M, a.D);
+    JEPA_TRY_CUDA(slab_sum(a.dtype, q, unscale, s));
   }
-  if (dx != nullptr && !l.dx.direct)
-    JEPA_TRY_CUDA(slab_sum(a.dtype, l.dx, dx_slabs, l.dx.mp, dx, a.M, a.D, unscale, s));
   return cudaSuccess;
 }
 
@@ -712,8 +847,8 @@ struct FfnBwd {
   int fp, d_plane;
   uint8_t* d[2];
   float* colp[2];
+  PairPlan plan;
   Reduce dx, dw;
-  float* dw_slab[2];
   size_t bytes;
 };
 FfnBwd ffn_bwd_layout(const FfnArgs& a, void* ws) {
@@ -725,29 +860,33 @@ FfnBwd ffn_bwd_layout(const FfnArgs& a, void* ws) {
   const long rows = split(a.dtype) ? 3 * (long)l.d_plane : a.M;
   for (int k = 0; k < 2; ++k) l.d[k] = cv.take<uint8_t>((size_t)rows * l.fp * 2);
   for (int k = 0; k < 2; ++k) l.colp[k] = cv.take<float>((size_t)ceil_div(a.M, 32) * l.fp * 4);
-  l.dx = plan_reduce(a.dtype, a.M, a.D, 1, 2 * ceil_div(a.F, tg::kBK), false, cv);
-  l.dw = plan_reduce(a.dtype, a.F, a.D, 2, ceil_div(a.M, tg::kBK), false, cv);
-  l.dw_slab[0] = l.dw.slab;
-  l.dw_slab[1] = l.dw.direct ? nullptr : cv.take<float>((size_t)l.dw.splits * l.dw.mp * l.dw.np * 4);
+  const Product dx{a.M, a.D, 1, 2 * ceil_div(a.F, tg::kBK)}, dw{a.F, a.D, 2, ceil_div(a.M, tg::kBK)};
+  l.plan = plan_pair(a.dtype, dx, dw);
+  l.dx = plan_reduce(a.dtype, dx, l.plan.splits[0], false, cv);
+  l.dw = plan_reduce(a.dtype, dw, l.plan.splits[1], false, cv);
   l.bytes = cv.used;
   return l;
 }
-cudaError_t ffn_product(const FfnArgs& a, const FfnFwd& l, Params& p, cudaStream_t s) {
+cudaError_t ffn_product(const FfnArgs& a, const FfnFwd& l, Job& j, cudaStream_t s) {
   JEPA_TRY_CUDA(fill(a.dtype, a.x, l.x, s));
   JEPA_TRY_CUDA(fill(a.dtype, a.wg, l.wg, s));
   JEPA_TRY_CUDA(fill(a.dtype, a.wu, l.wu, s));
-  p = base_params(a.M, a.F, tg::kBN / 2, a.status);
-  set_k(p, a.D, 1, 1);
+  j = base_job(a.M, a.F, tg::kBN / 2);
+  set_k(j, a.D, 1, 1);
+  JEPA_TRY_CUDA(map_k(&j.a[0], l.x));
+  JEPA_TRY_CUDA(map_k(&j.b[0], l.wg));
+  JEPA_TRY_CUDA(map_k(&j.b[1], l.wu));
+  j.a_plane = (int)l.x.plane_rows;
+  j.b_plane = (int)l.wg.plane_rows;
+  return cudaSuccess;
+}
+Params ffn_params(const FfnArgs& a, const Job& j) {
+  Params p = forward_params(j, 1, a.status);
   if (split(a.dtype)) p.kb_chunk = 1;
-  JEPA_TRY_CUDA(map_k(&p.a[0], l.x));
-  JEPA_TRY_CUDA(map_k(&p.b[0], l.wg));
-  JEPA_TRY_CUDA(map_k(&p.b[1], l.wu));
-  p.a_plane = (int)l.x.plane_rows;
-  p.b_plane = (int)l.wg.plane_rows;
   p.ep.bias = a.bg;
   p.ep.bias2 = a.bu;
   p.ep.act = a.act;
-  return cudaSuccess;
+  return p;
 }
 
 }  // namespace
@@ -770,17 +909,17 @@ cudaError_t gated_ffn_fwd(const FfnArgs& a, void* h, void* ws, cudaStream_t s) {
   if (few_rows_ok(a.dtype, a.M, a.D)) return few_rows_gate(a, h, s);
   Carver cv{static_cast<uint8_t*>(ws)};
   const FfnFwd l = ffn_fwd_layout(a, cv);
-  Params p;
-  JEPA_TRY_CUDA(ffn_product(a, l, p, s));
-  if ((a.F * elem(a.dtype)) % 16 != 0) {
+  Job j;
+  JEPA_TRY_CUDA(ffn_product(a, l, j, s));
+  const bool plain = (a.F * elem(a.dtype)) % 16 != 0;
+  if (!plain)
+    JEPA_TRY_CUDA(split(a.dtype) ? map_out32(&j.c[0], h, a.M, a.F, a.F) : map_out16(&j.c[0], h, a.M, a.F, a.F));
+  Params p = ffn_params(a, j);
+  if (plain) {
     p.plain = h;
     p.plain_ld = a.F;
-  } else if (split(a.dtype)) {
-    JEPA_TRY_CUDA(map_out32(&p.c[0], h, a.M, a.F, a.F));
-  } else {
-    JEPA_TRY_CUDA(map_out16(&p.c[0], h, a.M, a.F, a.F));
   }
-  return gemm(a.dtype, false, false, tg::GATE_FWD, p, a.num_sms, s);
+  return gemm(a.dtype, tg::GATE_FWD, p, a.num_sms, s);
 }
 
 cudaError_t gated_ffn_bwd(const FfnArgs& a, const void* dh, void* dx, void* dwg, void* dwu, float* dbg, float* dbu,
@@ -801,18 +940,19 @@ cudaError_t gated_ffn_bwd(const FfnArgs& a, const void* dh, void* dx, void* dwg,
     d[k].plane_rows = l.d_plane;
   }
   {
-    Params p;
-    JEPA_TRY_CUDA(ffn_product(a, l.in, p, s));
+    Job j;
+    JEPA_TRY_CUDA(ffn_product(a, l.in, j, s));
     for (int k = 0; k < 2; ++k)
-      JEPA_TRY_CUDA(map_out16(&p.c[k], l.d[k], sp ? 3 * (long)l.d_plane : a.M, l.fp, l.fp));
-    if (!sp && (dbg != nullptr || dbu != nullptr)) p.kb_chunk = chunk_blocks(p, true);
+      JEPA_TRY_CUDA(map_out16(&j.c[k], l.d[k], sp ? 3 * (long)l.d_plane : a.M, l.fp, l.fp));
+    Params p = ffn_params(a, j);
+    if (!sp && (dbg != nullptr || dbu != nullptr)) p.kb_chunk = chunk_blocks(j, true);
     p.c_plane = l.d_plane;
     p.ep.dh = dh;
     p.ep.dh_vec = (a.F * elem(a.dtype)) % 16 == 0;
     p.ep.col_part = dbg != nullptr ? l.colp[0] : nullptr;
     p.ep.col_part2 = dbu != nullptr ? l.colp[1] : nullptr;
     p.ep.ld_col = l.fp;
-    JEPA_TRY_CUDA(gemm(a.dtype, false, false, tg::GATE_BWD, p, a.num_sms, s));
+    JEPA_TRY_CUDA(gemm(a.dtype, tg::GATE_BWD, p, a.num_sms, s));
   }
   ColSums cs{};
   int sums = 0;
@@ -822,47 +962,39 @@ cudaError_t gated_ffn_bwd(const FfnArgs& a, const void* dh, void* dx, void* dwg,
       cs.out[sums++] = k == 0 ? dbg : dbu;
     }
   if (sums > 0) JEPA_TRY_CUDA(part_sum(cs, sums, l.fp, ceil_div(a.M, 32), a.F, nullptr, s));
+  Job jx = base_job(a.M, a.D, tg::kBN), jw = base_job(a.F, a.D, tg::kBN);
   if (dx != nullptr) {
-    Params p = base_params(a.M, a.D, tg::kBN, a.status);
-    set_k(p, a.F, 2, l.dx.splits);
-    if (sp) p.kb_chunk = 1;
+    set_k(jx, a.F, 2, l.dx.splits);
     for (int k = 0; k < 2; ++k) {
-      JEPA_TRY_CUDA(map_k(&p.a[k], d[k]));
-      JEPA_TRY_CUDA(map_mn(&p.b[k], k == 0 ? l.in.wg : l.in.wu));
+      JEPA_TRY_CUDA(map_k(&jx.a[k], d[k]));
+      JEPA_TRY_CUDA(map_mn(&jx.b[k], k == 0 ? l.in.wg : l.in.wu));
     }
-    p.a_plane = l.d_plane;
-    p.b_plane = (int)l.in.wg.plane_rows;
-    int epi;
-    JEPA_TRY_CUDA(reduce_output(a.dtype, l.dx, p, 0, dx, l.dx.slab, false, &epi));
-    JEPA_TRY_CUDA(gemm(a.dtype, false, true, epi, p, a.num_sms, s));
-    if (!l.dx.direct) JEPA_TRY_CUDA(slab_sum(a.dtype, l.dx, p.splits, p.slab_rows, dx, a.M, a.D, nullptr, s));
+    jx.a_plane = l.d_plane;
+    jx.b_plane = (int)l.in.wg.plane_rows;
+    JEPA_TRY_CUDA(reduce_output(a.dtype, l.dx, jx, 0, dx, l.dx.slab[0], false));
   }
+  // the weight gradients that are wanted are one job
   void* dw[2] = {dwg, dwu};
-  if (dwg == nullptr && dwu == nullptr) return cudaSuccess;
-  // the weight gradients that are wanted are one launch
-  Params p = base_params(a.F, a.D, tg::kBN, a.status);
-  set_k(p, a.M, 1, l.dw.splits);
-  if (sp) p.kb_chunk = 1;
-  JEPA_TRY_CUDA(map_mn(&p.b[0], l.in.x));
-  p.a_plane = l.d_plane;
-  p.b_plane = (int)l.in.x.plane_rows;
-  int nz = 0, epi = 0;
+  jw.nz = 0;
+  set_k(jw, a.M, 1, l.dw.splits);
+  jw.a_mn = 1;
   for (int k = 0; k < 2; ++k) {
     if (dw[k] == nullptr) continue;
-    JEPA_TRY_CUDA(map_mn(&p.a[nz], d[k]));
-    JEPA_TRY_CUDA(reduce_output(a.dtype, l.dw, p, nz, dw[k], l.dw_slab[k], false, &epi));
-    ++nz;
+    JEPA_TRY_CUDA(map_mn(&jw.a[jw.nz], d[k]));
+    JEPA_TRY_CUDA(reduce_output(a.dtype, l.dw, jw, jw.nz, dw[k], l.dw.slab[k], false));
+    ++jw.nz;
   }
-  p.nz = nz;
-  JEPA_TRY_CUDA(gemm(a.dtype, true, true, epi, p, a.num_sms, s));
-  if (!l.dw.direct)
-    for (int k = 0; k < 2; ++k) {
-      if (dw[k] == nullptr) continue;
-      Reduce r = l.dw;
-      r.slab = l.dw_slab[k];
-      JEPA_TRY_CUDA(slab_sum(a.dtype, r, p.splits, p.slab_rows, dw[k], a.F, a.D, nullptr, s));
-    }
-  return cudaSuccess;
+  if (jw.nz > 0) {
+    JEPA_TRY_CUDA(map_mn(&jw.b[0], l.in.x));
+    jw.a_plane = l.d_plane;
+    jw.b_plane = (int)l.in.x.plane_rows;
+  }
+  JEPA_TRY_CUDA(gemm_reduce(a.dtype, dx != nullptr ? &jx : nullptr, jw.nz > 0 ? &jw : nullptr, l.plan, a.status,
+                            a.num_sms, s));
+  SlabSums q{};
+  add_slab_sum(q, l.dx, 0, jx.splits, jx.slab_rows, dx, a.M, a.D);
+  for (int k = 0; k < 2; ++k) add_slab_sum(q, l.dw, k, jw.splits, jw.slab_rows, dw[k], a.F, a.D);
+  return slab_sum(a.dtype, q, nullptr, s);
 }
 
 // ----------------------------------------------------------------------------- linear layer backward
@@ -870,6 +1002,7 @@ namespace {
 
 struct LinBwd {
   Mat d, A, W;
+  PairPlan plan;
   Reduce dA, dW;
   float* colp;
   size_t bytes;
@@ -880,8 +1013,10 @@ LinBwd lin_bwd_layout(int dtype, const void* dout, const void* A, const void* W,
   l.d = operand(dtype, dout, M, N, cv);
   l.A = operand(dtype, A, M, K, cv);
   l.W = operand(dtype, W, N, K, cv);
-  l.dA = plan_reduce(dtype, M, K, 1, ceil_div(N, tg::kBK), false, cv);
-  l.dW = plan_reduce(dtype, N, K, 1, ceil_div(M, tg::kBK), false, cv);
+  const Product da{M, K, 1, ceil_div(N, tg::kBK)}, dw{N, K, 1, ceil_div(M, tg::kBK)};
+  l.plan = plan_pair(dtype, da, dw);
+  l.dA = plan_reduce(dtype, da, l.plan.splits[0], false, cv);
+  l.dW = plan_reduce(dtype, dw, l.plan.splits[1], false, cv);
   l.colp = cv.take<float>((size_t)col_strips(M, N) * N * 4);
   l.bytes = cv.used;
   return l;
@@ -901,26 +1036,30 @@ cudaError_t linear_bwd(int dtype, const void* dout, const void* A, const void* W
   }
   const LinBwd l = lin_bwd_layout(dtype, dout, A, W, M, N, K, ws);
   if (dA != nullptr || dW != nullptr) JEPA_TRY_CUDA(fill(dtype, dout, l.d, s));
+  Job jobs[2];
   for (int k = 0; k < 2; ++k) {
-    // dA = dout W, then dW = dout^T A
+    // dA = dout W, dW = dout^T A
     void* out = k == 0 ? dA : dW;
     if (out == nullptr) continue;
     const Mat& b = k == 0 ? l.W : l.A;
     const Reduce& rd = k == 0 ? l.dA : l.dW;
     const int rows = k == 0 ? M : N;
     JEPA_TRY_CUDA(fill(dtype, k == 0 ? W : A, b, s));
-    Params p = base_params(rows, K, tg::kBN, status);
-    set_k(p, k == 0 ? N : M, 1, rd.splits);
-    if (split(dtype)) p.kb_chunk = 1;
-    JEPA_TRY_CUDA(k == 0 ? map_k(&p.a[0], l.d) : map_mn(&p.a[0], l.d));
-    JEPA_TRY_CUDA(map_mn(&p.b[0], b));
-    p.a_plane = (int)l.d.plane_rows;
-    p.b_plane = (int)b.plane_rows;
-    int epi;
-    JEPA_TRY_CUDA(reduce_output(dtype, rd, p, 0, out, rd.slab, false, &epi));
-    JEPA_TRY_CUDA(gemm(dtype, k != 0, true, epi, p, num_sms, s));
-    if (!rd.direct) JEPA_TRY_CUDA(slab_sum(dtype, rd, p.splits, p.slab_rows, out, rows, K, nullptr, s));
+    Job& j = jobs[k] = base_job(rows, K, tg::kBN);
+    set_k(j, k == 0 ? N : M, 1, rd.splits);
+    JEPA_TRY_CUDA(k == 0 ? map_k(&j.a[0], l.d) : map_mn(&j.a[0], l.d));
+    JEPA_TRY_CUDA(map_mn(&j.b[0], b));
+    j.a_mn = k;
+    j.a_plane = (int)l.d.plane_rows;
+    j.b_plane = (int)b.plane_rows;
+    JEPA_TRY_CUDA(reduce_output(dtype, rd, j, 0, out, rd.slab[0], false));
   }
+  JEPA_TRY_CUDA(gemm_reduce(dtype, dA != nullptr ? &jobs[0] : nullptr, dW != nullptr ? &jobs[1] : nullptr, l.plan, status,
+                            num_sms, s));
+  SlabSums q{};
+  if (dA != nullptr) add_slab_sum(q, l.dA, 0, jobs[0].splits, jobs[0].slab_rows, dA, M, K);
+  if (dW != nullptr) add_slab_sum(q, l.dW, 0, jobs[1].splits, jobs[1].slab_rows, dW, N, K);
+  JEPA_TRY_CUDA(slab_sum(dtype, q, nullptr, s));
   if (dbias == nullptr) return cudaSuccess;
   if (dtype == DTYPE_F32) return col_sum_t<float>(dout, M, N, l.colp, dbias, s);
   if (dtype == DTYPE_F16) return col_sum_t<__half>(dout, M, N, l.colp, dbias, s);
