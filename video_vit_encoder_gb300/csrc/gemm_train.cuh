@@ -253,33 +253,30 @@ __device__ __forceinline__ void add_bias(const float* bias, int col, int n, floa
 
 // Column sums over the warp's 32 rows of 32 columns, written to part[0 .. n):
 // the block goes through the staging buffer (its last store has to have been
-// read), eight rows are summed by a lane for four columns, and the four row
-// groups joined.
+// read), a lane sums 16 rows of two columns, and the two row groups are joined.
 __device__ __forceinline__ void col_sum32(const float* v, uint8_t* buf, int lane, float* part, int n) {
   uint8_t* row = buf + lane * 128;
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     *reinterpret_cast<float4*>(row + ((k ^ (lane & 7)) << 4)) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
   __syncwarp();
-  const int k = lane & 7, g = lane >> 3;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  // lane (g, k) sums rows 16 g .. 16 g + 15 of columns 2 k, 2 k + 1
+  const int k = lane & 15, g = lane >> 4;
+  float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const float4 q = *reinterpret_cast<const float4*>(buf + (g * 8 + r) * 128 + ((k ^ r) << 4));
-    add2f(s.x, s.y, q.x, q.y);
-    add2f(s.z, s.w, q.z, q.w);
+  for (int r = 0; r < 16; r += 2) {
+    const float2 q = *reinterpret_cast<const float2*>(buf + (g * 16 + r) * 128 + (((k >> 1) ^ (r & 7)) << 4) + (k & 1) * 8);
+    const float2 p = *reinterpret_cast<const float2*>(buf + (g * 16 + r + 1) * 128 + (((k >> 1) ^ ((r + 1) & 7)) << 4) + (k & 1) * 8);
+    add2f(s0, s1, q.x, q.y);
+    add2f(t0, t1, p.x, p.y);
   }
-#pragma unroll
-  for (int o = 8; o < 32; o <<= 1) {
-    s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-    s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
-    s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
-    s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
-  }
+  s0 += t0;
+  s1 += t1;
+  s0 += __shfl_xor_sync(0xffffffffu, s0, 16);
+  s1 += __shfl_xor_sync(0xffffffffu, s1, 16);
   __syncwarp();   // the buffer has been read
-  // lane (g, k) writes column 4 k + g
-  const float out = g == 0 ? s.x : (g == 1 ? s.y : (g == 2 ? s.z : s.w));
-  if (4 * k + g < n) part[4 * k + g] = out;
+  const int c = 2 * k + g;
+  if (c < n) part[c] = g == 0 ? s0 : s1;
 }
 
 // This warp's 32 x 128-byte block of C at column x, row y, from each lane's row
@@ -464,6 +461,11 @@ __device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], co
   // dW 3.0e-3 from the exact gradients in norm instead of 1.7e-3 at 1999 x 768 x 50021 in bf16.)
   const float uni = ep.smoothing / (float)ep.V;
   const float cs = SPLIT ? 1.0f : 1.0f / (1.0f - ep.smoothing), hit = SPLIT ? 1.0f - ep.smoothing : 1.0f;
+  const int y = row - lane;
+  if (ep.col_part != nullptr) {
+    if (lane == 0) bulk_wait_read_all();
+    __syncwarp();
+  }
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const int cc = col0 + c * 32;
@@ -492,16 +494,9 @@ __device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], co
 #pragma unroll
       for (int j = 0; j < 32; ++j) w[j] = 0.f;
     }
-  }
-  const int y = row - lane;
-  if (ep.col_part != nullptr) {
-    if (lane == 0) bulk_wait_read_all();
-    __syncwarp();
-    float* to = ep.col_part + (size_t)(y >> 5) * ep.ld_col + col0;
-    const int n = y < p.j[0].M ? p.j[0].N - col0 : 0;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (col0 + c * 32 < p.j[0].N) col_sum32(v + c * 32, buf, lane, to + c * 32, n - c * 32);
+    // its column sums, while the next 32 columns are computed
+    if (ep.col_part != nullptr)
+      col_sum32(w, buf, lane, ep.col_part + (size_t)(y >> 5) * ep.ld_col + cc, y < p.j[0].M ? p.j[0].N - cc : 0);
   }
 #pragma unroll
   for (int c = 0; c < 2; ++c)
