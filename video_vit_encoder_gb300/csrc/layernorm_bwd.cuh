@@ -33,15 +33,17 @@ struct BwdShape {
   static constexpr int kRowVec = NV * V * ((RES ? 2 : 1) * sizeof(TX) + sizeof(TY));   // a thread's columns of x, res, dy
   static constexpr size_t kHead = 32 * sizeof(float);
   static constexpr int kMostGroups = 512 / TPR;
-  static constexpr size_t kLargestTable = SHIFT ? LnTable<V, NV, TPR, kMostGroups>::kBytes : 0;
+  static constexpr size_t kRowTable = sizeof(float) * TPR * NV * V;   // w as it is, where columns do not shift
+  static constexpr size_t kLargestTable = SHIFT ? LnTable<V, NV, TPR, kMostGroups>::kBytes : kRowTable;
   static constexpr int kSlots = (int)((kMostSmem - kHead - kLargestTable) / (TPR * kRowVec));
   static constexpr int kHalf = kSlots / 2 > 0 ? kSlots / 2 : 1;
   static constexpr int kRows = SHIFT && kHalf < kMostGroups ? kHalf : kMostGroups;
   static constexpr int kThreads = kRows * TPR;
   using Table = LnTable<V, NV, TPR, kRows>;
-  // w comes from a table, or where that does not fit beside a row from global memory
-  static constexpr bool kTable = SHIFT && kHead + (size_t)kThreads * kRowVec + Table::kBytes <= kMostSmem;
-  static constexpr size_t kTableBytes = kTable ? Table::kBytes : 0;
+  // w comes from shared memory, or where that does not fit beside a row from global memory
+  static constexpr size_t kWanted = SHIFT ? Table::kBytes : kRowTable;
+  static constexpr bool kTable = kHead + (size_t)kThreads * kRowVec + kWanted <= kMostSmem;
+  static constexpr size_t kTableBytes = kTable ? kWanted : 0;
   static constexpr int kFit = (int)((kMostSmem - kHead - kTableBytes) / (kThreads * kRowVec));
   static constexpr int kDepth = kFit > 4 ? 4 : kFit;
   static_assert(kDepth >= 1, "a row must fit");
@@ -71,7 +73,9 @@ __global__ void __launch_bounds__(BwdShape<TX, TY, V, NV, TPR, SHIFT, RES>::kThr
   const int head = SHIFT && t == 0 ? o : 0;   // elements of this thread's vector 0 that are the previous row's
   const float inv = 1.0f / (float)dim;
   if constexpr (S::kTable) {
-    S::Table::fill(table, w, dim, o);
+    if constexpr (SHIFT) S::Table::fill(table, w, dim, o);
+    else
+      for (int c = tid; c < dim; c += kThreads) table[c] = __ldg(w + c);
     __syncthreads();
   }
 
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(BwdShape<TX, TY, V, NV, TPR, SHIFT, RES>::kThr
       } else if constexpr (SHIFT) {
         S::Table::load(table, i, ww);
       } else {
-        ln_load<float, V>(w + c0, ww);
+        ln_load<float, V>((S::kTable ? table : w) + c0, ww);
       }
     };
     float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
