@@ -10,9 +10,7 @@
 //
 // Rows come through shared memory: each thread copies its own vectors of its
 // next rows asynchronously (no other thread reads them, so there is no
-// barrier) and reads them twice, once for the row sums and once for dx.  Only
-// the dw and db sums stay in registers, which leaves room for 16 warps per SM
-// to hide the latency of the row sums.
+// barrier) while 16 warps per SM work on the current ones.
 #pragma once
 #include "layernorm_train.cuh"
 
@@ -79,122 +77,139 @@ __global__ void __launch_bounds__(BwdShape<TX, TY, V, NV, TPR, SHIFT, RES>::kThr
     __syncthreads();
   }
 
-  // this thread's vectors of `row` into slot d of the ring; the last vector ends with the row (zeros follow)
-  auto fetch = [&](long row, int d) {
-    if (row < rows) {
-      uint8_t* slot = ring + (size_t)d * kThreads * S::kRowVec;
+  // this thread's first column, and how many columns follow from there
+  const int col = t * V - o, left = dim - col;
+  const TX* fx = x + first * dim + col;      // of the next row to fetch
+  const TY* fg = dy + first * dim + col;
+  const TX* fr = RES ? res + first * dim + col : nullptr;
+  TX* out_row = dx + first * dim + col;      // of the current row
+  const long step = stride * dim;
+  // this thread's vectors of the next row into slot d of the ring; the last vector ends with the row (zeros follow)
+  long next = first;
+  auto fetch = [&](int d) {
+    if (next < rows) {
+      uint8_t* q = ring + (size_t)d * kThreads * S::kRowVec + tid * kBX;
+      uint8_t* qy = ring + (size_t)d * kThreads * S::kRowVec + kOffY + tid * kBY;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c0 = (t + i * TPR) * V - o;
-        if (c0 < dim) {
-          const long at = row * dim + c0;
-          const int n = SHIFT ? min(V, dim - c0) : V;
-          uint8_t* q = slot + (size_t)(i * kThreads + tid) * kBX;
-          ln_copy_async<kBX>(q, x + at, n * (int)sizeof(TX));
-          if constexpr (RES) ln_copy_async<kBX>(q + (size_t)NV * kThreads * kBX, res + at, n * (int)sizeof(TX));
-          ln_copy_async<kBY>(slot + kOffY + (size_t)(i * kThreads + tid) * kBY, dy + at, n * (int)sizeof(TY));
+        if (i * TPR * V < left) {
+          const int n = SHIFT ? min(V, left - i * TPR * V) : V;
+          ln_copy_async<kBX>(q + i * kThreads * kBX, fx + i * TPR * V, n * (int)sizeof(TX));
+          if constexpr (RES)
+            ln_copy_async<kBX>(q + (NV + i) * kThreads * kBX, fr + i * TPR * V, n * (int)sizeof(TX));
+          ln_copy_async<kBY>(qy + i * kThreads * kBY, fg + i * TPR * V, n * (int)sizeof(TY));
         }
       }
+      fx += step;
+      fg += step;
+      if constexpr (RES) fr += step;
+      next += stride;
     }
     ln_copy_commit();
   };
 #pragma unroll
-  for (int d = 0; d < S::kDepth; ++d) fetch(first + d * stride, d);
+  for (int d = 0; d < S::kDepth; ++d) fetch(d);
 
-  float aw[NV][V], ab[NV][V];
+  f2 aw[NV][V / 2], ab[NV][V / 2];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < V; ++j) aw[i][j] = ab[i][j] = 0.f;
+    for (int j = 0; j < V / 2; ++j) aw[i][j] = ab[i][j] = 0ull;
 
   int d = 0;
-  float mu = 0.f, rs = 0.f;
-  if (first < rows) {
-    mu = __ldg(mean + first);
-    rs = __ldg(rstd + first);
-  }
+  // mean and rstd of 32 rows, one a lane, and of the next 32 (loaded for one row ahead, and handed on in registers, their
+  // latency was most of a narrow row's time: 73728 x 768 in bf16 80 us instead of 63)
+  const int lane = tid & 31;
+  auto stat = [&](const float* p, long from) {
+    const long r = from + lane * stride;
+    return r < rows ? __ldg(p + r) : 0.f;
+  };
+  float mean_c = stat(mean, first), rstd_c = stat(rstd, first);
+  float mean_n = stat(mean, first + 32 * stride), rstd_n = stat(rstd, first + 32 * stride);
+  int k = 0;
   for (long row = first; row < rows; row += stride) {
-    float mu_next = 0.f, rs_next = 0.f;
-    if (row + stride < rows) {
-      mu_next = __ldg(mean + row + stride);
-      rs_next = __ldg(rstd + row + stride);
+    if (k == 32) {
+      k = 0;
+      mean_c = mean_n;
+      rstd_c = rstd_n;
+      mean_n = stat(mean, row + 32 * stride);
+      rstd_n = stat(rstd, row + 32 * stride);
     }
+    const float mu = __shfl_sync(0xffffffffu, mean_c, k), rs = __shfl_sync(0xffffffffu, rstd_c, k);
+    ++k;
     ln_copy_wait<S::kDepth - 1>();
     const uint8_t* slot = ring + (size_t)d * kThreads * S::kRowVec;
-    // vector i: x - mean in xv, dy in gv and w in ww; the previous row's values and the zeros after the row meet w = 0
-    // and dy = 0
-    auto load = [&](int i, int c0, float (&xv)[V], float (&gv)[V], float (&ww)[V]) {
-      ln_load<TX, V>(reinterpret_cast<const TX*>(slot + (size_t)(i * kThreads + tid) * kBX), xv);
-      ln_load<TY, V>(reinterpret_cast<const TY*>(slot + kOffY + (size_t)(i * kThreads + tid) * kBY), gv);
-      if (SHIFT && i == 0) {
-#pragma unroll
-        for (int j = 0; j < V - 1; ++j) {
-          xv[j] = j < head ? 0.f : xv[j];
-          gv[j] = j < head ? 0.f : gv[j];
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < V; j += 2) add2f(xv[j], xv[j + 1], -mu, -mu);
-      if constexpr (SHIFT && !S::kTable) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) ww[j] = c0 + j >= 0 && c0 + j < dim ? __ldg(w + c0 + j) : 0.f;
-      } else if constexpr (SHIFT) {
-        S::Table::load(table, i, ww);
-      } else {
-        ln_load<float, V>((S::kTable ? table : w) + c0, ww);
-      }
-    };
-    float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
+    const f2 mu2 = f2_make(-mu, -mu), rs2 = f2_make(rs, rs);
+    // x - mean in xv and c = dy w in gv; the previous row's values and the zeros after the row meet w = 0 and dy = 0
+    f2 xv[NV][V / 2], gv[NV][V / 2];
+    f2 sa = 0ull, sb = 0ull;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c0 = (t + i * TPR) * V - o;
-      if (c0 < dim) {
-        float xv[V], gv[V], ww[V];
-        load(i, c0, xv, gv, ww);
+      if (i * TPR * V < left) {
+        LnVec<TX, V> vx;
+        LnVec<TY, V> vg;
+        vx.load(slot + tid * kBX + i * kThreads * kBX);
+        vg.load(slot + kOffY + tid * kBY + i * kThreads * kBY);
+        if (SHIFT && i == 0) {
+          vx.drop_head(head);
+          vg.drop_head(head);
+        }
+        vx.pairs(xv[i]);
+        vg.pairs(gv[i]);
+        f2 ww[V / 2];
+        if constexpr (SHIFT && !S::kTable) {
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-          ln_mul2(xv[j], xv[j + 1], rs, rs);
-          ln_fma2(aw[i][j], aw[i][j + 1], gv[j], gv[j + 1], xv[j], xv[j + 1]);
-          add2f(ab[i][j], ab[i][j + 1], gv[j], gv[j + 1]);
-          ln_mul2(gv[j], gv[j + 1], ww[j], ww[j + 1]);
-          add2f(sa[0], sa[1], gv[j], gv[j + 1]);
-          ln_fma2(sb[0], sb[1], gv[j], gv[j + 1], xv[j], xv[j + 1]);
+          for (int j = 0; j < V; j += 2) {
+            const int c = col + i * TPR * V + j;
+            ww[j / 2] = f2_make(c >= 0 && c < dim ? __ldg(w + c) : 0.f, c + 1 >= 0 && c + 1 < dim ? __ldg(w + c + 1) : 0.f);
+          }
+        } else if constexpr (SHIFT) {
+          S::Table::load(table, i, ww);
+        } else {
+          ln_floats<V>((S::kTable ? table : w) + col + i * TPR * V, ww);
+        }
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+          xv[i][j] = f2_add(xv[i][j], mu2);
+          const f2 xh = f2_mul(xv[i][j], rs2);
+          aw[i][j] = f2_fma(gv[i][j], xh, aw[i][j]);
+          ab[i][j] = f2_add(ab[i][j], gv[i][j]);
+          gv[i][j] = f2_mul(gv[i][j], ww[j]);
+          sa = f2_add(sa, gv[i][j]);
+          sb = f2_fma(gv[i][j], xh, sb);
         }
       }
     }
-    float s[2] = {sa[0] + sa[1], sb[0] + sb[1]};
+    if constexpr (!RES) fetch(d);   // the slot has been read
+    float s[2] = {f2_sum(sa), f2_sum(sb)};
     ln_row_sum<TPR, 2>(s, red);
     // dx = rs c - rs m0 - (rs m1 rs) (x - mean)
     const float k0 = -rs * (s[0] * inv), k1 = -rs * (s[1] * inv) * rs;
-    TX* dr = dx + row * dim;
+    const f2 k02 = f2_make(k0, k0), k12 = f2_make(k1, k1);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c0 = (t + i * TPR) * V - o;
-      if (c0 < dim) {
-        float xv[V], gv[V], ww[V];
-        load(i, c0, xv, gv, ww);
-        float out[V];
+      if (i * TPR * V < left) {
+        f2 out[V / 2];
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-          ln_mul2(gv[j], gv[j + 1], ww[j], ww[j + 1]);
-          out[j] = out[j + 1] = k0;
-          ln_fma2(out[j], out[j + 1], xv[j], xv[j + 1], k1, k1);
-          ln_fma2(out[j], out[j + 1], gv[j], gv[j + 1], rs, rs);
-        }
+        for (int j = 0; j < V / 2; ++j) out[j] = f2_fma(gv[i][j], rs2, f2_fma(xv[i][j], k12, k02));
         if constexpr (RES) {
-          float r[V];
-          ln_load<TX, V>(reinterpret_cast<const TX*>(slot + (size_t)((NV + i) * kThreads + tid) * kBX), r);
+          LnVec<TX, V> vr;
+          f2 r[V / 2];
+          vr.load(slot + tid * kBX + (NV + i) * kThreads * kBX);
+          vr.pairs(r);
 #pragma unroll
-          for (int j = 0; j < V; j += 2) add2f(out[j], out[j + 1], r[j], r[j + 1]);
+          for (int j = 0; j < V / 2; ++j) out[j] = f2_add(out[j], r[j]);
         }
-        if constexpr (SHIFT) ln_store_part<TX, V>(dr, c0, dim, out);
-        else ln_store<TX, V>(dr + c0, out);
+        LnVec<TX, V> vo;
+        vo.set(out);
+        TX* to = out_row + i * TPR * V;
+        if (!SHIFT || ((i > 0 || head == 0) && i * TPR * V + V <= left)) vo.store(to);
+        else ln_store_part<TX, V>(to, i == 0 ? head : 0, left - i * TPR * V, vo);   // shared with a neighbouring row
       }
     }
-    fetch(row + S::kDepth * stride, d);   // the slot has been read
+    if constexpr (RES) fetch(d);   // the slot has been read
     if (++d == S::kDepth) d = 0;
-    mu = mu_next;
-    rs = rs_next;
+    out_row += step;
   }
   ln_copy_wait<0>();
 
@@ -204,15 +219,22 @@ __global__ void __launch_bounds__(BwdShape<TX, TY, V, NV, TPR, SHIFT, RES>::kThr
   __syncthreads();
   float* mine = reinterpret_cast<float*>(ring) + (size_t)(tid / TPR) * 2 * dim;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c0 = (t + i * TPR) * V - o;
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (c0 + j >= 0 && c0 + j < dim) {
-        mine[c0 + j] = aw[i][j];
-        mine[dim + c0 + j] = ab[i][j];
+    for (int j = 0; j < V / 2; ++j) {
+      const int c = col + i * TPR * V + 2 * j;
+      float w0, w1, b0, b1;
+      f2_get(aw[i][j], w0, w1);
+      f2_get(ab[i][j], b0, b1);
+      if (c >= 0 && c < dim) {
+        mine[c] = w0;
+        mine[dim + c] = b0;
       }
-  }
+      if (c + 1 >= 0 && c + 1 < dim) {
+        mine[c + 1] = w1;
+        mine[dim + c + 1] = b1;
+      }
+    }
   __syncthreads();
   const float* all = reinterpret_cast<const float*>(ring);
   for (int c = tid; c < 2 * dim; c += kThreads) {
@@ -331,16 +353,17 @@ cudaError_t launch_rows(const Args& a, cudaStream_t s) {
   return e == cudaSuccess ? join(a, strips, s) : e;
 }
 
-// The fewest threads a row whose registers hold 32 columns each of dw and db.
+// The fewest threads a row that hold at most 16 columns each: x - mean, c and the
+// sums of dw and db of 16 columns fit in the registers that 16 warps have.
 template <typename TX, typename TY, int V, bool SHIFT, bool RES>
 cudaError_t launch_width(const Args& a, cudaStream_t s) {
   const int n = a.dim + (SHIFT ? V - 1 : 0);   // columns that the vectors cover
   if (n <= 256) return launch_rows<TX, TY, V, 8 / V, 32, SHIFT, RES>(a, s);
   if (n <= 512) return launch_rows<TX, TY, V, 16 / V, 32, SHIFT, RES>(a, s);
-  if (n <= 1024) return launch_rows<TX, TY, V, 32 / V, 32, SHIFT, RES>(a, s);
-  if (n <= 2048) return launch_rows<TX, TY, V, 32 / V, 64, SHIFT, RES>(a, s);
-  if (n <= 4096) return launch_rows<TX, TY, V, 32 / V, 128, SHIFT, RES>(a, s);
-  return launch_rows<TX, TY, V, 32 / V, 256, SHIFT, RES>(a, s);
+  if (n <= 1024) return launch_rows<TX, TY, V, 16 / V, 64, SHIFT, RES>(a, s);
+  if (n <= 2048) return launch_rows<TX, TY, V, 16 / V, 128, SHIFT, RES>(a, s);
+  if (n <= 4096) return launch_rows<TX, TY, V, 16 / V, 256, SHIFT, RES>(a, s);
+  return launch_rows<TX, TY, V, 16 / V, 512, SHIFT, RES>(a, s);
 }
 
 template <typename TX, typename TY>

@@ -111,92 +111,97 @@ __global__ void __launch_bounds__(kShiftThreads, 1)
   S::Table::fill(tw, w, dim, o);
   S::Table::fill(tb, b, dim, o);
   __syncthreads();
-  auto fetch = [&](long row, int d) {
-    if (row < rows) {
-      uint8_t* slot = ring + (size_t)d * kShiftThreads * S::kRowVec;
+  // this thread's first column, and how many columns follow from there
+  const int col = t * V - o, left = dim - col;
+  const TX* fx = x + first * dim + col;   // of the next row to fetch
+  TY* out_row = y + first * dim + col;    // of the current row
+  const long step = stride * dim;
+  long next = first;
+  auto fetch = [&](int d) {
+    if (next < rows) {
+      uint8_t* q = ring + (size_t)d * kShiftThreads * S::kRowVec + tid * kBX;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c0 = (t + i * TPR) * V - o;
-        if (c0 < dim)   // the last vector ends with the row (zeros follow)
-          ln_copy_async<kBX>(slot + (size_t)(i * kShiftThreads + tid) * kBX, x + row * dim + c0,
-                             min(V, dim - c0) * (int)sizeof(TX));
-      }
+      for (int i = 0; i < NV; ++i)
+        if (i * TPR * V < left)   // the last vector ends with the row (zeros follow)
+          ln_copy_async<kBX>(q + i * kShiftThreads * kBX, fx + i * TPR * V,
+                             min(V, left - i * TPR * V) * (int)sizeof(TX));
+      fx += step;
+      next += stride;
     }
     ln_copy_commit();
   };
 #pragma unroll
-  for (int d = 0; d < S::kDepth; ++d) fetch(first + d * stride, d);
+  for (int d = 0; d < S::kDepth; ++d) fetch(d);
   int d = 0;
   for (long row = first; row < rows; row += stride) {
     ln_copy_wait<S::kDepth - 1>();
     const uint8_t* slot = ring + (size_t)d * kShiftThreads * S::kRowVec;
-    float v[NV][V];
-    float sa[2] = {0.f, 0.f};
+    f2 v[NV][V / 2];
+    f2 sa = 0ull;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c0 = (t + i * TPR) * V - o;
+      if (i * TPR * V < left) {
+        LnVec<TX, V> vx;
+        vx.load(slot + tid * kBX + i * kShiftThreads * kBX);
+        if (i == 0) vx.drop_head(head);
+        vx.pairs(v[i]);
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[i][j] = 0.f;
-      if (c0 < dim) {
-        ln_load<TX, V>(reinterpret_cast<const TX*>(slot + (size_t)(i * kShiftThreads + tid) * kBX), v[i]);
-        if (i == 0) {
-#pragma unroll
-          for (int j = 0; j < V - 1; ++j) v[i][j] = j < head ? 0.f : v[i][j];
-        }
+        for (int j = 0; j < V / 2; ++j) sa = f2_add(sa, v[i][j]);
       }
-#pragma unroll
-      for (int j = 0; j < V; j += 2) add2f(sa[0], sa[1], v[i][j], v[i][j + 1]);
     }
-    fetch(row + S::kDepth * stride, d);   // the slot has been read
+    fetch(d);   // the slot has been read
     if (++d == S::kDepth) d = 0;
-    float s[1] = {sa[0] + sa[1]};
+    float s[1] = {f2_sum(sa)};
     ln_row_sum<TPR, 1>(s, red);
     const float mu = s[0] * inv;
-    float qa[2] = {0.f, 0.f};
+    const f2 mu2 = f2_make(-mu, -mu);
+    f2 qa = 0ull;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c0 = (t + i * TPR) * V - o;
-      if (c0 < dim) {
-        float dv[V];
+      if (i * TPR * V < left) {
 #pragma unroll
-        for (int j = 0; j < V; j += 2) add2f(v[i][j], v[i][j + 1], -mu, -mu);
+        for (int j = 0; j < V / 2; ++j) v[i][j] = f2_add(v[i][j], mu2);
+        const int lo = i == 0 ? head : 0, hi = left - i * TPR * V;
+        if (lo == 0 && hi >= V) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) dv[j] = v[i][j];
-        if (c0 + V > dim) {   // zeros that follow the row
+          for (int j = 0; j < V / 2; ++j) qa = f2_fma(v[i][j], v[i][j], qa);
+        } else {   // without the values that are not the row's
 #pragma unroll
-          for (int j = 1; j < V; ++j) dv[j] = c0 + j < dim ? dv[j] : 0.f;
+          for (int j = 0; j < V / 2; ++j) {
+            float a0, a1;
+            f2_get(v[i][j], a0, a1);
+            if (2 * j < lo || 2 * j >= hi) a0 = 0.f;
+            if (2 * j + 1 < lo || 2 * j + 1 >= hi) a1 = 0.f;
+            const f2 a = f2_make(a0, a1);
+            qa = f2_fma(a, a, qa);
+          }
         }
-        if (i == 0) {
-#pragma unroll
-          for (int j = 0; j < V - 1; ++j) dv[j] = j < head ? 0.f : dv[j];
-        }
-#pragma unroll
-        for (int j = 0; j < V; j += 2) ln_fma2(qa[0], qa[1], dv[j], dv[j + 1], dv[j], dv[j + 1]);
       }
     }
-    float q[1] = {qa[0] + qa[1]};
+    float q[1] = {f2_sum(qa)};
     ln_row_sum<TPR, 1>(q, red);
     const float rs = 1.0f / sqrtf(q[0] * inv + eps);
     if (t == 0) {
       if (mean != nullptr) mean[row] = mu;
       if (rstd != nullptr) rstd[row] = rs;
     }
-    TY* yr = y + row * dim;
+    const f2 rs2 = f2_make(rs, rs);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c0 = (t + i * TPR) * V - o;
-      if (c0 < dim) {
-        float ww[V], out[V];
+      if (i * TPR * V < left) {
+        f2 ww[V / 2], out[V / 2];
         S::Table::load(tw, i, ww);
         S::Table::load(tb, i, out);
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-          ln_mul2(v[i][j], v[i][j + 1], rs, rs);
-          ln_fma2(out[j], out[j + 1], v[i][j], v[i][j + 1], ww[j], ww[j + 1]);
-        }
-        ln_store_part<TY, V>(yr, c0, dim, out);
+        for (int j = 0; j < V / 2; ++j) out[j] = f2_fma(f2_mul(v[i][j], rs2), ww[j], out[j]);
+        LnVec<TY, V> vo;
+        vo.set(out);
+        const int lo = i == 0 ? head : 0, hi = left - i * TPR * V;
+        if (lo == 0 && hi >= V) vo.store(out_row + i * TPR * V);
+        else ln_store_part<TY, V>(out_row + i * TPR * V, lo, hi, vo);   // shared with a neighbouring row
       }
     }
+    out_row += step;
   }
   ln_copy_wait<0>();
 }

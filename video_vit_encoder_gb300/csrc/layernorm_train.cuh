@@ -60,21 +60,101 @@ __device__ __forceinline__ void ln_store(T* p, const float (&v)[V]) {
   }
 }
 
-// Packed arithmetic on two neighbouring values: (a, b) *= (x, y), (a, b) += (x, y) (p, q).
-__device__ __forceinline__ void ln_mul2(float& a, float& b, float x, float y) {
-  uint64_t v, k;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(k) : "f"(x), "f"(y));
-  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(k));
+// Two neighbouring fp32 values in one register pair; the rows' arithmetic is
+// packed, because it is instruction issue that bounds it.
+using f2 = uint64_t;
+__device__ __forceinline__ f2 f2_make(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_get(f2 v, float& a, float& b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
 }
-__device__ __forceinline__ void ln_fma2(float& a, float& b, float x, float y, float p, float q) {
-  uint64_t v, k, l;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(k) : "f"(x), "f"(y));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(l) : "f"(p), "f"(q));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(v) : "l"(k), "l"(l));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float f2_sum(f2 v) {
+  float a, b;
+  f2_get(v, a, b);
+  return a + b;
+}
+
+// The 32-bit words of a vector of V values, and their values in pairs.
+template <typename T, int V>
+struct LnVec {
+  static constexpr int kWords = V * sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void* p) {
+    if constexpr (kWords == 4) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p);
+      w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+    } else {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      w[0] = q.x; w[1] = q.y;
+    }
+  }
+  __device__ __forceinline__ void store(void* p) const {
+    if constexpr (kWords == 4) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  }
+  // Zeros in place of the first n values.
+  __device__ __forceinline__ void drop_head(int n) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      if constexpr (sizeof(T) == 4) w[k] = k < n ? 0u : w[k];
+      else w[k] &= 2 * k + 1 < n ? 0u : (2 * k < n ? 0xffff0000u : 0xffffffffu);
+    }
+  }
+  __device__ __forceinline__ void pairs(f2 (&v)[V / 2]) const {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      if constexpr (sizeof(T) == 4) {
+        asm("mov.b64 %0, {%1, %2};" : "=l"(v[k]) : "r"(w[2 * k]), "r"(w[2 * k + 1]));
+      } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        asm("mov.b64 %0, {%1, %2};" : "=l"(v[k]) : "r"(w[k] << 16), "r"(w[k] & 0xffff0000u));
+      } else {
+        T h[2];
+        memcpy(h, &w[k], 4);
+        v[k] = f2_make(DT<T>::to(h[0]), DT<T>::to(h[1]));
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const f2 (&v)[V / 2]) {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      float a, b;
+      f2_get(v[k], a, b);
+      if constexpr (sizeof(T) == 4) {
+        w[2 * k] = __float_as_uint(a);
+        w[2 * k + 1] = __float_as_uint(b);
+      } else {
+        w[k] = pack2<T>(a, b);
+      }
+    }
+  }
+};
+// Four to eight consecutive floats in pairs.
+template <int V>
+__device__ __forceinline__ void ln_floats(const float* p, f2 (&v)[V / 2]) {
+#pragma unroll
+  for (int j = 0; j < V / 4; ++j) {
+    const ulonglong2 q = reinterpret_cast<const ulonglong2*>(p)[j];
+    v[2 * j] = q.x;
+    v[2 * j + 1] = q.y;
+  }
 }
 
 __device__ __forceinline__ float ln_warp_sum(float v) {
@@ -146,31 +226,30 @@ struct LnTable {
         }
     }
   }
-  static __device__ __forceinline__ void load(const float* table, int i, float (&v)[V]) {
+  static __device__ __forceinline__ void load(const float* table, int i, f2 (&v)[V / 2]) {
     const int g = threadIdx.x / TPR % kClasses, t = threadIdx.x % TPR;
 #pragma unroll
     for (int j = 0; j < V; j += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(table + ((g * (NV * V / 4) + (i * V + j) / 4) * TPR + t) * 4);
-      v[j] = q.x; v[j + 1] = q.y; v[j + 2] = q.z; v[j + 3] = q.w;
+      const ulonglong2 q =
+          *reinterpret_cast<const ulonglong2*>(table + ((g * (NV * V / 4) + (i * V + j) / 4) * TPR + t) * 4);
+      v[j / 2] = q.x;
+      v[j / 2 + 1] = q.y;
     }
   }
 };
 
-// Whether a vector whose first column is c0 lies inside the row as a whole.
-template <int V>
-__device__ __forceinline__ bool ln_whole(int c0, int dim) {
-  return c0 >= 0 && c0 + V <= dim;
-}
-// Stores the part of a vector that lies inside the row.
+// Stores values lo .. hi - 1 of a vector.
 template <typename T, int V>
-__device__ __forceinline__ void ln_store_part(T* row, int c0, int dim, const float (&v)[V]) {
-  if (ln_whole<V>(c0, dim)) {
-    ln_store<T, V>(row + c0, v);
-  } else {
+__device__ __forceinline__ void ln_store_part(T* p, int lo, int hi, const LnVec<T, V>& v) {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (c0 + j >= 0 && c0 + j < dim) row[c0 + j] = DT<T>::from(v[j]);
-  }
+  for (int j = 0; j < V; ++j)
+    if (j >= lo && j < hi) {
+      if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<uint32_t*>(p)[j] = v.w[j];
+      } else {
+        reinterpret_cast<uint16_t*>(p)[j] = (uint16_t)(v.w[j / 2] >> (16 * (j & 1)));
+      }
+    }
 }
 
 inline bool ln_aligned(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
