@@ -96,36 +96,47 @@ cudaError_t map_out32(CUtensorMap* t, void* p, long rows, long cols, long ld) {
   return make_tmap_2d(t, p, 4, cols, rows, ld * 4, 32, 32);
 }
 
-// Rows of src to rows of 16 bytes.  8 columns a thread.
-__global__ void __launch_bounds__(kBlock) pad_kernel(const uint16_t* __restrict__ src, long rows, int cols,
-                                                     uint16_t* __restrict__ dst, int ld8) {
+// Up to three matrices to be laid out at once (grid.y).
+struct Fills {
+  const void* src[3];
+  uint16_t* dst[3];
+  long rows[3], plane_rows[3];
+  int cols[3], ld8[3];   // row length in the workspace, in 8 values
+  int count;
+};
+// Rows to rows of 16 bytes.  8 columns a thread.
+__global__ void __launch_bounds__(kBlock) pad_kernel(const __grid_constant__ Fills f) {
+  const int y = blockIdx.y;
+  const int cols = f.cols[y], ld8 = f.ld8[y];
+  const uint16_t* src = static_cast<const uint16_t*>(f.src[y]);
   const long i = (long)blockIdx.x * kBlock + threadIdx.x;
   const long r = i / ld8;
-  if (r >= rows) return;
+  if (r >= f.rows[y]) return;
   const int c = (int)(i - r * ld8) * 8;
   uint16_t h[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) h[j] = c + j < cols ? __ldg(src + r * cols + c + j) : (uint16_t)0;
   uint4 q;
   memcpy(&q, h, 16);
-  reinterpret_cast<uint4*>(dst)[i] = q;
+  reinterpret_cast<uint4*>(f.dst[y])[i] = q;
 }
 // fp32 rows to three bf16 planes x = x0 + x1 + x2, each the rounding of what
 // the ones before leave.  A finite value that rounds to infinity is truncated
 // instead; one that is not finite has no further planes.  Padding is zero.
-// VEC: rows start on 16 bytes.  8 columns a thread.
-template <bool VEC>
-__global__ void __launch_bounds__(kBlock) split_kernel(const float* __restrict__ src, long rows, int cols,
-                                                       uint16_t* __restrict__ dst, int ld8, long plane_rows) {
+// 8 columns a thread.
+__global__ void __launch_bounds__(kBlock) split_kernel(const __grid_constant__ Fills f) {
+  const int y = blockIdx.y;
+  const int cols = f.cols[y], ld8 = f.ld8[y];
+  const long rows = f.rows[y], plane_rows = f.plane_rows[y];
   const long i = (long)blockIdx.x * kBlock + threadIdx.x;
   const long r = i / ld8;
   if (r >= plane_rows) return;
   const int c = (int)(i - r * ld8) * 8;
   float x[8];
-  const float* p = src + r * cols + c;
+  const float* p = static_cast<const float*>(f.src[y]) + r * cols + c;
 #pragma unroll
   for (int j = 0; j < 8; j += 4) {
-    if (VEC) {   // cols is a multiple of 4
+    if (cols % 4 == 0) {   // rows start on 16 bytes
       const float4 q = r < rows && c + j < cols ? __ldg(reinterpret_cast<const float4*>(p + j)) : make_float4(0, 0, 0, 0);
       x[j] = q.x; x[j + 1] = q.y; x[j + 2] = q.z; x[j + 3] = q.w;
     } else {
@@ -147,23 +158,30 @@ __global__ void __launch_bounds__(kBlock) split_kernel(const float* __restrict__
   for (int k = 0; k < 3; ++k) {
     uint4 q;
     memcpy(&q, h[k], 16);
-    reinterpret_cast<uint4*>(dst)[k * plane_rows * ld8 + i] = q;
+    reinterpret_cast<uint4*>(f.dst[y])[k * plane_rows * ld8 + i] = q;
   }
 }
-// Fills an operand that lives in the workspace.
-cudaError_t fill(int dtype, const void* src, const Mat& m, cudaStream_t s) {
-  if (!m.own) return cudaSuccess;
-  const int ld8 = (int)(m.ld / 8);
-  uint16_t* dst = reinterpret_cast<uint16_t*>(const_cast<uint8_t*>(m.p));
-  if (!split(dtype)) {
-    pad_kernel<<<blocks_for(m.rows * ld8, kBlock), kBlock, 0, s>>>((const uint16_t*)src, m.rows, (int)m.cols, dst, ld8);
-  } else {
-    const unsigned b = blocks_for(m.plane_rows * ld8, kBlock);
-    if (m.cols % 4 == 0)
-      split_kernel<true><<<b, kBlock, 0, s>>>((const float*)src, m.rows, (int)m.cols, dst, ld8, m.plane_rows);
-    else
-      split_kernel<false><<<b, kBlock, 0, s>>>((const float*)src, m.rows, (int)m.cols, dst, ld8, m.plane_rows);
+// An operand that lives in the workspace is to be filled.
+void add_fill(Fills& f, const void* src, const Mat& m) {
+  if (!m.own) return;
+  const int k = f.count++;
+  f.src[k] = src;
+  f.dst[k] = reinterpret_cast<uint16_t*>(const_cast<uint8_t*>(m.p));
+  f.rows[k] = m.rows;
+  f.plane_rows[k] = m.plane_rows;
+  f.cols[k] = (int)m.cols;
+  f.ld8[k] = (int)(m.ld / 8);
+}
+cudaError_t fill(int dtype, const Fills& f, cudaStream_t s) {
+  if (f.count == 0) return cudaSuccess;
+  long most = 0;
+  for (int k = 0; k < f.count; ++k) {
+    const long n = (split(dtype) ? f.plane_rows[k] : f.rows[k]) * f.ld8[k];
+    most = n > most ? n : most;
   }
+  const dim3 g(blocks_for(most, kBlock), f.count);
+  if (split(dtype)) split_kernel<<<g, kBlock, 0, s>>>(f);
+  else pad_kernel<<<g, kBlock, 0, s>>>(f);
   return cudaGetLastError();
 }
 
@@ -449,34 +467,37 @@ cudaError_t slab_sum(int dtype, const SlabSums& q, const float* scale, cudaStrea
 
 // ----------------------------------------------------------------------------- column sums
 // out[c] = scale * sum over r of a[r, c], for two matrices at once (grid.y):
-// 32 columns a block, 32 threads a column, each over every 32nd row, joined in
-// a fixed order.
+// 32 columns a block, G threads a column, each over every G-th row, joined in a
+// fixed order.  G is 32 where there are rows for them and 8 else (63 rows of
+// 50021 columns: 17 us with 32).
 struct ColSums {
   const float* a[2];
   float* out[2];
 };
-__global__ void __launch_bounds__(1024) part_sum_kernel(ColSums cs, long ld, int rows, int n,
-                                                        const float* __restrict__ scale) {
-  __shared__ float sm[32][33];
+template <int G>
+__global__ void __launch_bounds__(32 * G) part_sum_kernel(ColSums cs, long ld, int rows, int n,
+                                                          const float* __restrict__ scale) {
+  __shared__ float sm[G][33];
   const float* a = cs.a[blockIdx.y];
   float* out = cs.out[blockIdx.y];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < n) {
-#pragma unroll 4
-    for (int r = g; r < rows; r += 32) s += __ldg(a + (long)r * ld + c);
+#pragma unroll 8
+    for (int r = g; r < rows; r += G) s += __ldg(a + (long)r * ld + c);
   }
   sm[g][lane] = s;
   __syncthreads();
-  s = sm[lane][g];   // warp g joins column g
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const int cc = blockIdx.x * 32 + g;
-  if (lane == 0 && cc < n) out[cc] = scale != nullptr ? s * __ldg(scale) : s;
+  if (g == 0 && c < n) {
+    for (int k = 1; k < G; ++k) s += sm[k][lane];
+    out[c] = scale != nullptr ? s * __ldg(scale) : s;
+  }
 }
 cudaError_t part_sum(const ColSums& cs, int count, long ld, int rows, int n, const float* scale, cudaStream_t s) {
-  part_sum_kernel<<<dim3(blocks_for(n, 32), count), 1024, 0, s>>>(cs, ld, rows, n, scale);
+  const dim3 g(blocks_for(n, 32), count);
+  if (rows > 128) part_sum_kernel<32><<<g, 1024, 0, s>>>(cs, ld, rows, n, scale);
+  else part_sum_kernel<8><<<g, 256, 0, s>>>(cs, ld, rows, n, scale);
   return cudaGetLastError();
 }
 
@@ -523,7 +544,7 @@ __global__ void __launch_bounds__(kBlock) col_strip_kernel(const T* __restrict__
   }
 }
 int col_strips(int M, int N) {
-  const int want = ceil_div(4 * 152, ceil_div(N, 256)), most = ceil_div(M, 64);
+  const int want = ceil_div(4 * 152, ceil_div(N, 256)), most = ceil_div(M, 32);
   return want < most ? want : most;
 }
 template <typename T>
@@ -721,8 +742,10 @@ cudaError_t linear_ce_fwd(const CeArgs& a, float* loss, float* lse, void* ws, cu
     JEPA_TRY_CUDA(few_rows_ce(a, l.ms, l.sums, l.zy, s));
     return ce_join(a, l.ms, l.sums, l.zy, l.parts, loss, lse, s);
   }
-  JEPA_TRY_CUDA(fill(a.dtype, a.x, l.x, s));
-  JEPA_TRY_CUDA(fill(a.dtype, a.w, l.w, s));
+  Fills f{};
+  add_fill(f, a.x, l.x);
+  add_fill(f, a.w, l.w);
+  JEPA_TRY_CUDA(fill(a.dtype, f, s));
   Job j = base_job(a.M, a.V, tg::kBN);
   set_k(j, a.D, 1, 1);
   JEPA_TRY_CUDA(map_k(&j.a[0], l.x));
@@ -749,8 +772,10 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
   }
   const CeBwd l = ce_bwd_layout(a, ws);
   const bool sp = split(a.dtype);
-  JEPA_TRY_CUDA(fill(a.dtype, a.x, l.x, s));
-  JEPA_TRY_CUDA(fill(a.dtype, a.w, l.w, s));
+  Fills f{};
+  add_fill(f, a.x, l.x);
+  add_fill(f, a.w, l.w);
+  JEPA_TRY_CUDA(fill(a.dtype, f, s));
   const float* unscale = nullptr;
   if (!sp) {
     dz_scale_kernel<<<1, 1024, 0, s>>>(dloss, a.M, a.dtype == DTYPE_F16 ? 16384.f : 1.f, a.smoothing, l.scale);
@@ -868,9 +893,11 @@ FfnBwd ffn_bwd_layout(const FfnArgs& a, void* ws) {
   return l;
 }
 cudaError_t ffn_product(const FfnArgs& a, const FfnFwd& l, Job& j, cudaStream_t s) {
-  JEPA_TRY_CUDA(fill(a.dtype, a.x, l.x, s));
-  JEPA_TRY_CUDA(fill(a.dtype, a.wg, l.wg, s));
-  JEPA_TRY_CUDA(fill(a.dtype, a.wu, l.wu, s));
+  Fills f{};
+  add_fill(f, a.x, l.x);
+  add_fill(f, a.wg, l.wg);
+  add_fill(f, a.wu, l.wu);
+  JEPA_TRY_CUDA(fill(a.dtype, f, s));
   j = base_job(a.M, a.F, tg::kBN / 2);
   set_k(j, a.D, 1, 1);
   JEPA_TRY_CUDA(map_k(&j.a[0], l.x));
@@ -1035,7 +1062,11 @@ cudaError_t linear_bwd(int dtype, const void* dout, const void* A, const void* W
     return zero(dbias, sizeof(float) * (size_t)N, s);
   }
   const LinBwd l = lin_bwd_layout(dtype, dout, A, W, M, N, K, ws);
-  if (dA != nullptr || dW != nullptr) JEPA_TRY_CUDA(fill(dtype, dout, l.d, s));
+  Fills f{};
+  if (dA != nullptr || dW != nullptr) add_fill(f, dout, l.d);
+  if (dA != nullptr) add_fill(f, W, l.W);
+  if (dW != nullptr) add_fill(f, A, l.A);
+  JEPA_TRY_CUDA(fill(dtype, f, s));
   Job jobs[2];
   for (int k = 0; k < 2; ++k) {
     // dA = dout W, dW = dout^T A
@@ -1044,7 +1075,6 @@ cudaError_t linear_bwd(int dtype, const void* dout, const void* A, const void* W
     const Mat& b = k == 0 ? l.W : l.A;
     const Reduce& rd = k == 0 ? l.dA : l.dW;
     const int rows = k == 0 ? M : N;
-    JEPA_TRY_CUDA(fill(dtype, k == 0 ? W : A, b, s));
     Job& j = jobs[k] = base_job(rows, K, tg::kBN);
     set_k(j, k == 0 ? N : M, 1, rd.splits);
     JEPA_TRY_CUDA(k == 0 ? map_k(&j.a[0], l.d) : map_mn(&j.a[0], l.d));
