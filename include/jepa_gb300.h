@@ -402,15 +402,17 @@ JEPA_API jepa_status jepa_qkv_rope(const void* A, const void* W, const float* bi
  *     widths are at most 2^24 (layer norm: dim at most 2^20).
  *   - `workspace` is a device buffer of the caller, 256-byte aligned, of at
  *     least the bytes that the _workspace_bytes function gives for the same
- *     arguments (it returns 0 for arguments that the call refuses).  Its
- *     contents mean nothing between calls.  Two calls that may run at the same
- *     time need two workspaces; nothing else is shared between calls.
+ *     arguments: 0 where none is needed (the workspace may then be NULL), and
+ *     for arguments that the call refuses.  Its contents mean nothing between
+ *     calls.  Two calls that may run at the same time need two workspaces;
+ *     nothing else is shared between calls.
  *   - Outputs must not overlap inputs, the workspace or each other.  Gradients
  *     are written, not added to.
  *   - Results do not depend on scheduling: every sum has a fixed order.
  *   - The calls only enqueue kernels and memsets and can be captured into a
- *     CUDA graph; the first call on a device (which allocates that device's
- *     status word) has to be made outside a capture. */
+ *     CUDA graph; the first call of an entry point on a device (which sets its
+ *     kernels up, and allocates the device's status word) has to be made
+ *     outside a capture. */
 
 /* Layer norm over the last dimension: y = (x - mean) rstd w + b, with the
  * biased centred variance, rstd = 1/sqrt(var + eps).
@@ -442,7 +444,8 @@ JEPA_API jepa_status jepa_layernorm_bwd(const void* dy, const void* x, const flo
  * still its own).  A label outside [0, V) that is not ignore_index gives loss
  * NaN, no gradient, and JEPA_ERR_ARG from the next jepa_ops_sync.  A bias of
  * -infinity takes a class out (its gradient is 0 without smoothing); NaN
- * logits give a NaN row. */
+ * logits give a NaN row.  Rows without a gradient still meet dW's products,
+ * with a factor of 0, so their x has to be finite; their dloss is not used. */
 JEPA_API size_t jepa_linear_ce_workspace_bytes(int M, int D, int V, int dtype, int backward);
 JEPA_API jepa_status jepa_linear_ce_fwd(const void* x, const void* W, const float* bias, const int64_t* labels,
                                         float* loss, float* lse, int M, int D, int V, int dtype, int64_t ignore_index,

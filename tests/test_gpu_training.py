@@ -42,7 +42,7 @@ def _np(t):
 LN_TYPES = [("f32", "f32"), ("f32", "bf16"), ("f32", "f16"), ("bf16", "bf16"), ("f16", "f16")]
 LN_SHAPES = [(1, 1, 0), (3, 7, 0), (5, 64, 0), (37, 777, 0), (2, 256, 0), (130, 1000, 0), (70, 1024, 0), (9, 1025, 0),
              (6, 1536, 0), (4, 2050, 0), (3, 4096, 0), (2, 8192, 0), (3, 8193, 0), (3000, 136, 0), (16, 512, 1),
-             (5, 1664, 1)]
+             (5, 1664, 1), (1, 1, 0), (3, 100003, 0), (2, 1 << 20, 0)]
 
 
 def _depth(dim):
@@ -135,7 +135,7 @@ def test_layernorm_nan_row_stays_in_its_row(jg):
 # ----------------------------------------------------------------------------- softmax cross entropy
 CE_SHAPES = [(1, 8, 1, 0), (1, 64, 2, 0), (8, 1024, 174, 0), (129, 72, 257, 0), (300, 768, 1000, 0), (257, 65, 513, 0),
              (64, 128, 4097, 0), (33, 40, 30, 1), (600, 64, 300, 0), (5, 8, 9000, 0), (16, 200, 5000, 0), (9, 1032, 40, 0),
-             (17, 512, 300, 0)]
+             (17, 512, 300, 0), (2600, 64, 300, 0), (700, 1100, 400, 0), (1, 1, 1, 0), (20, 1, 3, 0)]
 
 
 def _ce_case(M, D, V, dtype, shift, key, ignore=0.2):
@@ -185,6 +185,95 @@ def test_linear_ce_bwd(jg, M, D, V, shift, dtype, smooth, bias, scale):
     tb.check(_np(dx), rx, tb.rounded(rx, tb.product(dz, Wv.T, er), dtype), "dx")
     tb.check(_np(dW), rw, tb.rounded(rw, tb.product(dz.T, xv.T, er.T), dtype), "dW")
     jg.ops_sync()
+
+
+def _sample(rng, n, k, tile=256):
+    """k of n places, with those at both ends and around tiles' borders."""
+    edge = [i for b in (0, tile, n // 2 // tile * tile, n) for i in (b - 1, b) if 0 <= i < n]
+    return np.unique(np.concatenate([edge, rng.integers(0, n, k)]).astype(int))
+
+
+@pytest.mark.parametrize("dtype,M,D,V", [("bf16", 2048, 64, 40000), ("f32", 2048, 40, 40001), ("f16", 700, 33, 150001)])
+def test_linear_ce_fwd_many_tiles(jg, dtype, M, D, V):
+    """Row statistics carried over several column tiles."""
+    rng, x, xv, W, Wv, b, bv, lab, labels = _ce_case(M, D, V, dtype, 0, 6)
+    loss, lse = jg.linear_ce_fwd(x, W, b, labels, smoothing=0.1)
+    r = _sample(rng, M, 24)
+    rl, rs, z = ot.linear_ce(xv[r], Wv, bv, lab[r], smoothing=0.1)
+    el, es = tb.ce_forward(xv[r], Wv, bv, z, rs, rl, lab[r], 0.1)
+    tb.check(_np(lse)[r], rs, es, "lse")
+    tb.check(_np(loss)[r], rl, el, "loss")
+    # every row against float64 on the device; the rows' bounds are of one size, 4 is for their spread
+    z64 = x.double() @ W.double().T + b.double()
+    assert (lse.double() - torch.logsumexp(z64, 1)).abs().max() <= 4 * es.max()
+    jg.ops_sync()
+
+
+@pytest.mark.parametrize("dtype,M,D,V", [("bf16", 20000, 64, 9000), ("f16", 20001, 72, 9001), ("f32", 12000, 64, 5000),
+                                         ("f32", 12001, 30, 9001)])
+def test_linear_ce_bwd_in_pieces(jg, dtype, M, D, V):
+    """Vocabularies whose dz does not fit the workspace's 256 MB at once."""
+    rng, x, xv, W, Wv, b, bv, lab, labels = _ce_case(M, D, V, dtype, 0, 7)
+    smooth = 0.1
+    dl, dlv = _dev(rng.standard_normal(M) / M)
+    # in blocks of rows: 64-bit lse, then dz as the oracle's, on the device
+    x64, W64, b64 = x.double(), W.double(), b.double()
+    lse = torch.cat([torch.logsumexp(x64[i:i + 4000] @ W64.T + b64, 1) for i in range(0, M, 4000)]).float()
+    lsev = _np(lse)
+    dx, dW, db = jg.linear_ce_bwd(dl, x, W, b, labels, lse, smoothing=smooth)
+    h = 0 if dtype == "f32" else tb.HALF[dtype]
+    floor = 2.0 ** -38 * np.abs(dlv).max() if dtype == "f16" else 0.0
+
+    def dz_of(rows, classes):
+        z = xv[rows] @ Wv[classes].T + bv[classes]
+        keep = (lab[rows] != -100)[:, None]
+        hit = np.arange(V)[classes][None] == lab[rows][:, None]
+        g = dlv[rows][:, None] * keep
+        dz = g * (np.exp(z - lsev[rows][:, None]) - smooth / V - (1 - smooth) * hit)
+        e = tb.ce_logits(xv[rows], Wv[classes], bv[classes])
+        arg = e + 4 * tb.U * (np.abs(z) + np.abs(lsev[rows])[:, None] + 4)
+        p = np.exp(z - lsev[rows][:, None])
+        e = np.abs(g) * (p * np.expm1(arg) + 2 * tb.U + 6 * tb.U * (p + hit + smooth))
+        return dz, e, e + h * (np.abs(dz) + e) + floor * keep
+    r, c = _sample(rng, M, 40), _sample(rng, V, 40)
+    every = slice(None)
+    dz, _, er = dz_of(r, every)
+    rx = dz @ Wv
+    tb.check(_np(dx)[r], rx, tb.rounded(rx, tb.product(dz, Wv.T, er), dtype), "dx")
+    dz, e, er = dz_of(every, c)
+    rw = dz.T @ xv
+    tb.check(_np(dW)[c], rw, tb.rounded(rw, tb.product(dz.T, xv.T, er.T), dtype), "dW")
+    tb.check(_np(db)[c], dz.sum(0), e.sum(0) + 2 * tb.U * (M + 16) * np.abs(dz).sum(0), "dbias")
+    # one gradient at a time gives the same
+    assert torch.equal(jg.linear_ce_bwd(dl, x, W, b, labels, lse, smoothing=smooth, needs=(True, False, False))[0], dx)
+    assert torch.equal(jg.linear_ce_bwd(dl, x, W, b, labels, lse, smoothing=smooth, needs=(False, True, False))[1], dW)
+    jg.ops_sync()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_linear_ce_dloss_of_rows_without_a_gradient(jg, dtype):
+    """dloss of ignored rows is not used: not its size, not an infinity, not NaN."""
+    M, D, V = 150, 64, 300
+    _, x, _, W, _, b, _, lab, labels = _ce_case(M, D, V, dtype, 0, 8, ignore=0.5)
+    _, lse = jg.linear_ce_fwd(x, W, b, labels)
+    dl = torch.randn(M, device="cuda")
+    want = jg.linear_ce_bwd(torch.where(labels == -100, 0.0, dl), x, W, b, labels, lse)
+    for v in (1e30, float("inf"), float("nan")):
+        got = jg.linear_ce_bwd(torch.where(labels == -100, v, dl), x, W, b, labels, lse)
+        for a, r in zip(got, want):
+            assert torch.equal(a, r), v
+
+
+def test_linear_ce_forms_of_labels_and_dloss(jg):
+    """int32 labels, one dloss as a number or as a tensor without dimensions."""
+    _, x, _, W, _, b, _, lab, labels = _ce_case(200, 64, 300, "bf16", 0, 9)
+    loss, lse = jg.linear_ce_fwd(x, W, b, labels)
+    l32, s32 = jg.linear_ce_fwd(x, W, b, labels.int())
+    assert torch.equal(loss, l32) and torch.equal(lse, s32)
+    want = jg.linear_ce_bwd(torch.full((200,), 0.25, device="cuda"), x, W, b, labels, lse)
+    for dl in (0.25, torch.tensor(0.25), torch.tensor(0.25, device="cuda", dtype=torch.float64)):
+        for a, r in zip(jg.linear_ce_bwd(dl, x, W, b, labels.int(), lse), want):
+            assert torch.equal(a, r)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -264,7 +353,8 @@ def test_linear_ce_nan_rows(jg, dtype, D):
 # ----------------------------------------------------------------------------- gated feed-forward
 FFN_SHAPES = [(1, 64, 8, 0), (1, 8, 1, 0), (8, 1024, 256, 0), (129, 72, 136, 0), (300, 256, 520, 0), (257, 128, 1000, 0),
               (5, 33, 17, 0), (200, 65, 300, 0), (40, 64, 64, 1), (700, 128, 256, 0), (16, 200, 72, 0), (12, 1032, 520, 0),
-              (17, 512, 77, 0), (2, 4, 3, 0)]
+              (17, 512, 77, 0), (2, 4, 3, 0), (2600, 72, 136, 0), (400, 1100, 520, 0), (1, 1, 1, 0),
+              (20, 1, 3, 0)]
 
 
 def _ffn_case(M, D, F, dtype, shift, bias, key):
@@ -507,6 +597,79 @@ def test_calls_on_two_streams(jg):
     for o in outs:
         for a, b in zip(o, ref):
             assert torch.equal(a, b)
+    jg.ops_sync()
+
+
+def test_inputs_dropped_while_another_stream_uses_them(jg):
+    """Inputs that are dropped right after a call on another stream: their
+    memory is not given out before that stream is done with it."""
+    side = torch.cuda.Stream()
+    W = (torch.randn(300, 256, device="cuda") / 16).bfloat16()
+    lab = torch.randint(0, 300, (400,), device="cuda")
+    x = torch.randn(400, 256, device="cuda").bfloat16()
+    want = jg.linear_ce_fwd(x, W, None, lab)
+    ref = jg.linear_ce_bwd(1.0, x, W, None, lab, want[1])
+    keep = x.clone()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        x = keep.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)   # clocks, about 10 ms
+        got = jg.linear_ce_bwd(1.0, x, W, None, lab, want[1], stream=side)
+        del x
+        others = [torch.zeros(400, 256, device="cuda", dtype=torch.bfloat16) for _ in range(8)]
+        torch.cuda.synchronize()
+        for a, r in zip(got, ref):
+            assert torch.equal(a, r)
+        del others
+
+
+def test_offsets_past_32_bits_in_products(jg):
+    """The same on the tensor-core path: a classifier whose W passes 2^31
+    elements, a gate whose h does, a linear layer whose dout does."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows, dim, M = (1 << 20) + 3, 2056, 40
+    big = torch.randn(rows, dim, device="cuda", generator=g, dtype=torch.bfloat16)
+    inp = (torch.randn(M, dim, device="cuda", generator=g) / 45).bfloat16()
+    lab = torch.randint(0, rows, (M,), device="cuda", generator=g)
+    lab[:3] = torch.tensor([rows - 1, rows - 2, 0])
+    loss, lse = jg.linear_ce_fwd(inp, big, None, lab)
+    z = torch.cat([inp.double() @ big[i:i + 65536].double().T for i in range(0, rows, 65536)], 1)
+    ref = torch.logsumexp(z, 1)
+    # 2056 products a logit, 2^-23 each at most, of logits of size 1
+    assert (lse.double() - ref).abs().max() < 1e-4
+    assert (loss.double() - (ref - z.gather(1, lab[:, None])[:, 0])).abs().max() < 2e-4
+    dx, dW, db = jg.linear_ce_bwd(1.0, inp, big, None, lab, lse)
+    tail = slice(rows - 5, rows)
+    dz = torch.exp(z - ref[:, None])
+    dz[torch.arange(M, device="cuda"), lab] -= 1
+    # dz and the results are rounded to bf16, half a step each
+    want = dz[:, tail].T @ inp.double()
+    assert (dW[tail].double() - want).abs().max() <= 2 ** -7 * want.abs().max()
+    want = sum(dz[:, i:i + 65536] @ big[i:i + 65536].double() for i in range(0, rows, 65536))
+    assert (dx.double() - want).norm() <= 2 ** -7 * want.norm()
+    del z, dz, dW
+    # dout = big, K = 8
+    A = torch.randn(rows, 8, device="cuda", generator=g).bfloat16()
+    W = torch.randn(dim, 8, device="cuda", generator=g).bfloat16()
+    dA, dW, db = jg.linear_bwd(big, A, W)
+    want = big[tail].double() @ W.double()
+    assert (dA[tail].double() - want).norm() <= 2 ** -7 * want.norm()
+    want = sum(big[i:i + 65536].double().T @ A[i:i + 65536].double() for i in range(0, rows, 65536))
+    assert (dW.double() - want).norm() <= 2 ** -7 * want.norm()
+    want = sum(big[i:i + 65536].double().sum(0) for i in range(0, rows, 65536))
+    assert (db.double() - want).abs().max() <= 2 * tb.U * rows * 0.8 * 16   # of sums of |dout| of 0.8 a row
+    # h and dh [rows, dim], D = 8
+    h = jg.gated_ffn_fwd(A, W, W)
+    gt = A[tail].double() @ W.double().T
+    want = gt * torch.sigmoid(gt) * gt
+    assert (h[tail].double() - want).norm() <= 2 ** -7 * want.norm()
+    dx, dWg, *_ = jg.gated_ffn_bwd(big, A, W, W)
+    s = torch.sigmoid(gt)
+    dh = big[tail].double()
+    want = (dh * gt * s * (1 + gt * (1 - s))) @ W.double() + (dh * gt * s) @ W.double()
+    assert (dx[tail].double() - want).norm() <= 2 ** -6 * want.norm()
     jg.ops_sync()
 
 

@@ -120,6 +120,8 @@ def test_binding_refusals():
         lambda: jg.layernorm_fwd(x, torch.zeros(7), torch.zeros(8), 1e-6),
         lambda: jg.layernorm_fwd(x.t(), torch.zeros(4), torch.zeros(4), 1e-6),
         lambda: jg.layernorm_fwd(x.double(), torch.zeros(8), torch.zeros(8), 1e-6),
+        lambda: jg.layernorm_fwd(torch.tensor(1.0), f[:1], f[:1], 1e-6),
+        lambda: jg.layernorm_bwd(torch.tensor(1.0), torch.tensor(1.0), f[:1], f[:1], f[:1]),
         lambda: jg.layernorm_bwd(x, x, torch.zeros(8), f, torch.zeros(5)),
         lambda: jg.linear_ce_fwd(x, W.half(), None, lab),
         lambda: jg.linear_ce_fwd(x, torch.zeros(6, 9), None, lab),

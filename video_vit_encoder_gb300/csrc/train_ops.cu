@@ -632,15 +632,20 @@ cudaError_t ce_join(const CeArgs& a, const float2* ms, const float* sums, const 
   return cudaGetLastError();
 }
 
-// What dz is held in units of: scale[0] = max |dloss| (1 if that is 0 or not
-// finite), scale[1] = F, and scale[2] = scale[0] (1 - smoothing) / F brings
+// What dz is held in units of: scale[0] = max |dloss| over the rows that have a
+// gradient (1 if that is 0 or not finite), scale[1] = F, and scale[2] = scale[0] (1 - smoothing) / F brings
 // products of dz back.  F is 2^14 in fp16, so that |dz| stays below fp16's
 // largest value and small probabilities stay normal numbers, and 1 in bf16.
-__global__ void __launch_bounds__(1024) dz_scale_kernel(const float* __restrict__ dloss, int M, float f,
-                                                        float smoothing, float* scale) {
+__global__ void __launch_bounds__(1024) dz_scale_kernel(const float* __restrict__ dloss,
+                                                        const int64_t* __restrict__ labels, long ignore_index, int M,
+                                                        int V, float f, float smoothing, float* scale) {
   __shared__ float sm[32];
   float m = 0.f;
-  for (int i = threadIdx.x; i < M; i += 1024) m = fmaxf(m, fabsf(dloss[i]));
+  for (int i = threadIdx.x; i < M; i += 1024) {
+    const long label = __ldg(labels + i);
+    const float d = __ldg(dloss + i);
+    if (label != ignore_index && label >= 0 && label < V) m = fmaxf(m, fabsf(d));
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = m;
@@ -778,7 +783,8 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
   JEPA_TRY_CUDA(fill(a.dtype, f, s));
   const float* unscale = nullptr;
   if (!sp) {
-    dz_scale_kernel<<<1, 1024, 0, s>>>(dloss, a.M, a.dtype == DTYPE_F16 ? 16384.f : 1.f, a.smoothing, l.scale);
+    dz_scale_kernel<<<1, 1024, 0, s>>>(dloss, a.labels, a.ignore_index, a.M, a.V,
+                                       a.dtype == DTYPE_F16 ? 16384.f : 1.f, a.smoothing, l.scale);
     JEPA_TRY_CUDA(cudaGetLastError());
     unscale = l.scale + 2;
   }

@@ -8,8 +8,10 @@ libjepa_gb300.so; torch supplies device memory and streams.
 Tensors are contiguous and on one CUDA device, which need not be the current
 one.  Work is enqueued on ``stream``, or on that device's current stream; the
 outputs and the workspace are allocated on the stream that uses them, so
-calls on several streams, and captured graphs, never share one.  Gradients
-not asked for (``needs``) are returned as None.
+calls on several streams, and captured graphs, never share one.  ``stream``
+has to have waited for whatever wrote the inputs; they may be dropped as soon
+as the call returns.  Gradients not asked for (``needs``) are returned as
+None.  The first call of a function on a device is made outside a capture.
 """
 from __future__ import annotations
 
@@ -73,15 +75,20 @@ def _workspace_bytes(query, *sizes):
 
 
 @contextlib.contextmanager
-def _place(t, stream):
+def _place(t, stream, *inputs):
     """t's device and the stream current, so that what a call allocates
-    belongs to the stream that uses it."""
+    belongs to the stream that uses it; the memory of t and of the other inputs
+    is not given out again before the stream is done with it."""
     if t.get_device() < 0:
         raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
     if stream is not None and stream.device != t.device:
         raise ValueError(f"stream is on {stream.device}, tensors are on {t.device}")
     with torch.cuda.device(t.device), torch.cuda.stream(stream):
         yield
+    if stream is not None:
+        for i in (t,) + inputs:
+            if torch.is_tensor(i) and i.is_cuda:
+                i.record_stream(stream)
 
 
 def _elsewhere(t, stream):
@@ -95,6 +102,8 @@ def layernorm_fwd(x, w, b, eps, out_dtype=None, stream=None):
     [dim].  y has out_dtype (default x's; another one needs float32 x), mean
     and rstd are float32 of x's leading shape."""
     shape, dt, dev = x.shape, x.dtype, x.device
+    if not shape:
+        raise ValueError("x must have at least one dimension")
     dim, lead = shape[-1], shape[:-1]
     out_dtype = out_dtype or dt
     xc, yc = _code("x", dt), _code("out_dtype", out_dtype)
@@ -102,7 +111,7 @@ def layernorm_fwd(x, w, b, eps, out_dtype=None, stream=None):
     _expect("w", w, (dim,), _f32, dev)
     _expect("b", b, (dim,), _f32, dev)
     if _elsewhere(x, stream):
-        with _place(x, stream):
+        with _place(x, stream, w, b):
             return layernorm_fwd(x, w, b, eps, out_dtype)
     y = _empty(shape, dtype=out_dtype, device=dev)
     mean, rstd = _empty(lead, dtype=_f32, device=dev), _empty(lead, dtype=_f32, device=dev)
@@ -116,6 +125,8 @@ def layernorm_bwd(dy, x, w, mean, rstd, residual=None, needs=(True, True), strea
     mean and rstd.  residual: x's shape and dtype, added to dx.  needs: (dw,
     db)."""
     shape, dt, dev = x.shape, x.dtype, x.device
+    if not shape:
+        raise ValueError("x must have at least one dimension")
     dim, lead = shape[-1], shape[:-1]
     xc, yc = _code("x", dt), _code("dy", dy.dtype)
     _expect("x", x, shape, dt, dev)
@@ -125,7 +136,7 @@ def layernorm_bwd(dy, x, w, mean, rstd, residual=None, needs=(True, True), strea
     _expect("rstd", rstd, lead, _f32, dev)
     _expect("residual", residual, shape, dt, dev)
     if _elsewhere(x, stream):
-        with _place(x, stream):
+        with _place(x, stream, dy, w, mean, rstd, residual):
             return layernorm_bwd(dy, x, w, mean, rstd, residual, needs)
     rows = lead.numel()
     dx = _empty(shape, dtype=dt, device=dev)
@@ -159,7 +170,7 @@ def linear_ce_fwd(x, W, bias, labels, ignore_index=-100, smoothing=0.0, stream=N
     Rows with label ignore_index have loss 0."""
     M, D, V, code = _ce_args(x, W, bias, labels)
     if _elsewhere(x, stream):
-        with _place(x, stream):
+        with _place(x, stream, W, bias, labels):
             return linear_ce_fwd(x, W, bias, labels, ignore_index, smoothing)
     dev = x.device
     lab, x, W = labels.long(), _a16(x), _a16(W)
@@ -180,7 +191,7 @@ def linear_ce_bwd(dloss, x, W, bias, labels, lse, ignore_index=-100, smoothing=0
     M, D, V, code = _ce_args(x, W, bias, labels)
     _expect("lse", lse, (M,), _f32, x.device)
     if _elsewhere(x, stream):
-        with _place(x, stream):
+        with _place(x, stream, dloss, W, bias, labels, lse):
             return linear_ce_bwd(dloss, x, W, bias, labels, lse, ignore_index, smoothing, needs)
     dt, dev = x.dtype, x.device
     if not torch.is_tensor(dloss):
@@ -220,7 +231,7 @@ def gated_ffn_fwd(x, Wg, Wu, bg=None, bu=None, act="silu", stream=None):
     Wg, Wu [F, D]; bg, bu float [F] or None; act 'silu' or 'gelu' (erf)."""
     M, D, F, code, a = _ffn_args(x, Wg, Wu, bg, bu, act)
     if _elsewhere(x, stream):
-        with _place(x, stream):
+        with _place(x, stream, Wg, Wu, bg, bu):
             return gated_ffn_fwd(x, Wg, Wu, bg, bu, act)
     dev = x.device
     x, Wg, Wu = _a16(x), _a16(Wg), _a16(Wu)
@@ -238,7 +249,7 @@ def gated_ffn_bwd(dh, x, Wg, Wu, bg=None, bu=None, act="silu", needs=(True, True
     M, D, F, code, a = _ffn_args(x, Wg, Wu, bg, bu, act)
     _expect("dh", dh, (M, F), x.dtype, x.device)
     if _elsewhere(x, stream):
-        with _place(x, stream):
+        with _place(x, stream, dh, Wg, Wu, bg, bu):
             return gated_ffn_bwd(dh, x, Wg, Wu, bg, bu, act, needs)
     dt, dev = x.dtype, x.device
     dh, x, Wg, Wu = _a16(dh), _a16(x), _a16(Wg), _a16(Wu)
@@ -267,7 +278,7 @@ def linear_bwd(dout, A, W, bias=True, needs=(True, True), stream=None):
     _expect("W", W, (N, K), dt, dev)
     _expect("dout", dout, (M, N), dt, dev)
     if _elsewhere(A, stream):
-        with _place(A, stream):
+        with _place(A, stream, dout, W):
             return linear_bwd(dout, A, W, bias, needs)
     dout, A, W = _a16(dout), _a16(A), _a16(W)
     dA = _empty((M, K), dtype=dt, device=dev) if needs[0] else None
