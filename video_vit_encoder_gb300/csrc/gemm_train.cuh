@@ -157,21 +157,27 @@ struct Walk {
 struct Unit {
   int job, m, n0, nr, run_index, z, split, kb0, kb1;
 };
+template <int EPI>
 __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
   Unit t;
-  t.job = u >= p.units[0] ? 1 : 0;
+  t.job = EPI == REDUCE && u >= p.units[0] ? 1 : 0;
   if (t.job) u -= p.units[0];
   const Job& j = p.j[t.job];
-  const int runs = (j.num_n + p.run - 1) / p.run;
-  const int tiles = j.num_m * runs;
-  const int q = u / tiles;
-  const int r = u - q * tiles;
-  t.split = q / j.nz;
-  t.z = q - t.split * j.nz;
+  // dividing is what takes time here: only CE_FWD has longer runs, only REDUCE splits, and most groups are full
+  const int runs = EPI == CE_FWD ? (j.num_n + p.run - 1) / p.run : j.num_n;
+  t.split = t.z = 0;
+  int r = u;
+  if constexpr (EPI == REDUCE) {
+    const int tiles = j.num_m * runs;
+    const int q = u / tiles;
+    r = u - q * tiles;
+    t.split = q / j.nz;
+    t.z = q - t.split * j.nz;
+  }
   const int group = kGroupM * runs;
-  const int gi = r / group, w = r - gi * group;
+  const int gi = (int)((unsigned)r / (unsigned)group), w = r - gi * group;
   const int gm = min(j.num_m - gi * kGroupM, kGroupM);
-  t.run_index = w / gm;
+  t.run_index = gm == kGroupM ? w / kGroupM : w / gm;
   t.m = gi * kGroupM + (w - t.run_index * gm);
   t.n0 = t.run_index * p.run;
   t.nr = min(p.run, j.num_n - t.n0);
@@ -251,32 +257,90 @@ __device__ __forceinline__ void add_bias(const float* bias, int col, int n, floa
   }
 }
 
-// Column sums over the warp's 32 rows of 32 columns, written to part[0 .. n):
-// the block goes through the staging buffer (its last store has to have been
-// read), a lane sums 16 rows of two columns, and the two row groups are joined.
-__device__ __forceinline__ void col_sum32(const float* v, uint8_t* buf, int lane, float* part, int n) {
-  uint8_t* row = buf + lane * 128;
+// The backward epilogues (CE_BWD, GATE_BWD) hold their 32 rows x 2 x 64 columns
+// in 8 x 8 blocks, as stmatrix and ldmatrix do: v[32 c + 4 g + e] with c = 2 h +
+// q is row 16 h + 8 (e / 2) + lane / 4, column 8 g + 2 (lane % 4) + e % 2 of the
+// q-th 64 columns.  Four rows of a column are in one thread and eight threads
+// share it, so that column sums cost 28 shuffles instead of a pass of fp32
+// values through shared memory, whose bandwidth the main loop needs (with rows
+// in threads: FRAG_BEFORE).
+__device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Where the pair of columns of block g and the rows lane / 4 + 8 i lies in v.
+__device__ __forceinline__ constexpr int block_at(int q, int g, int i) { return (2 * (i >> 1) + q) * 32 + g * 4 + (i & 1) * 2; }
+
+__device__ __forceinline__ void stmatrix4(uint8_t* row, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(row)), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(const uint8_t* row, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(row))
+               : "memory");
+}
+
+// A tile's biases at this thread's columns (0 past the last), loaded at once
+// while the accumulator is waited for.
+struct Biases {
+  float2 b[2][8];   // [q][g]
+};
+__device__ __forceinline__ void load_biases(Biases& t, int q, const float* bias, int col, int n, int lane) {
+  const int c = col + 2 * (lane & 3);
+  if (bias != nullptr && col + 64 <= n && (reinterpret_cast<uintptr_t>(bias) & 7) == 0) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    *reinterpret_cast<float4*>(row + ((k ^ (lane & 7)) << 4)) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-  __syncwarp();
-  // lane (g, k) sums rows 16 g .. 16 g + 15 of columns 2 k, 2 k + 1
-  const int k = lane & 15, g = lane >> 4;
-  float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
+    for (int g = 0; g < 8; ++g) t.b[q][g] = __ldg(reinterpret_cast<const float2*>(bias + c + 8 * g));
+  } else {
 #pragma unroll
-  for (int r = 0; r < 16; r += 2) {
-    const float2 q = *reinterpret_cast<const float2*>(buf + (g * 16 + r) * 128 + (((k >> 1) ^ (r & 7)) << 4) + (k & 1) * 8);
-    const float2 p = *reinterpret_cast<const float2*>(buf + (g * 16 + r + 1) * 128 + (((k >> 1) ^ ((r + 1) & 7)) << 4) + (k & 1) * 8);
-    add2f(s0, s1, q.x, q.y);
-    add2f(t0, t1, p.x, p.y);
+    for (int g = 0; g < 8; ++g) {
+      const int k = c + 8 * g;
+      t.b[q][g].x = bias != nullptr && k < n ? __ldg(bias + k) : 0.f;
+      t.b[q][g].y = bias != nullptr && k + 1 < n ? __ldg(bias + k + 1) : 0.f;
+    }
   }
-  s0 += t0;
-  s1 += t1;
-  s0 += __shfl_xor_sync(0xffffffffu, s0, 16);
-  s1 += __shfl_xor_sync(0xffffffffu, s1, 16);
-  __syncwarp();   // the buffer has been read
-  const int c = 2 * k + g;
-  if (c < n) part[c] = g == 0 ? s0 : s1;
+}
+
+// This thread's part of the column sums of block column (q, g): its four rows.
+__device__ __forceinline__ void sum_rows(const float (&v)[128], int q, int g, float& s0, float& s1) {
+  const int a = block_at(q, g, 0), b = block_at(q, g, 1), c = block_at(q, g, 2), d = block_at(q, g, 3);
+  s0 = v[a];
+  s1 = v[a + 1];
+  add2f(s0, s1, v[b], v[b + 1]);
+  float t0 = v[c], t1 = v[c + 1];
+  add2f(t0, t1, v[d], v[d + 1]);
+  add2f(s0, s1, t0, t1);
+}
+// s[16 q + 2 g + e % 2] over the eight threads of each column: every step hands
+// over half of what is left.  Columns below n0 of q = 0 go to part0, below n1 of
+// q = 1 to part1.
+__device__ __forceinline__ void col_sums(float (&s)[32], int lane, float* part0, int n0, float* part1, int n1) {
+#pragma unroll
+  for (int half = 16; half >= 4; half >>= 1) {
+    const bool up = (lane & half) != 0;
+#pragma unroll
+    for (int j = 0; j < half; ++j) {
+      const float keep = up ? s[half + j] : s[j], give = up ? s[j] : s[half + j];
+      s[j] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+    }
+  }
+  float* part = (lane & 16) != 0 ? part1 : part0;
+  const int n = (lane & 16) != 0 ? n1 : n0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int c = ((lane & 12) << 2) + 8 * j + 2 * (lane & 3);
+    if (c + 1 < n) *reinterpret_cast<float2*>(part + c) = make_float2(s[2 * j], s[2 * j + 1]);
+    else if (c < n) part[c] = s[2 * j];
+  }
 }
 
 // This warp's 32 x 128-byte block of C at column x, row y, from each lane's row
@@ -327,21 +391,35 @@ __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 64 columns v[at ..] of an intermediate operand (dz, dg, du): the type's
+// The q-th 64 columns of an intermediate operand (dz, dg, du): the type's
 // rounding, or three bf16 planes, each the rounding of what the ones before
 // leave (v is used up).
 template <typename T, bool SPLIT>
-__device__ __forceinline__ void emit_operand(const Params& p, const CUtensorMap* c, float (&v)[128], int at,
+__device__ __forceinline__ void emit_operand(const Params& p, const CUtensorMap* c, float (&v)[128], int q,
                                              uint8_t* buf, int lane, int x, int y) {
 #pragma unroll
   for (int pl = 0; pl < (SPLIT ? 3 : 1); ++pl) {
-    emit(c, buf, lane, x, y + pl * p.c_plane, false, [&](int k) {
-      const float* q = v + at + 8 * k;
-      return make_uint4(pack2<T>(q[0], q[1]), pack2<T>(q[2], q[3]), pack2<T>(q[4], q[5]), pack2<T>(q[6], q[7]));
-    });
-    if (SPLIT && pl < 2) {
+    if (lane == 0) bulk_wait_read_all();   // the previous store has read the buffer
+    __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 64; ++j) v[at + j] -= DT<T>::to(DT<T>::from(v[at + j]));
+    for (int g = 0; g < 8; ++g) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = block_at(q, g, i);
+        w[i] = pack2<T>(v[at], v[at + 1]);
+        if (SPLIT && pl < 2) {
+          v[at] -= DT<T>::to(DT<T>::from(v[at]));
+          v[at + 1] -= DT<T>::to(DT<T>::from(v[at + 1]));
+        }
+      }
+      stmatrix4(buf + lane * 128 + ((g ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(c, buf, x, y + pl * p.c_plane);
+      bulk_commit_group();
     }
   }
 }
@@ -421,86 +499,144 @@ __device__ __forceinline__ void ce_fwd_tile(const Params& p, float (&v)[128], in
   }
 }
 
-// What the cross entropy's gradient needs of a thread's row.  A row that takes
-// no part (past M, ignored, bad label) gets zeros.
-struct RowGrad {
-  bool part;
-  int label;      // the label's column of this piece, if it lies in it
-  float l2, g;    // lse in base 2, the row's factor
+// What the cross entropy's gradient needs of a thread's four rows, row0 + lane / 4
+// + 8 i.  A row that takes no part (past M, ignored, bad label) gets zeros.
+struct RowGrads {
+  float l2[4], g[4];   // lse in base 2, the row's factor
+  int label[4];        // the label's column of this piece, if it lies in it
+  int part;            // bit i: the row takes part
+};
+struct RowLoads {
+  long y[4];
+  float lse[4], dl[4], unit, factor;
 };
 template <bool SPLIT>
-__device__ __forceinline__ RowGrad ce_bwd_row(const Params& p, int row, bool report) {
+__device__ __forceinline__ void load_rows(RowLoads& r, const Params& p, int row0, int lane) {
   const EpiArgs& ep = p.ep;
-  RowGrad r{false, -1, 0.f, 0.f};
-  if (row < p.j[0].M) {
-    const long y = __ldg(reinterpret_cast<const long long*>(ep.labels) + row);
-    const float lse = __ldg(ep.lse + row), dl = __ldg(ep.dloss + row);
-    r.part = y != ep.ignore_index && y >= 0 && y < ep.V;
-    if (r.part) {
-      r.label = (int)y - ep.v0;
-      r.l2 = lse * kLog2e;
-      r.g = dl;
-      if constexpr (!SPLIT) r.g = dl / __ldg(ep.dz_scale) * __ldg(ep.dz_scale + 1);
-    } else if (y != ep.ignore_index && report) {
-      atomicOr(p.status, DEV_BAD_INDEX);
-    }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = min(row0 + (lane >> 2) + 8 * i, p.j[0].M - 1);
+    r.y[i] = __ldg(reinterpret_cast<const long long*>(ep.labels) + row);
+    r.lse[i] = __ldg(ep.lse + row);
+    r.dl[i] = __ldg(ep.dloss + row);
+  }
+  if constexpr (!SPLIT) {
+    r.unit = __ldg(ep.dz_scale);
+    r.factor = __ldg(ep.dz_scale + 1);
+  }
+}
+template <bool SPLIT>
+__device__ __forceinline__ RowGrads ce_bwd_rows(const RowLoads& l, const Params& p, int row0, int lane, bool report) {
+  RowGrads r;
+  r.part = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool in = row0 + (lane >> 2) + 8 * i < p.j[0].M && l.y[i] != p.ep.ignore_index;
+    const bool part = in && l.y[i] >= 0 && l.y[i] < p.ep.V;
+    r.part |= part ? 1 << i : 0;
+    r.label[i] = part ? (int)l.y[i] - p.ep.v0 : -1;
+    r.l2[i] = part ? l.lse[i] * kLog2e : 0.f;
+    r.g[i] = part ? (SPLIT ? l.dl[i] : l.dl[i] / l.unit * l.factor) : 0.f;
+    if (in && !part && report) atomicOr(p.status, DEV_BAD_INDEX);
   }
   return r;
 }
 
-template <typename T, bool SPLIT>
-__device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], const RowGrad& rg, int row, int col0,
-                                            uint8_t* buf, int lane) {
+// Asks for what the epilogue of a pair's next tile reads: the lines of 32 rows'
+// labels, lse and dloss, of dh, and of the biases.
+__device__ __forceinline__ void prefetch_l1(const void* q) { asm volatile("prefetch.global.L1 [%0];" ::"l"(q)); }
+__device__ __forceinline__ void prefetch_l2(const void* q) { asm volatile("prefetch.global.L2 [%0];" ::"l"(q)); }
+template <typename T, bool SPLIT, int EPI>
+__device__ __forceinline__ void prefetch_tile(const Params& p, int row0, int col, int lane) {
   const EpiArgs& ep = p.ep;
-  const bool part = rg.part;
-  const int label = rg.label;
-  const float l2 = rg.l2, g = rg.g;
+  const int row = min(row0 + lane, p.j[0].M - 1), N = p.j[0].N;
+  if constexpr (EPI == CE_BWD) {
+    if ((lane & 15) == 0) prefetch_l1(ep.labels + row);
+    if (lane == 0) prefetch_l1(ep.lse + row);
+    if (lane == 0) prefetch_l1(ep.dloss + row);
+    if (ep.bias != nullptr && lane < 4) prefetch_l1(ep.bias + min(col + 32 * lane, N - 1));
+  } else {
+    if (ep.bias != nullptr && lane < 2) prefetch_l1(ep.bias + min(col + 32 * lane, N - 1));
+    if (ep.bias2 != nullptr && lane < 2) prefetch_l1(ep.bias2 + min(col + 32 * lane, N - 1));
+    using TD = typename std::conditional<SPLIT, float, T>::type;
+    const TD* dh = static_cast<const TD*>(ep.dh) + (size_t)row * N;
+    prefetch_l2(dh + min(col, N - 1));
+    prefetch_l2(dh + min(col + 63, N - 1));
+  }
+}
+
+template <typename T, bool SPLIT>
+__device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], const RowGrads& rg, const Biases& bias,
+                                            int row0, int col0, uint8_t* buf, int lane) {
+  const EpiArgs& ep = p.ep;
+  const int N = p.j[0].N;
   // 16-bit dz is held as g ((p - e / V) / (1 - e) - [v = y]) with g = dloss / max |dloss| (times 2^14 in fp16): with one
   // dloss for all rows, as a mean's, the label's entry is then near -1, which 16 bits hold exactly.  (As dloss (p - (1 - e)
   // [v = y] - e / V) those entries, which make up most of dx and dW, were all off by the same rounding of dloss: dx and
   // dW 3.0e-3 from the exact gradients in norm instead of 1.7e-3 at 1999 x 768 x 50021 in bf16.)
   const float uni = ep.smoothing / (float)ep.V;
   const float cs = SPLIT ? 1.0f : 1.0f / (1.0f - ep.smoothing), hit = SPLIT ? 1.0f - ep.smoothing : 1.0f;
-  const int y = row - lane;
-  if (ep.col_part != nullptr) {
-    if (lane == 0) bulk_wait_read_all();
-    __syncwarp();
-  }
+  const int lc = 2 * (lane & 3);
+  const bool whole = __all_sync(0xffffffffu, rg.part == 15);
+  float s[32];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int cc = col0 + c * 32;
-    float* w = v + c * 32;
-    if (cc >= p.j[0].N) continue;
+  for (int q = 0; q < 2; ++q) {
+    const int cc = col0 + q * 64;
+    if (cc >= N) continue;
     // columns past N keep finite values: nothing reads them
-    if (ep.bias != nullptr) add_bias(ep.bias, cc, p.j[0].N, 0.f, w);
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      fma2(w[j], w[j + 1], kLog2e, -l2);
-      w[j] = ex2(w[j]);
-      w[j + 1] = ex2(w[j + 1]);
-    }
-    if (ep.smoothing > 0.f) {
+    for (int g = 0; g < 8; ++g) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) fma2(w[j], w[j + 1], cs, -uni * cs);
-    }
-    const int ly = label - cc;
-    if (part && ly >= 0 && ly < 32) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) w[j] = j == ly ? w[j] - hit : w[j];
+      for (int i = 0; i < 4; ++i) {
+        float& z0 = v[block_at(q, g, i)];
+        float& z1 = v[block_at(q, g, i) + 1];
+        add2f(z0, z1, bias.b[q][g].x, bias.b[q][g].y);
+        fma2(z0, z1, kLog2e, -rg.l2[i]);
+        z0 = ex2(z0);
+        z1 = ex2(z1);
+        if (ep.smoothing > 0.f) fma2(z0, z1, cs, -uni * cs);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) mul2(w[j], w[j + 1], g);
-    if (!part) {
+    for (int i = 0; i < 4; ++i) {
+      const int ly = rg.label[i] - cc;
+      if (__any_sync(0xffffffffu, ly >= 0 && ly < 64)) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) w[j] = 0.f;
+        for (int g = 0; g < 8; ++g) {
+          const int at = block_at(q, g, i);
+          v[at] -= ly == 8 * g + lc ? hit : 0.f;
+          v[at + 1] -= ly == 8 * g + lc + 1 ? hit : 0.f;
+        }
+      }
     }
-    // its column sums, while the next 32 columns are computed
-    if (ep.col_part != nullptr)
-      col_sum32(w, buf, lane, ep.col_part + (size_t)(y >> 5) * ep.ld_col + cc, y < p.j[0].M ? p.j[0].N - cc : 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int g = 0; g < 8; ++g) mul2(v[block_at(q, g, i)], v[block_at(q, g, i) + 1], rg.g[i]);
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool part = (rg.part >> i & 1) != 0;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          float& z0 = v[block_at(q, g, i)];
+          float& z1 = v[block_at(q, g, i) + 1];
+          z0 = part ? z0 : 0.f;
+          z1 = part ? z1 : 0.f;
+        }
+      }
+    }
+    if (ep.col_part != nullptr) {
+#pragma unroll
+      for (int g = 0; g < 8; ++g) sum_rows(v, q, g, s[16 * q + 2 * g], s[16 * q + 2 * g + 1]);
+    }
+    emit_operand<T, SPLIT>(p, &p.j[0].c[0], v, q, buf, lane, cc, row0);
   }
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-    if (col0 + c * 64 < p.j[0].N) emit_operand<T, SPLIT>(p, &p.j[0].c[0], v, c * 64, buf, lane, col0 + c * 64, y);
+  if (ep.col_part != nullptr) {
+    float* part = ep.col_part + (size_t)(row0 >> 5) * ep.ld_col + col0;
+    const int n = row0 < p.j[0].M ? N - col0 : 0;
+    col_sums(s, lane, part, n, part + 64, n - 64);
+  }
 }
 
 // Copies this warp's 32 x 64 block of dh into the staging buffer (swizzled as
@@ -523,15 +659,10 @@ __device__ __forceinline__ void fetch_dh(const Params& p, uint8_t* buf, int lane
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// 64 output columns col .. col + 63 from the gates v[0..63] and the ups v[64..127].
-template <typename T, bool SPLIT, int ACT, bool BWD>
-__device__ __forceinline__ void gate_tile(const Params& p, float (&v)[128], int row, int col, uint8_t* buf, int lane) {
-  using TD = typename std::conditional<SPLIT, float, T>::type;   // the operator's type
+// 64 columns of h from the gates v[0 .. 63] and the ups v[64 .. 127] of a row.
+template <typename T, bool SPLIT, int ACT>
+__device__ __forceinline__ void gate_fwd_tile(const Params& p, float (&v)[128], int row, int col, uint8_t* buf, int lane) {
   const EpiArgs& ep = p.ep;
-  if constexpr (BWD && !SPLIT) {
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncwarp();
-  }
   if (col >= p.j[0].N) return;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -540,60 +671,14 @@ __device__ __forceinline__ void gate_tile(const Params& p, float (&v)[128], int 
     float* u = v + 64 + h * 32;
     if (ep.bias != nullptr) add_bias(ep.bias, cc, p.j[0].N, 0.f, g);
     if (ep.bias2 != nullptr) add_bias(ep.bias2, cc, p.j[0].N, 0.f, u);
-    if constexpr (!BWD) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        float a, da;
-        gate<ACT, false>(g[j], a, da);
-        g[j] = a * u[j];
-      }
-    } else {
-      constexpr int kPer = 16 / sizeof(TD);   // values of dh in 16 bytes
-      const TD* dh = static_cast<const TD*>(ep.dh) + (size_t)row * p.j[0].N + cc;
-#pragma unroll
-      for (int j = 0; j < 32; j += kPer) {
-        TD d[kPer];
-        if (ep.dh_vec) {
-          uint4 q;
-          if constexpr (!SPLIT)   // fetch_dh has put it into the staging buffer
-            q = *reinterpret_cast<const uint4*>(buf + lane * 128 + (((h * 4 + j / 8) ^ (lane & 7)) << 4));
-          else   // rows are multiples of 16 bytes: a piece is inside or outside as a whole
-            q = row < p.j[0].M && cc + j < p.j[0].N ? __ldg(reinterpret_cast<const uint4*>(dh + j)) : make_uint4(0, 0, 0, 0);
-          memcpy(d, &q, 16);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) d[i] = row < p.j[0].M && cc + j + i < p.j[0].N ? dh[j + i] : DT<TD>::from(0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          float a, da;
-          gate<ACT, true>(g[j + i], a, da);
-          const float dd = DT<TD>::to(d[i]);
-          g[j + i] = dd * u[j + i] * da;
-          u[j + i] = dd * a;
-        }
-      }
+    for (int j = 0; j < 32; ++j) {
+      float a, da;
+      gate<ACT, false>(g[j], a, da);
+      g[j] = a * u[j];
     }
   }
-  if constexpr (BWD) {
-    const int y = row - lane;
-    __syncwarp();   // dh has been read from the staging buffer
-    if (ep.col_part != nullptr || ep.col_part2 != nullptr) {
-      if (lane == 0) bulk_wait_read_all();
-      __syncwarp();
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float* part = k == 0 ? ep.col_part : ep.col_part2;
-        if (part == nullptr) continue;
-        float* to = part + (size_t)(y >> 5) * ep.ld_col + col;
-        const int n = y < p.j[0].M ? p.j[0].N - col : 0;
-        col_sum32(v + k * 64, buf, lane, to, n);
-        col_sum32(v + k * 64 + 32, buf, lane, to + 32, n - 32);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) emit_operand<T, SPLIT>(p, &p.j[0].c[k], v, k * 64, buf, lane, col, y);
-  } else if constexpr (!SPLIT) {
+  if constexpr (!SPLIT) {
     auto put = [&](int k) {
       const float* q = v + 8 * k;
       return make_uint4(pack2<T>(q[0], q[1]), pack2<T>(q[2], q[3]), pack2<T>(q[4], q[5]), pack2<T>(q[6], q[7]));
@@ -612,6 +697,73 @@ __device__ __forceinline__ void gate_tile(const Params& p, float (&v)[128], int 
       if (p.plain == nullptr) emit(&p.j[0].c[0], buf, lane, cc, row - lane, false, put);
       else emit_plain(static_cast<float*>(p.plain), p.plain_ld, p.j[0].M, p.j[0].N, buf, lane, cc, row - lane, put);
     }
+  }
+}
+
+// dg and du of 64 columns: gates are the blocks of q = 0, ups those of q = 1.
+template <typename T, bool SPLIT, int ACT>
+__device__ __forceinline__ void gate_bwd_tile(const Params& p, float (&v)[128], const Biases& bias, int row0, int col, uint8_t* buf,
+                                              int lane) {
+  using TD = typename std::conditional<SPLIT, float, T>::type;   // the operator's type
+  const EpiArgs& ep = p.ep;
+  const int M = p.j[0].M, N = p.j[0].N;
+  if constexpr (!SPLIT) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");   // fetch_dh's
+    __syncwarp();
+  }
+  if (col >= N) return;
+  const int lc = 2 * (lane & 3), row = row0 + (lane >> 2);
+  const TD* dh = static_cast<const TD*>(ep.dh) + (size_t)row * N + col + lc;
+  float s[32];
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    const int left = N - (col + 8 * g + lc);   // columns from this thread's first on
+    float2 d[4];
+    if (!SPLIT && ep.dh_vec) {
+      uint32_t w[4];
+      ldmatrix4(buf + lane * 128 + ((g ^ (lane & 7)) << 4), w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        TD t[2];
+        memcpy(t, &w[i], 4);   // of a 16-bit type
+        d[i] = make_float2(DT<TD>::to(t[0]), DT<TD>::to(t[1]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const TD* q = dh + (size_t)(8 * i) * N + 8 * g;
+        const bool in = row + 8 * i < M;
+        if (SPLIT && ep.dh_vec)   // rows are multiples of 16 bytes: a pair is inside or outside as a whole
+          d[i] = in && left > 0 ? __ldg(reinterpret_cast<const float2*>(q)) : make_float2(0.f, 0.f);
+        else
+          d[i] = make_float2(in && left > 0 ? DT<TD>::to(q[0]) : 0.f, in && left > 1 ? DT<TD>::to(q[1]) : 0.f);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float* vg = v + block_at(0, g, i);
+      float* vu = v + block_at(1, g, i);
+      add2f(vg[0], vg[1], bias.b[0][g].x, bias.b[0][g].y);
+      add2f(vu[0], vu[1], bias.b[1][g].x, bias.b[1][g].y);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float a, da;
+        gate<ACT, true>(vg[e], a, da);
+        const float dd = e == 0 ? d[i].x : d[i].y;
+        vg[e] = dd * vu[e] * da;
+        vu[e] = dd * a;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) sum_rows(v, q, g, s[16 * q + 2 * g], s[16 * q + 2 * g + 1]);
+  }
+  __syncwarp();   // dh has been read from the staging buffer
+#pragma unroll
+  for (int q = 0; q < 2; ++q) emit_operand<T, SPLIT>(p, &p.j[0].c[q], v, q, buf, lane, col, row0);
+  if (ep.col_part != nullptr || ep.col_part2 != nullptr) {
+    const size_t at = (size_t)(row0 >> 5) * ep.ld_col + col;
+    const int n = row0 < M ? N - col : 0;
+    col_sums(s, lane, ep.col_part + at, ep.col_part != nullptr ? n : 0, ep.col_part2 + at, ep.col_part2 != nullptr ? n : 0);
   }
 }
 
@@ -730,7 +882,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
         long issued = 0;
         bool stop = false;
         for (int i = 0, u; !stop && (u = walk.at(p, i)) >= 0; ++i) {
-          const Unit t = unit_of(p, u);
+          const Unit t = unit_of<EPI>(p, u);
           const Job& job = p.j[t.job];
           const bool amn = BMN && job.a_mn != 0;
           const int ra = (t.m * 2 + rank) * kBM;
@@ -795,7 +947,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
         int acc = 0;
         bool ok = true;
         for (int i = 0, u; ok && (u = walk.at(p, i)) >= 0; ++i) {
-          const Unit t = unit_of(p, u);
+          const Unit t = unit_of<EPI>(p, u);
           const bool amn = BMN && p.j[t.job].a_mn != 0;
           const uint32_t idesc = idesc_f16<T, 2 * kBM, kBN>() | (amn ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
           const uint32_t step = amn ? 128 : 2;   // 16 k on in A's descriptor
@@ -863,13 +1015,13 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
     uint8_t* buf_s = sEpi + (warp - kFirstEpi) * kEpiStage;
     int acc = 0;
     bool stop = false;
-    for (int i = 0, u; !stop && (u = walk.at(p, i)) >= 0; ++i) {
-      const Unit t = unit_of(p, u);
+    int u = walk.at(p, 0);
+    for (int i = 1; !stop && u >= 0; ++i) {
+      const Unit t = unit_of<EPI>(p, u);
+      u = walk.at(p, i);   // the next one
       const Job& job = p.j[t.job];
       const int row = (t.m * 2 + rank) * kBM + quarter * 32 + lane;
       RowStats st{-INFINITY, 0.f, 0.f};
-      RowGrad rg{};
-      if constexpr (EPI == CE_BWD) rg = ce_bwd_row<SPLIT>(p, row, t.n0 == 0 && half == 0);
       int label = -1;
       if constexpr (EPI == CE_FWD) {
         if (row < job.M) {
@@ -899,13 +1051,26 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
           if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + 8 * buf);
           ++acc;
         };
-        // of this thread's 128 columns, where the c-th 32 start (gates: this half's 64 gate columns, then its 64 up columns)
-        auto column = [&](int c) {
-          return (uint32_t)(kGate ? half * 64 + (c & 1) * 32 + (c >> 1) * (kBN / 2) : half * (kBN / 2) + c * 32);
+        // the c-th 32 values of this thread: of its row's 128 columns (gates: 64 gate columns, then the 64 up columns),
+        // or blocks (block_at)
+        auto load = [&](uint32_t tb, int c, uint32_t (&w)[32]) {
+          if constexpr (EPI == CE_BWD || EPI == GATE_BWD)
+            tmem_ld_blocks(tb + ((uint32_t)(c >> 1) << 20) +
+                               (EPI == GATE_BWD ? half * 64 + (c & 1) * (kBN / 2) : half * (kBN / 2) + (c & 1) * 64), w);
+          else
+            tmem_ld32(tb + (kGate ? half * 64 + (c & 1) * 32 + (c >> 1) * (kBN / 2) : half * (kBN / 2) + c * 32), w);
         };
         // what the epilogue reads from memory, on its way while the products run
         float warm = 0.f;
-        if constexpr (EPI >= CE_FWD) {
+        [[maybe_unused]] RowLoads rows;
+        [[maybe_unused]] Biases biases;
+        if constexpr (EPI == CE_BWD) {
+          load_rows<SPLIT>(rows, p, row - lane, lane);
+          for (int q = 0; q < 2; ++q) load_biases(biases, q, p.ep.bias, col + q * 64, job.N, lane);
+        } else if constexpr (EPI == GATE_BWD) {
+          for (int q = 0; q < 2; ++q)
+            load_biases(biases, q, q == 0 ? p.ep.bias : p.ep.bias2, (t.n0 + r) * (kBN / 2) + half * 64, job.N, lane);
+        } else if constexpr (EPI >= CE_FWD) {
           const int c = kGate ? (t.n0 + r) * (kBN / 2) + half * 64 + lane * 2 : col + lane * 4;
           const int at = min(c, job.N - 1);
           if (p.ep.bias != nullptr) warm = __ldg(p.ep.bias + at);
@@ -919,12 +1084,14 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
           break;
         }
         asm volatile("" ::"f"(warm));
+        [[maybe_unused]] RowGrads rg;
+        if constexpr (EPI == CE_BWD) rg = ce_bwd_rows<SPLIT>(rows, p, row - lane, lane, t.n0 == 0 && half == 0);
         if constexpr (kRegs) {
           {
             const uint32_t tb = tl + (acc & 1) * kBN;
             uint32_t w[4][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(tb + column(c), w[c]);
+            for (int c = 0; c < 4; ++c) load(tb, c, w[c]);
             tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -942,7 +1109,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t w[32];
-              tmem_ld32(tb + column(c), w);
+              load(tb, c, w);
               tmem_wait_ld();
 #pragma unroll
               for (int j = 0; j < 32; j += 2)
@@ -962,15 +1129,28 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
         }
         if constexpr (kRegs) {
           if (stop) break;
+          if constexpr (EPI == CE_BWD || EPI == GATE_BWD) {
+            if (u >= 0) {
+              const Unit next = unit_of<EPI>(p, u);
+              prefetch_tile<T, SPLIT, EPI>(p, (next.m * 2 + rank) * kBM + quarter * 32,
+                                           EPI == CE_BWD ? next.n0 * kBN + half * (kBN / 2) : next.n0 * (kBN / 2) + half * 64,
+                                           lane);
+            }
+          }
           if constexpr (EPI == CE_FWD) {
             if (p.ep.part_sum != nullptr) ce_fwd_tile<true>(p, v, row, col, lane, label, st);
             else ce_fwd_tile<false>(p, v, row, col, lane, label, st);
           } else if constexpr (EPI == CE_BWD) {
-            ce_bwd_tile<T, SPLIT>(p, v, rg, row, col, buf_s, lane);
+            ce_bwd_tile<T, SPLIT>(p, v, rg, biases, row - lane, col, buf_s, lane);
           } else if constexpr (kGate) {
             const int oc = (t.n0 + r) * (kBN / 2) + half * 64;
-            if (p.ep.act == ACT_SILU) gate_tile<T, SPLIT, ACT_SILU, EPI == GATE_BWD>(p, v, row, oc, buf_s, lane);
-            else gate_tile<T, SPLIT, ACT_GELU, EPI == GATE_BWD>(p, v, row, oc, buf_s, lane);
+            if constexpr (EPI == GATE_FWD) {
+              if (p.ep.act == ACT_SILU) gate_fwd_tile<T, SPLIT, ACT_SILU>(p, v, row, oc, buf_s, lane);
+              else gate_fwd_tile<T, SPLIT, ACT_GELU>(p, v, row, oc, buf_s, lane);
+            } else {
+              if (p.ep.act == ACT_SILU) gate_bwd_tile<T, SPLIT, ACT_SILU>(p, v, biases, row - lane, oc, buf_s, lane);
+              else gate_bwd_tile<T, SPLIT, ACT_GELU>(p, v, biases, row - lane, oc, buf_s, lane);
+            }
           } else {
             slab_regs(job, &job.c[t.z], v, row - lane + t.split * job.slab_rows, col, buf_s, lane, job.out == F32_ADD);
           }
