@@ -133,7 +133,12 @@ struct Walk {
     part = p.units[0] - full * nc;
   }
   // The i-th unit, counted over both jobs, or -1.
+  template <int EPI>
   __device__ __forceinline__ int at(const Params& p, int i) const {
+    if constexpr (EPI == CE_BWD || EPI == GATE_BWD) {   // one job (so have the forward passes, but they then spill 1 KB)
+      const int k = i * nc + cid;
+      return k < p.units[0] ? k : -1;
+    }
     if (i < full || (i == full && cid < part)) return i * nc + cid;
     if (p.units[1] == 0) return -1;
     i -= full + (cid < part ? 1 : 0);
@@ -159,30 +164,32 @@ struct Unit {
 };
 template <int EPI>
 __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
-  Unit t;
-  t.job = EPI == REDUCE && u >= p.units[0] ? 1 : 0;
-  if (t.job) u -= p.units[0];
+  // dividing is what takes time here: only CE_FWD has longer runs, only REDUCE has two jobs and splits, and most groups
+  // of row tiles are full
+  Unit t{};
+  if constexpr (EPI == REDUCE) {
+    t.job = u >= p.units[0] ? 1 : 0;
+    if (t.job) u -= p.units[0];
+  }
   const Job& j = p.j[t.job];
-  // dividing is what takes time here: only CE_FWD has longer runs, only REDUCE splits, and most groups are full
   const int runs = EPI == CE_FWD ? (j.num_n + p.run - 1) / p.run : j.num_n;
-  t.split = t.z = 0;
-  int r = u;
+  t.kb1 = j.kb_seg * j.nseg;
   if constexpr (EPI == REDUCE) {
     const int tiles = j.num_m * runs;
     const int q = u / tiles;
-    r = u - q * tiles;
+    u -= q * tiles;
     t.split = q / j.nz;
     t.z = q - t.split * j.nz;
+    t.kb0 = t.split * j.kb_split;
+    t.kb1 = min(t.kb0 + j.kb_split, t.kb1);
   }
   const int group = kGroupM * runs;
-  const int gi = (int)((unsigned)r / (unsigned)group), w = r - gi * group;
+  const int gi = (int)((unsigned)u / (unsigned)group), w = u - gi * group;
   const int gm = min(j.num_m - gi * kGroupM, kGroupM);
   t.run_index = gm == kGroupM ? w / kGroupM : w / gm;
   t.m = gi * kGroupM + (w - t.run_index * gm);
-  t.n0 = t.run_index * p.run;
-  t.nr = min(p.run, j.num_n - t.n0);
-  t.kb0 = t.split * j.kb_split;
-  t.kb1 = min(t.kb0 + j.kb_split, j.kb_seg * j.nseg);
+  t.n0 = EPI == CE_FWD ? t.run_index * p.run : t.run_index;
+  t.nr = EPI == CE_FWD ? min(p.run, j.num_n - t.n0) : 1;
   return t;
 }
 
@@ -290,22 +297,21 @@ __device__ __forceinline__ void ldmatrix4(const uint8_t* row, uint32_t (&r)[4]) 
                : "memory");
 }
 
-// A tile's biases at this thread's columns (0 past the last), loaded at once
-// while the accumulator is waited for.
+// The biases of 64 columns at this thread's (0 past the last), loaded at once.
 struct Biases {
-  float2 b[2][8];   // [q][g]
+  float2 b[8];   // [g]
 };
-__device__ __forceinline__ void load_biases(Biases& t, int q, const float* bias, int col, int n, int lane) {
+__device__ __forceinline__ void load_biases(Biases& t, const float* bias, int col, int n, int lane) {
   const int c = col + 2 * (lane & 3);
   if (bias != nullptr && col + 64 <= n && (reinterpret_cast<uintptr_t>(bias) & 7) == 0) {
 #pragma unroll
-    for (int g = 0; g < 8; ++g) t.b[q][g] = __ldg(reinterpret_cast<const float2*>(bias + c + 8 * g));
+    for (int g = 0; g < 8; ++g) t.b[g] = __ldg(reinterpret_cast<const float2*>(bias + c + 8 * g));
   } else {
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
       const int k = c + 8 * g;
-      t.b[q][g].x = bias != nullptr && k < n ? __ldg(bias + k) : 0.f;
-      t.b[q][g].y = bias != nullptr && k + 1 < n ? __ldg(bias + k + 1) : 0.f;
+      t.b[g].x = bias != nullptr && k < n ? __ldg(bias + k) : 0.f;
+      t.b[g].y = bias != nullptr && k + 1 < n ? __ldg(bias + k + 1) : 0.f;
     }
   }
 }
@@ -320,12 +326,13 @@ __device__ __forceinline__ void sum_rows(const float (&v)[128], int q, int g, fl
   add2f(t0, t1, v[d], v[d + 1]);
   add2f(s0, s1, t0, t1);
 }
-// s[16 q + 2 g + e % 2] over the eight threads of each column: every step hands
-// over half of what is left.  Columns below n0 of q = 0 go to part0, below n1 of
-// q = 1 to part1.
-__device__ __forceinline__ void col_sums(float (&s)[32], int lane, float* part0, int n0, float* part1, int n1) {
+// The sums s[2 g + e % 2] of 64 columns over the eight threads of each: a step
+// hands over half of what is left.  fold_sums leaves the four of blocks g / 2 =
+// (lane & 12) / 4, over half the threads; join_sums joins those of q = 0 (to
+// part0, columns below n0) and of q = 1 (to part1, columns below n1).
+__device__ __forceinline__ void fold_sums(float (&s)[16], int lane) {
 #pragma unroll
-  for (int half = 16; half >= 4; half >>= 1) {
+  for (int half = 8; half >= 4; half >>= 1) {
     const bool up = (lane & half) != 0;
 #pragma unroll
     for (int j = 0; j < half; ++j) {
@@ -333,8 +340,15 @@ __device__ __forceinline__ void col_sums(float (&s)[32], int lane, float* part0,
       s[j] = keep + __shfl_xor_sync(0xffffffffu, give, half);
     }
   }
-  float* part = (lane & 16) != 0 ? part1 : part0;
-  const int n = (lane & 16) != 0 ? n1 : n0;
+}
+__device__ __forceinline__ void join_sums(const float (&s0)[16], const float (&s1)[16], int lane, float* part0, int n0,
+                                          float* part1, int n1) {
+  const bool up = (lane & 16) != 0;
+  float s[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s[j] = (up ? s1[j] : s0[j]) + __shfl_xor_sync(0xffffffffu, up ? s0[j] : s1[j], 16);
+  float* part = up ? part1 : part0;
+  const int n = up ? n1 : n0;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int c = ((lane & 12) << 2) + 8 * j + 2 * (lane & 3);
@@ -566,7 +580,7 @@ __device__ __forceinline__ void prefetch_tile(const Params& p, int row0, int col
 }
 
 template <typename T, bool SPLIT>
-__device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], const RowGrads& rg, const Biases& bias,
+__device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], const RowGrads& rg, Biases& bias,
                                             int row0, int col0, uint8_t* buf, int lane) {
   const EpiArgs& ep = p.ep;
   const int N = p.j[0].N;
@@ -578,7 +592,7 @@ __device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], co
   const float cs = SPLIT ? 1.0f : 1.0f / (1.0f - ep.smoothing), hit = SPLIT ? 1.0f - ep.smoothing : 1.0f;
   const int lc = 2 * (lane & 3);
   const bool whole = __all_sync(0xffffffffu, rg.part == 15);
-  float s[32];
+  float s[2][16] = {};
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int cc = col0 + q * 64;
@@ -590,7 +604,7 @@ __device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], co
       for (int i = 0; i < 4; ++i) {
         float& z0 = v[block_at(q, g, i)];
         float& z1 = v[block_at(q, g, i) + 1];
-        add2f(z0, z1, bias.b[q][g].x, bias.b[q][g].y);
+        add2f(z0, z1, bias.b[g].x, bias.b[g].y);
         fma2(z0, z1, kLog2e, -rg.l2[i]);
         z0 = ex2(z0);
         z1 = ex2(z1);
@@ -626,16 +640,18 @@ __device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], co
         }
       }
     }
+    if (q == 0) load_biases(bias, ep.bias, cc + 64, N, lane);
     if (ep.col_part != nullptr) {
 #pragma unroll
-      for (int g = 0; g < 8; ++g) sum_rows(v, q, g, s[16 * q + 2 * g], s[16 * q + 2 * g + 1]);
+      for (int g = 0; g < 8; ++g) sum_rows(v, q, g, s[q][2 * g], s[q][2 * g + 1]);
+      fold_sums(s[q], lane);
     }
     emit_operand<T, SPLIT>(p, &p.j[0].c[0], v, q, buf, lane, cc, row0);
   }
   if (ep.col_part != nullptr) {
     float* part = ep.col_part + (size_t)(row0 >> 5) * ep.ld_col + col0;
     const int n = row0 < p.j[0].M ? N - col0 : 0;
-    col_sums(s, lane, part, n, part + 64, n - 64);
+    join_sums(s[0], s[1], lane, part, n, part + 64, n - 64);
   }
 }
 
@@ -702,7 +718,7 @@ __device__ __forceinline__ void gate_fwd_tile(const Params& p, float (&v)[128], 
 
 // dg and du of 64 columns: gates are the blocks of q = 0, ups those of q = 1.
 template <typename T, bool SPLIT, int ACT>
-__device__ __forceinline__ void gate_bwd_tile(const Params& p, float (&v)[128], const Biases& bias, int row0, int col, uint8_t* buf,
+__device__ __forceinline__ void gate_bwd_tile(const Params& p, float (&v)[128], const Biases (&bias)[2], int row0, int col, uint8_t* buf,
                                               int lane) {
   using TD = typename std::conditional<SPLIT, float, T>::type;   // the operator's type
   const EpiArgs& ep = p.ep;
@@ -714,7 +730,7 @@ __device__ __forceinline__ void gate_bwd_tile(const Params& p, float (&v)[128], 
   if (col >= N) return;
   const int lc = 2 * (lane & 3), row = row0 + (lane >> 2);
   const TD* dh = static_cast<const TD*>(ep.dh) + (size_t)row * N + col + lc;
-  float s[32];
+  float s[2][16] = {};
 #pragma unroll
   for (int g = 0; g < 8; ++g) {
     const int left = N - (col + 8 * g + lc);   // columns from this thread's first on
@@ -743,8 +759,8 @@ __device__ __forceinline__ void gate_bwd_tile(const Params& p, float (&v)[128], 
     for (int i = 0; i < 4; ++i) {
       float* vg = v + block_at(0, g, i);
       float* vu = v + block_at(1, g, i);
-      add2f(vg[0], vg[1], bias.b[0][g].x, bias.b[0][g].y);
-      add2f(vu[0], vu[1], bias.b[1][g].x, bias.b[1][g].y);
+      add2f(vg[0], vg[1], bias[0].b[g].x, bias[0].b[g].y);
+      add2f(vu[0], vu[1], bias[1].b[g].x, bias[1].b[g].y);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float a, da;
@@ -755,7 +771,7 @@ __device__ __forceinline__ void gate_bwd_tile(const Params& p, float (&v)[128], 
       }
     }
 #pragma unroll
-    for (int q = 0; q < 2; ++q) sum_rows(v, q, g, s[16 * q + 2 * g], s[16 * q + 2 * g + 1]);
+    for (int q = 0; q < 2; ++q) sum_rows(v, q, g, s[q][2 * g], s[q][2 * g + 1]);
   }
   __syncwarp();   // dh has been read from the staging buffer
 #pragma unroll
@@ -763,7 +779,9 @@ __device__ __forceinline__ void gate_bwd_tile(const Params& p, float (&v)[128], 
   if (ep.col_part != nullptr || ep.col_part2 != nullptr) {
     const size_t at = (size_t)(row0 >> 5) * ep.ld_col + col;
     const int n = row0 < M ? N - col : 0;
-    col_sums(s, lane, ep.col_part + at, ep.col_part != nullptr ? n : 0, ep.col_part2 + at, ep.col_part2 != nullptr ? n : 0);
+    for (int q = 0; q < 2; ++q) fold_sums(s[q], lane);
+    join_sums(s[0], s[1], lane, ep.col_part + at, ep.col_part != nullptr ? n : 0, ep.col_part2 + at,
+              ep.col_part2 != nullptr ? n : 0);
   }
 }
 
@@ -881,9 +899,9 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
         uint32_t phase = 0;
         long issued = 0;
         bool stop = false;
-        for (int i = 0, u; !stop && (u = walk.at(p, i)) >= 0; ++i) {
+        for (int i = 0, u; !stop && (u = walk.at<EPI>(p, i)) >= 0; ++i) {
           const Unit t = unit_of<EPI>(p, u);
-          const Job& job = p.j[t.job];
+          const Job& job = p.j[EPI == REDUCE ? t.job : 0];
           const bool amn = BMN && job.a_mn != 0;
           const int ra = (t.m * 2 + rank) * kBM;
           for (int r = 0; r < t.nr && !stop; ++r) {
@@ -946,7 +964,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
         uint32_t phase = 0;
         int acc = 0;
         bool ok = true;
-        for (int i = 0, u; ok && (u = walk.at(p, i)) >= 0; ++i) {
+        for (int i = 0, u; ok && (u = walk.at<EPI>(p, i)) >= 0; ++i) {
           const Unit t = unit_of<EPI>(p, u);
           const bool amn = BMN && p.j[t.job].a_mn != 0;
           const uint32_t idesc = idesc_f16<T, 2 * kBM, kBN>() | (amn ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
@@ -1015,11 +1033,11 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
     uint8_t* buf_s = sEpi + (warp - kFirstEpi) * kEpiStage;
     int acc = 0;
     bool stop = false;
-    int u = walk.at(p, 0);
+    int u = walk.at<EPI>(p, 0);
     for (int i = 1; !stop && u >= 0; ++i) {
       const Unit t = unit_of<EPI>(p, u);
-      u = walk.at(p, i);   // the next one
-      const Job& job = p.j[t.job];
+      u = walk.at<EPI>(p, i);   // the next one
+      const Job& job = p.j[EPI == REDUCE ? t.job : 0];
       const int row = (t.m * 2 + rank) * kBM + quarter * 32 + lane;
       RowStats st{-INFINITY, 0.f, 0.f};
       int label = -1;
@@ -1063,13 +1081,13 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
         // what the epilogue reads from memory, on its way while the products run
         float warm = 0.f;
         [[maybe_unused]] RowLoads rows;
-        [[maybe_unused]] Biases biases;
+        [[maybe_unused]] Biases biases[EPI == GATE_BWD ? 2 : 1];
         if constexpr (EPI == CE_BWD) {
           load_rows<SPLIT>(rows, p, row - lane, lane);
-          for (int q = 0; q < 2; ++q) load_biases(biases, q, p.ep.bias, col + q * 64, job.N, lane);
+          load_biases(biases[0], p.ep.bias, col, job.N, lane);
         } else if constexpr (EPI == GATE_BWD) {
           for (int q = 0; q < 2; ++q)
-            load_biases(biases, q, q == 0 ? p.ep.bias : p.ep.bias2, (t.n0 + r) * (kBN / 2) + half * 64, job.N, lane);
+            load_biases(biases[q], q == 0 ? p.ep.bias : p.ep.bias2, (t.n0 + r) * (kBN / 2) + half * 64, job.N, lane);
         } else if constexpr (EPI >= CE_FWD) {
           const int c = kGate ? (t.n0 + r) * (kBN / 2) + half * 64 + lane * 2 : col + lane * 4;
           const int at = min(c, job.N - 1);
@@ -1141,7 +1159,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
             if (p.ep.part_sum != nullptr) ce_fwd_tile<true>(p, v, row, col, lane, label, st);
             else ce_fwd_tile<false>(p, v, row, col, lane, label, st);
           } else if constexpr (EPI == CE_BWD) {
-            ce_bwd_tile<T, SPLIT>(p, v, rg, biases, row - lane, col, buf_s, lane);
+            ce_bwd_tile<T, SPLIT>(p, v, rg, biases[0], row - lane, col, buf_s, lane);
           } else if constexpr (kGate) {
             const int oc = (t.n0 + r) * (kBN / 2) + half * 64;
             if constexpr (EPI == GATE_FWD) {
