@@ -347,14 +347,19 @@ cudaError_t reduce_output(int dtype, const Reduce& rd, Job& j, int z, void* out,
 }
 
 // K blocks between the register sums of a 16-bit product with fp32 results.
-// 8 (512 k) cost next to nothing where a tile's products hide the sums (cross
-// entropy backward, 4096 x 1024 x 32768: 0.54 ms, in one go 0.53, with 4
-// blocks 0.62, with 2 blocks 0.65).  Column sums (dbias) over few classes
-// cancel, so that the truncation shows: at 1789 x 448 x 12 they are 4.9e-6 off
-// with 8 blocks.  Such products have few tiles, and few blocks are affordable.
+// CE_FWD hides the sums behind its products: 8 (512 k), logits then lose less
+// than 2^-20 of themselves.  Column sums (dbias) of many tiles take up to 12
+// blocks, evenly: a sum less is 5% of a whole backward pass (1999 x 768 x 50021
+// 344 us with 8 + 4, 326 in one go), and dbias is 6e-7 off in norm; in one go
+// over 16 blocks it would be 1.9e-6 (4096 x 1024 x 32768).  Over few classes
+// they cancel, so that the truncation shows: at 1789 x 448 x 12 they are 4.9e-6
+// off with 8 blocks.  Such products have few tiles, and few blocks are
+// affordable.
 int chunk_blocks(const Job& j, bool column_sums) {
   const long tiles = (long)j.num_m * j.num_n;
-  return !column_sums || tiles > 4 * kPairs ? 8 : (tiles > kPairs ? 4 : 2);
+  if (!column_sums) return 8;
+  if (tiles > 4 * kPairs) return ceil_div(j.kb_seg, ceil_div(j.kb_seg, 12));
+  return tiles > kPairs ? 4 : 2;
 }
 
 cudaError_t gemm(int dtype, int epi, const Params& p, int num_sms, cudaStream_t s) {
