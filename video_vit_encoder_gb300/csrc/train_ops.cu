@@ -333,7 +333,7 @@ Reduce plan_reduce(int dtype, const Product& pr, int splits, bool add, Carver& c
     for (int z = 0; z < pr.nz; ++z) r.slab[z] = cv.take<float>((size_t)splits * r.mp * r.np * 4);
   return r;
 }
-// Sets j's output z; with slabs, slab_sum is still to come.
+// Sets j's output z; with slabs, finish is still to come.
 cudaError_t reduce_output(int dtype, const Reduce& rd, Job& j, int z, void* out, float* slab, bool add) {
   const long rows = j.M, N = j.N;
   j.out = add ? tg::F32_ADD : tg::F32;
@@ -393,10 +393,13 @@ cudaError_t gemm_reduce(int dtype, const Job* a, const Job* b, const PairPlan& p
   return gemm(dtype, tg::REDUCE, p, num_sms, s);
 }
 
-// out[r, c] = scale * sum over the slabs, in slab order, for up to three outputs
-// at once (grid.y).  VEC: N is the slabs' row length, 8 values a thread; else
-// one.
-struct SlabSums {
+// What is left after the products, in one launch (each launch less is 2 us of a
+// small call): outputs that went through fp32 slabs, out[r, c] = scale * sum
+// over the slabs, in slab order; and column sums from their parts, out[c] =
+// scale * sum over r of part[r, c], 32 columns a block, G threads a column,
+// each over every G-th row, joined in a fixed order.
+struct Finish {
+  // slabs
   const float* slab[3];
   long stride[3];      // from slab to slab
   int slabs[3];
@@ -404,12 +407,52 @@ struct SlabSums {
   long rows[3];
   int N, np;           // columns of the outputs and of the slabs
   int count;
+  unsigned end[3];     // of each output's blocks
+  // column sums
+  const float* part[2];
+  float* sum[2];
+  long ld;
+  int part_rows, n, sums;
+  unsigned sum_blocks; // of each
 };
+template <int G>
+__device__ __forceinline__ void part_sum(const Finish& f, int k, int block, const float* scale, float (*sm)[33]) {
+  const float* a = f.part[k];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int c = block * 32 + lane;
+  float s = 0.f;
+  if (c < f.n) {
+#pragma unroll 8
+    for (int r = g; r < f.part_rows; r += G) s += __ldg(a + (long)r * f.ld + c);
+  }
+  sm[g][lane] = s;
+  __syncthreads();
+  if (g == 0 && c < f.n) {
+    for (int j = 1; j < G; ++j) s += sm[j][lane];
+    f.sum[k][c] = scale != nullptr ? s * __ldg(scale) : s;
+  }
+}
+// Column sums of many parts.
+__global__ void __launch_bounds__(1024) part_sum_kernel(const __grid_constant__ Finish f, const float* scale) {
+  __shared__ float sm[32][33];
+  part_sum<32>(f, blockIdx.y, blockIdx.x, scale, sm);
+}
+// The column sums' blocks come first, then those of each slab output.  VEC: N is
+// the slabs' row length, 8 values a thread; else one.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kBlock) slab_sum_kernel(const __grid_constant__ SlabSums q,
-                                                          const float* __restrict__ scale) {
-  const int y = blockIdx.y;
-  const long i = (long)blockIdx.x * kBlock + threadIdx.x;
+__global__ void __launch_bounds__(kBlock) finish_kernel(const __grid_constant__ Finish q, const float* __restrict__ scale) {
+  __shared__ float sm[kBlock / 32][33];
+  unsigned block = blockIdx.x;
+  const unsigned sums = q.sums * q.sum_blocks;
+  if (block < sums) {
+    const int k = block < q.sum_blocks ? 0 : 1;
+    part_sum<kBlock / 32>(q, k, (int)(block - k * q.sum_blocks), scale, sm);
+    return;
+  }
+  block -= sums;
+  const int y = block < q.end[0] ? 0 : (block < q.end[1] ? 1 : 2);
+  if (y > 0) block -= q.end[y - 1];
+  const long i = (long)block * kBlock + threadIdx.x;
   const float sc = scale != nullptr ? __ldg(scale) : 1.f;
   T* out = static_cast<T*>(q.out[y]);
   const int n_slabs = q.slabs[y];
@@ -443,7 +486,7 @@ __global__ void __launch_bounds__(kBlock) slab_sum_kernel(const __grid_constant_
   }
 }
 // Adds an output of j that went through slabs.
-void add_slab_sum(SlabSums& q, const Reduce& rd, int z, int slabs, long slab_rows, void* out, long rows, long N) {
+void add_slab_sum(Finish& q, const Reduce& rd, int z, int slabs, long slab_rows, void* out, long rows, long N) {
   if (rd.direct || out == nullptr) return;
   const int k = q.count++;
   q.slab[k] = rd.slab[z];
@@ -454,58 +497,42 @@ void add_slab_sum(SlabSums& q, const Reduce& rd, int z, int slabs, long slab_row
   q.N = (int)N;
   q.np = (int)rd.np;
 }
+// Adds sums of n columns from `rows` rows of parts, ld apart.
+void add_part_sum(Finish& q, const float* part, float* sum, long ld, int rows, int n) {
+  if (sum == nullptr) return;
+  const int k = q.sums++;
+  q.part[k] = part;
+  q.sum[k] = sum;
+  q.ld = ld;
+  q.part_rows = rows;
+  q.n = n;
+  q.sum_blocks = blocks_for(n, 32);
+}
 template <typename T>
-cudaError_t slab_sum_t(const SlabSums& q, const float* scale, cudaStream_t s) {
-  long most = 0;
-  for (int k = 0; k < q.count; ++k) most = q.rows[k] > most ? q.rows[k] : most;
-  if (q.N % 8 == 0)
-    slab_sum_kernel<T, true><<<dim3(blocks_for(most * q.N / 8, kBlock), q.count), kBlock, 0, s>>>(q, scale);
-  else
-    slab_sum_kernel<T, false><<<dim3(blocks_for(most * q.N, kBlock), q.count), kBlock, 0, s>>>(q, scale);
+cudaError_t finish_t(Finish& q, const float* scale, cudaStream_t s) {
+  const bool vec = q.N % 8 == 0;
+  unsigned blocks = 0;
+  for (int k = 0; k < 3; ++k) {
+    if (k < q.count) blocks += blocks_for(vec ? q.rows[k] * q.N / 8 : q.rows[k] * q.N, kBlock);
+    q.end[k] = blocks;
+  }
+  blocks += q.sums * q.sum_blocks;
+  if (vec) finish_kernel<T, true><<<blocks, kBlock, 0, s>>>(q, scale);
+  else finish_kernel<T, false><<<blocks, kBlock, 0, s>>>(q, scale);
   return cudaGetLastError();
 }
-cudaError_t slab_sum(int dtype, const SlabSums& q, const float* scale, cudaStream_t s) {
-  if (q.count == 0) return cudaSuccess;
-  if (dtype == DTYPE_F32) return slab_sum_t<float>(q, scale, s);
-  return dtype == DTYPE_F16 ? slab_sum_t<__half>(q, scale, s) : slab_sum_t<__nv_bfloat16>(q, scale, s);
+cudaError_t finish(int dtype, Finish& q, const float* scale, cudaStream_t s) {
+  if (q.sums > 0 && q.part_rows > 512) {   // a launch of its own, 32 threads a column
+    part_sum_kernel<<<dim3(q.sum_blocks, q.sums), 1024, 0, s>>>(q, scale);
+    JEPA_TRY_CUDA(cudaGetLastError());
+    q.sums = 0;
+  }
+  if (q.count == 0 && q.sums == 0) return cudaSuccess;
+  if (dtype == DTYPE_F32) return finish_t<float>(q, scale, s);
+  return dtype == DTYPE_F16 ? finish_t<__half>(q, scale, s) : finish_t<__nv_bfloat16>(q, scale, s);
 }
 
 // ----------------------------------------------------------------------------- column sums
-// out[c] = scale * sum over r of a[r, c], for two matrices at once (grid.y):
-// 32 columns a block, G threads a column, each over every G-th row, joined in a
-// fixed order.  G is 32 where there are rows for them and 8 else (63 rows of
-// 50021 columns: 17 us with 32).
-struct ColSums {
-  const float* a[2];
-  float* out[2];
-};
-template <int G>
-__global__ void __launch_bounds__(32 * G) part_sum_kernel(ColSums cs, long ld, int rows, int n,
-                                                          const float* __restrict__ scale) {
-  __shared__ float sm[G][33];
-  const float* a = cs.a[blockIdx.y];
-  float* out = cs.out[blockIdx.y];
-  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float s = 0.f;
-  if (c < n) {
-#pragma unroll 8
-    for (int r = g; r < rows; r += G) s += __ldg(a + (long)r * ld + c);
-  }
-  sm[g][lane] = s;
-  __syncthreads();
-  if (g == 0 && c < n) {
-    for (int k = 1; k < G; ++k) s += sm[k][lane];
-    out[c] = scale != nullptr ? s * __ldg(scale) : s;
-  }
-}
-cudaError_t part_sum(const ColSums& cs, int count, long ld, int rows, int n, const float* scale, cudaStream_t s) {
-  const dim3 g(blocks_for(n, 32), count);
-  if (rows > 128) part_sum_kernel<32><<<g, 1024, 0, s>>>(cs, ld, rows, n, scale);
-  else part_sum_kernel<8><<<g, 256, 0, s>>>(cs, ld, rows, n, scale);
-  return cudaGetLastError();
-}
-
 // Column sums of an [M, N] matrix: block (256 columns, strip of rows), 8
 // consecutive columns a thread (VEC: rows of 16 bytes) or 8 columns 32 apart,
 // 8 rows at a time.
@@ -552,16 +579,19 @@ int col_strips(int M, int N) {
   const int want = ceil_div(4 * 152, ceil_div(N, 256)), most = ceil_div(M, 32);
   return want < most ? want : most;
 }
+// The strips' sums in part, or with one strip in out.
 template <typename T>
-cudaError_t col_sum_t(const void* a, int M, int N, float* part, float* out, cudaStream_t s) {
-  const int strips = col_strips(M, N), per = ceil_div(M, strips);
-  float* to = strips == 1 ? out : part;
+cudaError_t col_strip_t(const void* a, int M, int N, int strips, float* to, cudaStream_t s) {
+  const int per = ceil_div(M, strips);
   const dim3 g(ceil_div(N, 256), strips);
   if ((N * sizeof(T)) % 16 == 0) col_strip_kernel<T, true><<<g, kBlock, 0, s>>>((const T*)a, M, N, per, to);
   else col_strip_kernel<T, false><<<g, kBlock, 0, s>>>((const T*)a, M, N, per, to);
-  JEPA_TRY_CUDA(cudaGetLastError());
-  if (strips == 1) return cudaSuccess;
-  return part_sum(ColSums{{part, nullptr}, {out, nullptr}}, 1, N, strips, N, nullptr, s);
+  return cudaGetLastError();
+}
+cudaError_t col_strip(int dtype, const void* a, int M, int N, int strips, float* to, cudaStream_t s) {
+  if (dtype == DTYPE_F32) return col_strip_t<float>(a, M, N, strips, to, s);
+  if (dtype == DTYPE_F16) return col_strip_t<__half>(a, M, N, strips, to, s);
+  return col_strip_t<__nv_bfloat16>(a, M, N, strips, to, s);
 }
 
 cudaError_t zero(void* p, size_t bytes, cudaStream_t s) {
@@ -827,8 +857,6 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
       p.ep.ld_col = l.piece;
       JEPA_TRY_CUDA(gemm(a.dtype, tg::CE_BWD, p, a.num_sms, s));
     }
-    if (dbias != nullptr)
-      JEPA_TRY_CUDA(part_sum(ColSums{{l.colp, nullptr}, {dbias + v0, nullptr}}, 1, l.piece, ceil_div(a.M, 32), n, unscale, s));
     Job jx = base_job(a.M, a.D, tg::kBN), jw = base_job(n, a.D, tg::kBN);
     uint8_t* dw_out = dw != nullptr ? static_cast<uint8_t*>(dw) + elem(a.dtype) * (size_t)v0 * a.D : nullptr;
     if (dx != nullptr) {
@@ -854,10 +882,11 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
     }
     JEPA_TRY_CUDA(gemm_reduce(a.dtype, dx != nullptr ? &jx : nullptr, dw != nullptr ? &jw : nullptr, l.plan, a.status,
                               a.num_sms, s));
-    SlabSums q{};
+    Finish q{};
+    if (dbias != nullptr) add_part_sum(q, l.colp, dbias + v0, l.piece, ceil_div(a.M, 32), n);
     add_slab_sum(q, l.dw, 0, jw.splits, jw.slab_rows, dw_out, n, a.D);
     if (v0 + n == a.V) add_slab_sum(q, l.dx, 0, dx_slabs, l.dx.mp, dx, a.M, a.D);
-    JEPA_TRY_CUDA(slab_sum(a.dtype, q, unscale, s));
+    JEPA_TRY_CUDA(finish(a.dtype, q, unscale, s));
   }
   return cudaSuccess;
 }
@@ -992,14 +1021,6 @@ cudaError_t gated_ffn_bwd(const FfnArgs& a, const void* dh, void* dx, void* dwg,
     p.ep.ld_col = l.fp;
     JEPA_TRY_CUDA(gemm(a.dtype, tg::GATE_BWD, p, a.num_sms, s));
   }
-  ColSums cs{};
-  int sums = 0;
-  for (int k = 0; k < 2; ++k)
-    if ((k == 0 ? dbg : dbu) != nullptr) {
-      cs.a[sums] = l.colp[k];
-      cs.out[sums++] = k == 0 ? dbg : dbu;
-    }
-  if (sums > 0) JEPA_TRY_CUDA(part_sum(cs, sums, l.fp, ceil_div(a.M, 32), a.F, nullptr, s));
   Job jx = base_job(a.M, a.D, tg::kBN), jw = base_job(a.F, a.D, tg::kBN);
   if (dx != nullptr) {
     set_k(jx, a.F, 2, l.dx.splits);
@@ -1029,10 +1050,12 @@ cudaError_t gated_ffn_bwd(const FfnArgs& a, const void* dh, void* dx, void* dwg,
   }
   JEPA_TRY_CUDA(gemm_reduce(a.dtype, dx != nullptr ? &jx : nullptr, jw.nz > 0 ? &jw : nullptr, l.plan, a.status,
                             a.num_sms, s));
-  SlabSums q{};
+  Finish q{};
+  add_part_sum(q, l.colp[0], dbg, l.fp, ceil_div(a.M, 32), a.F);
+  add_part_sum(q, l.colp[1], dbu, l.fp, ceil_div(a.M, 32), a.F);
   add_slab_sum(q, l.dx, 0, jx.splits, jx.slab_rows, dx, a.M, a.D);
   for (int k = 0; k < 2; ++k) add_slab_sum(q, l.dw, k, jw.splits, jw.slab_rows, dw[k], a.F, a.D);
-  return slab_sum(a.dtype, q, nullptr, s);
+  return finish(a.dtype, q, nullptr, s);
 }
 
 // ----------------------------------------------------------------------------- linear layer backward
@@ -1097,14 +1120,15 @@ cudaError_t linear_bwd(int dtype, const void* dout, const void* A, const void* W
   }
   JEPA_TRY_CUDA(gemm_reduce(dtype, dA != nullptr ? &jobs[0] : nullptr, dW != nullptr ? &jobs[1] : nullptr, l.plan, status,
                             num_sms, s));
-  SlabSums q{};
+  Finish q{};
   if (dA != nullptr) add_slab_sum(q, l.dA, 0, jobs[0].splits, jobs[0].slab_rows, dA, M, K);
   if (dW != nullptr) add_slab_sum(q, l.dW, 0, jobs[1].splits, jobs[1].slab_rows, dW, N, K);
-  JEPA_TRY_CUDA(slab_sum(dtype, q, nullptr, s));
-  if (dbias == nullptr) return cudaSuccess;
-  if (dtype == DTYPE_F32) return col_sum_t<float>(dout, M, N, l.colp, dbias, s);
-  if (dtype == DTYPE_F16) return col_sum_t<__half>(dout, M, N, l.colp, dbias, s);
-  return col_sum_t<__nv_bfloat16>(dout, M, N, l.colp, dbias, s);
+  if (dbias != nullptr) {
+    const int strips = col_strips(M, N);
+    JEPA_TRY_CUDA(col_strip(dtype, dout, M, N, strips, strips == 1 ? dbias : l.colp, s));
+    if (strips > 1) add_part_sum(q, l.colp, dbias, N, strips, N);
+  }
+  return finish(dtype, q, nullptr, s);
 }
 
 }  // namespace jepa
