@@ -226,11 +226,11 @@ struct PairPlan {
   int splits[2], first, extra;
 };
 
-// Time of one unit over `per` blocks in us: 0.27 us a block (256 x 256 x 64 on a
+// Time of one unit over `per` blocks in us: 0.34 us a block (256 x 256 x 64 on a
 // CTA pair; 1.6 for planes), but at least an epilogue's, and a little to change
 // over.
 double unit_us(bool sp, int per) {
-  const double t = per * (sp ? 1.6 : 0.27), epilogue = sp ? 2.5 : 2.0;
+  const double t = per * (sp ? 1.6 : 0.34), epilogue = sp ? 2.5 : 2.0;
   return (t > epilogue ? t : epilogue) + 0.3;
 }
 // Rounds of the 76 pairs for n[0] units of c[0] us, then n[1] of c[1] (Walk's order).
