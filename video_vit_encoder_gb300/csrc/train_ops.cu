@@ -676,10 +676,18 @@ __global__ void __launch_bounds__(1024) dz_scale_kernel(const float* __restrict_
                                                         int V, float f, float smoothing, float* scale) {
   __shared__ float sm[32];
   float m = 0.f;
-  for (int i = threadIdx.x; i < M; i += 1024) {
-    const long label = __ldg(labels + i);
-    const float d = __ldg(dloss + i);
-    if (label != ignore_index && label >= 0 && label < V) m = fmaxf(m, fabsf(d));
+  for (int i0 = threadIdx.x; i0 < M; i0 += 8 * 1024) {
+    long label[8];
+    float d[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {   // past M: again the last row
+      const int i = min(i0 + j * 1024, M - 1);
+      label[j] = __ldg(reinterpret_cast<const long long*>(labels) + i);
+      d[j] = __ldg(dloss + i);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (label[j] != ignore_index && label[j] >= 0 && label[j] < V) m = fmaxf(m, fabsf(d[j]));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
