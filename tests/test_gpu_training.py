@@ -264,6 +264,31 @@ def test_linear_ce_dloss_of_rows_without_a_gradient(jg, dtype):
             assert torch.equal(a, r), v
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("smooth", [0.75, 0.8, 0.97])
+def test_linear_ce_strong_smoothing(jg, dtype, smooth):
+    """Certain of a wrong class: the 16-bit dz is largest, 1 / (1 - smoothing) in its unit."""
+    M, D, V = 150, 64, 300
+    rng, x, xv, _, Wv, b, bv, lab, labels = _ce_case(M, D, V, dtype, 0, 10)
+    W, Wv = _dev(8 * Wv, dtype)
+    dl, dlv = _dev(rng.standard_normal(M))
+    _, rs, z = ot.linear_ce(xv, Wv, bv, lab, smoothing=smooth)
+    assert (np.exp(z - rs[:, None]).max(1) > 0.999).any()
+    lse, lsev = _dev(rs)
+    dx, dW, db = jg.linear_ce_bwd(dl, x, W, b, labels, lse, smoothing=smooth)
+    dz = ot.linear_ce_dz(z, lsev, dlv, lab, smoothing=smooth)
+    e = tb.ce_dz(xv, Wv, bv, z, lsev, dlv, lab, smooth, dtype)
+    e[lab == -100] = 0
+    tb.check(_np(db), dz.sum(0), e.sum(0) + 2 * tb.U * (M + 16) * np.abs(dz).sum(0), "dbias")
+    # fp16: half its smallest subnormal, 2^-25, in units of max |dloss| (1 - smoothing) / 2^(14 + floor(log2(1 - smoothing)))
+    h = 0 if dtype == "f32" else tb.HALF[dtype]
+    floor = 2.0 ** -38 * np.abs(dlv).max() if dtype == "f16" else 0.0
+    er = e + h * (np.abs(dz) + e) + floor * (lab != -100)[:, None]
+    rx, rw = dz @ Wv, dz.T @ xv
+    tb.check(_np(dx), rx, tb.rounded(rx, tb.product(dz, Wv.T, er), dtype), "dx")
+    tb.check(_np(dW), rw, tb.rounded(rw, tb.product(dz.T, xv.T, er.T), dtype), "dW")
+
+
 def test_linear_ce_forms_of_labels_and_dloss(jg):
     """int32 labels, one dloss as a number or as a tensor without dimensions."""
     _, x, _, W, _, b, _, lab, labels = _ce_case(200, 64, 300, "bf16", 0, 9)

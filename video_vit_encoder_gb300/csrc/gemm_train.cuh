@@ -592,7 +592,7 @@ __device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], co
                                             int row0, int col0, uint8_t* buf, int lane) {
   const EpiArgs& ep = p.ep;
   const int N = p.j[0].N;
-  // 16-bit dz is held as g ((p - e / V) / (1 - e) - [v = y]) with g = dloss / max |dloss| (times 2^14 in fp16): with one
+  // 16-bit dz is held as g ((p - e / V) / (1 - e) - [v = y]) with g = dloss / max |dloss| (times a power of 2 in fp16): with one
   // dloss for all rows, as a mean's, the label's entry is then near -1, which 16 bits hold exactly.  (As dloss (p - (1 - e)
   // [v = y] - e / V) those entries, which make up most of dx and dW, were all off by the same rounding of dloss: dx and
   // dW 3.0e-3 from the exact gradients in norm instead of 1.7e-3 at 1999 x 768 x 50021 in bf16.)

@@ -669,8 +669,12 @@ cudaError_t ce_join(const CeArgs& a, const float2* ms, const float* sums, const 
 
 // What dz is held in units of: scale[0] = max |dloss| over the rows that have a
 // gradient (1 if that is 0 or not finite), scale[1] = F, and scale[2] = scale[0] (1 - smoothing) / F brings
-// products of dz back.  F is 2^14 in fp16, so that |dz| stays below fp16's
-// largest value and small probabilities stay normal numbers, and 1 in bf16.
+// products of dz back.  F is 1 in bf16; in fp16 dz_factor, so that |dz|, at most
+// F / (1 - smoothing), stays below fp16's largest value and small probabilities
+// stay normal numbers.
+float dz_factor(int dtype, float smoothing) {
+  return dtype == DTYPE_F16 ? ldexpf(1.0f, 14 + (int)floorf(log2f(1.0f - smoothing))) : 1.0f;
+}
 __global__ void __launch_bounds__(1024) dz_scale_kernel(const float* __restrict__ dloss,
                                                         const int64_t* __restrict__ labels, long ignore_index, int M,
                                                         int V, float f, float smoothing, float* scale) {
@@ -827,7 +831,7 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
   const float* unscale = nullptr;
   if (!sp) {
     dz_scale_kernel<<<1, 1024, 0, s>>>(dloss, a.labels, a.ignore_index, a.M, a.V,
-                                       a.dtype == DTYPE_F16 ? 16384.f : 1.f, a.smoothing, l.scale);
+                                       dz_factor(a.dtype, a.smoothing), a.smoothing, l.scale);
     JEPA_TRY_CUDA(cudaGetLastError());
     unscale = l.scale + 2;
   }

@@ -25,9 +25,10 @@ from ._lib import check, load
 from .binding import DTYPE_CODE
 
 _CODE = {torch.float32: DTYPE_CODE["f32"], torch.float16: DTYPE_CODE["f16"], torch.bfloat16: DTYPE_CODE["bf16"]}
-# the handle of a device's current stream (a call a fifth as long as through torch.cuda.current_stream)
+# the handle of a device's current stream, and the current device (calls a fifth as long as through torch.cuda)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _empty, _like = torch.empty, torch.empty_like   # _like takes half the time
 _f32, _u8 = torch.float32, torch.uint8
 _ACT = {"silu": _lib.GATE_SILU, "gelu": _lib.GATE_GELU}
@@ -99,7 +100,7 @@ def _place(t, stream, *inputs):
 def _elsewhere(t, stream):
     """Whether a call on t has to be made under _place (which refuses CPU tensors)."""
     index = t.get_device()
-    return stream is not None or index < 0 or index != torch.cuda.current_device()
+    return stream is not None or index < 0 or index != _current_device()
 
 
 def layernorm_fwd(x, w, b, eps, out_dtype=None, stream=None):
