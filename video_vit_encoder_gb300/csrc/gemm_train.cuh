@@ -87,7 +87,9 @@ struct EpiArgs {
   long ignore_index;
   const float* lse;
   const float* dloss;
-  const float* dz_scale;   // CE_BWD, 16-bit: [0] what dloss is divided by, [1] the factor of every dz
+  float* dz_scale;         // CE_BWD, 16-bit: [0] what dloss is divided by, [1] what brings products of dz back
+  float dz_factor;         // CE_BWD, 16-bit: the factor of every dz
+  int dz_inline;           // dz_scale is computed here, and written for the kernels that follow
   float smoothing;
   int v0, V;
   float2* part_ms;         // CE_FWD: [parts][M] (max, sum) in base 2
@@ -530,9 +532,8 @@ struct RowGrads {
 };
 struct RowLoads {
   long y[4];
-  float lse[4], dl[4], unit, factor;
+  float lse[4], dl[4];
 };
-template <bool SPLIT>
 __device__ __forceinline__ void load_rows(RowLoads& r, const Params& p, int row0, int lane) {
   const EpiArgs& ep = p.ep;
 #pragma unroll
@@ -542,13 +543,9 @@ __device__ __forceinline__ void load_rows(RowLoads& r, const Params& p, int row0
     r.lse[i] = __ldg(ep.lse + row);
     r.dl[i] = __ldg(ep.dloss + row);
   }
-  if constexpr (!SPLIT) {
-    r.unit = __ldg(ep.dz_scale);
-    r.factor = __ldg(ep.dz_scale + 1);
-  }
 }
 template <bool SPLIT>
-__device__ __forceinline__ RowGrads ce_bwd_rows(const RowLoads& l, const Params& p, int row0, int lane, bool report) {
+__device__ __forceinline__ RowGrads ce_bwd_rows(const RowLoads& l, const Params& p, float unit, int row0, int lane, bool report) {
   RowGrads r;
   r.part = 0;
 #pragma unroll
@@ -558,10 +555,53 @@ __device__ __forceinline__ RowGrads ce_bwd_rows(const RowLoads& l, const Params&
     r.part |= part ? 1 << i : 0;
     r.label[i] = part ? (int)l.y[i] - p.ep.v0 : -1;
     r.l2[i] = part ? l.lse[i] * kLog2e : 0.f;
-    r.g[i] = part ? (SPLIT ? l.dl[i] : l.dl[i] / l.unit * l.factor) : 0.f;
+    r.g[i] = part ? (SPLIT ? l.dl[i] : l.dl[i] / unit * p.ep.dz_factor) : 0.f;
     if (in && !part && report) atomicOr(p.status, DEV_BAD_INDEX);
   }
   return r;
+}
+
+// max |dloss| over the rows that have a gradient, of this thread's of `threads`.
+__device__ __forceinline__ float dz_max(const float* dloss, const int64_t* labels, long ignore_index, int M, int V,
+                                        int thread, int threads) {
+  float m = 0.f;
+  for (int i0 = thread; i0 < M; i0 += 8 * threads) {
+    long label[8];
+    float d[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {   // past M: again the last row
+      const int i = min(i0 + j * threads, M - 1);
+      label[j] = __ldg(reinterpret_cast<const long long*>(labels) + i);
+      d[j] = __ldg(dloss + i);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (label[j] != ignore_index && label[j] >= 0 && label[j] < V) m = fmaxf(m, fabsf(d[j]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+// What dz is held in units of, from the maximum over all rows: that, or 1 if it
+// is 0 or not finite.
+__device__ __forceinline__ float dz_unit(float m, float factor, float smoothing, float* scale) {
+  if (!(m > 0.f && m < INFINITY)) m = 1.f;
+  if (scale != nullptr) {
+    scale[0] = m;
+    scale[1] = m * (1.0f - smoothing) / factor;
+  }
+  return m;
+}
+// The same by the eight epilogue warps of every CTA, through their staging
+// buffers, while the first products run.
+__device__ __forceinline__ float dz_unit_inline(const Params& p, uint8_t* stage, int warp, int lane) {
+  const EpiArgs& ep = p.ep;
+  float m = dz_max(ep.dloss, ep.labels, ep.ignore_index, p.j[0].M, ep.V, warp * 32 + lane, 32 * kEpiWarps);
+  if (lane == 0) *reinterpret_cast<float*>(stage + warp * kEpiStage) = m;
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+  for (int k = 0; k < kEpiWarps; ++k) m = fmaxf(m, *reinterpret_cast<const float*>(stage + k * kEpiStage));
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");   // read before a buffer is used
+  return dz_unit(m, ep.dz_factor, ep.smoothing, blockIdx.x == 0 && warp == 0 && lane == 0 ? ep.dz_scale : nullptr);
 }
 
 // Asks for what the epilogue of a pair's next tile reads: the lines of 32 rows'
@@ -1039,6 +1079,9 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
     const int quarter = warp & 3, half = (warp - kFirstEpi) >> 2;
     const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
     uint8_t* buf_s = sEpi + (warp - kFirstEpi) * kEpiStage;
+    [[maybe_unused]] float unit = 1.f;
+    if constexpr (EPI == CE_BWD && !SPLIT)
+      unit = p.ep.dz_inline ? dz_unit_inline(p, sEpi, warp - kFirstEpi, lane) : __ldg(p.ep.dz_scale);
     int acc = 0;
     bool stop = false;
     int u = walk.at<EPI>(p, 0);
@@ -1091,7 +1134,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
         [[maybe_unused]] RowLoads rows;
         [[maybe_unused]] Biases biases[EPI == GATE_BWD ? 2 : 1];
         if constexpr (EPI == CE_BWD) {
-          load_rows<SPLIT>(rows, p, row - lane, lane);
+          load_rows(rows, p, row - lane, lane);
           load_biases(biases[0], p.ep.bias, col, job.N, lane);
         } else if constexpr (EPI == GATE_BWD) {
           for (int q = 0; q < 2; ++q)
@@ -1111,7 +1154,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
         }
         asm volatile("" ::"f"(warm));
         [[maybe_unused]] RowGrads rg;
-        if constexpr (EPI == CE_BWD) rg = ce_bwd_rows<SPLIT>(rows, p, row - lane, lane, t.n0 == 0 && half == 0);
+        if constexpr (EPI == CE_BWD) rg = ce_bwd_rows<SPLIT>(rows, p, unit, row - lane, lane, t.n0 == 0 && half == 0);
         if constexpr (kRegs) {
           {
             const uint32_t tb = tl + (acc & 1) * kBN;

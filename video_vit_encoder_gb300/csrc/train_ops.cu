@@ -667,42 +667,28 @@ cudaError_t ce_join(const CeArgs& a, const float2* ms, const float* sums, const 
   return cudaGetLastError();
 }
 
-// What dz is held in units of: scale[0] = max |dloss| over the rows that have a
-// gradient (1 if that is 0 or not finite), scale[1] = F, and scale[2] = scale[0] (1 - smoothing) / F brings
-// products of dz back.  F is 1 in bf16; in fp16 dz_factor, so that |dz|, at most
-// F / (1 - smoothing), stays below fp16's largest value and small probabilities
-// stay normal numbers.
+// 16-bit dz is held in units of max |dloss| over the rows that have a gradient,
+// times a factor: 1 in bf16; in fp16 a power of 2, so that |dz|, at most factor /
+// (1 - smoothing), stays below fp16's largest value and small probabilities stay
+// normal numbers.
 float dz_factor(int dtype, float smoothing) {
   return dtype == DTYPE_F16 ? ldexpf(1.0f, 14 + (int)floorf(log2f(1.0f - smoothing))) : 1.0f;
 }
-__global__ void __launch_bounds__(1024) dz_scale_kernel(const float* __restrict__ dloss,
-                                                        const int64_t* __restrict__ labels, long ignore_index, int M,
-                                                        int V, float f, float smoothing, float* scale) {
+// Up to 16384 rows CE_BWD finds the unit itself (4096 x 256 x 2048: 37 us, with
+// a kernel for it 39, and 3 us less on the host); where there are more rows a
+// kernel does (65536 x 256 x 512: 103 us, in CE_BWD 110).
+constexpr int kInlineRows = 16384;
+__global__ void __launch_bounds__(1024) dz_unit_kernel(const float* __restrict__ dloss,
+                                                       const int64_t* __restrict__ labels, long ignore_index, int M,
+                                                       int V, float factor, float smoothing, float* scale) {
   __shared__ float sm[32];
-  float m = 0.f;
-  for (int i0 = threadIdx.x; i0 < M; i0 += 8 * 1024) {
-    long label[8];
-    float d[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {   // past M: again the last row
-      const int i = min(i0 + j * 1024, M - 1);
-      label[j] = __ldg(reinterpret_cast<const long long*>(labels) + i);
-      d[j] = __ldg(dloss + i);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (label[j] != ignore_index && label[j] >= 0 && label[j] < V) m = fmaxf(m, fabsf(d[j]));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float m = tg::dz_max(dloss, labels, ignore_index, M, V, threadIdx.x, 1024);
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int k = 1; k < 32; ++k) m = fmaxf(m, sm[k]);
-    if (!(m > 0.f && m < INFINITY)) m = 1.f;
-    scale[0] = m;
-    scale[1] = f;
-    scale[2] = m * (1.0f - smoothing) / f;
+    float all = m;
+    for (int k = 1; k < 32; ++k) all = fmaxf(all, sm[k]);
+    tg::dz_unit(all, factor, smoothing, scale);
   }
 }
 
@@ -763,7 +749,7 @@ CeBwd ce_bwd_layout(const CeArgs& a, void* ws) {
   pieces = ceil_div(a.V, l.piece);
   l.dz_plane = split(a.dtype) ? (int)round_up(a.M, 256) : 0;
   l.dz = cv.take<uint8_t>((size_t)rows * l.piece * 2);
-  l.scale = cv.take<float>(3 * sizeof(float));
+  l.scale = cv.take<float>(2 * sizeof(float));
   l.colp = cv.take<float>((size_t)ceil_div(a.M, 32) * l.piece * 4);
   const int n = a.V < l.piece ? a.V : l.piece;
   const Product dx{a.M, a.D, 1, ceil_div(n, tg::kBK)}, dw{n, a.D, 1, ceil_div(a.M, tg::kBK)};
@@ -830,10 +816,12 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
   JEPA_TRY_CUDA(fill(a.dtype, f, s));
   const float* unscale = nullptr;
   if (!sp) {
-    dz_scale_kernel<<<1, 1024, 0, s>>>(dloss, a.labels, a.ignore_index, a.M, a.V,
-                                       dz_factor(a.dtype, a.smoothing), a.smoothing, l.scale);
-    JEPA_TRY_CUDA(cudaGetLastError());
-    unscale = l.scale + 2;
+    if (a.M > kInlineRows) {
+      dz_unit_kernel<<<1, 1024, 0, s>>>(dloss, a.labels, a.ignore_index, a.M, a.V, dz_factor(a.dtype, a.smoothing),
+                                        a.smoothing, l.scale);
+      JEPA_TRY_CUDA(cudaGetLastError());
+    }
+    unscale = l.scale + 1;
   }
   int dx_slabs = 1;
   for (int v0 = 0; v0 < a.V; v0 += l.piece) {
@@ -862,6 +850,8 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
       p.ep.lse = lse;
       p.ep.dloss = dloss;
       p.ep.dz_scale = l.scale;
+      p.ep.dz_factor = dz_factor(a.dtype, a.smoothing);
+      p.ep.dz_inline = a.M <= kInlineRows;
       p.ep.smoothing = a.smoothing;
       p.ep.v0 = v0;
       p.ep.V = a.V;
