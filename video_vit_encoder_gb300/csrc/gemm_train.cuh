@@ -219,11 +219,29 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Arrival on a barrier of the pair that hands back tensor memory: the loads
-// before it have completed (tcgen05.wait::ld and the fence), and no memory is
-// passed on, so it need not wait for the thread's stores as a release does.
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// mbar_wait on a barrier that the other CTA's threads arrive on too (with
+// mbar_arrive_cluster): tensor memory handed back by both is acquired from both.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  auto arrived = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (arrived()) return true;
+  const long long t0 = clock64();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (arrived()) return true;
+    if ((unsigned long long)(clock64() - t0) > 2ull * kWaitLimitNs) return false;
+  }
 }
 
 // Packed arithmetic on two neighbouring values: (a, b) = (a, b) m + (c, c), and
@@ -1024,7 +1042,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
                 break;
               }
               const int buf = acc & 1;
-              if (!__all_sync(0xffffffffu, mbar_wait(&tempty[buf], ((acc >> 1) & 1) ^ 1))) {
+              if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[buf], ((acc >> 1) & 1) ^ 1))) {
                 ok = false;
                 break;
               }
@@ -1117,7 +1135,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
         auto chunk_taken = [&](int buf) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + 8 * buf);
+          if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * buf);   // the even CTA's barrier
           ++acc;
         };
         // the c-th 32 values of this thread: of its row's 128 columns (gates: 64 gate columns, then the 64 up columns),
