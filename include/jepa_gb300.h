@@ -398,6 +398,10 @@ JEPA_API jepa_status jepa_qkv_rope(const void* A, const void* W, const float* bi
  *     are dropped) and summed in fp32, so results have fp32's accuracy; an
  *     infinity in an F32 matrix gives NaN where it takes part.  Widths whose
  *     16-bit rows are not multiples of 16 bytes cost a copy of the matrix.
+ *   - The tensor cores truncate the sums they hold.  Results in fp32 and F32
+ *     matrices are summed in short pieces that are added with rounding; in F16
+ *     and BF16 matrices the loss is at most half as much as the rounding of
+ *     the result, over any number of rows or columns.
  *   - Rows 0 is valid: gradients of weights are then zeros.  Row counts and
  *     widths are at most 2^24 (layer norm: dim at most 2^20).
  *   - `workspace` is a device buffer of the caller, 256-byte aligned, of at

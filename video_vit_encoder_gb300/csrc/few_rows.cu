@@ -11,8 +11,10 @@
 // 16-bit: products m16n8k16 with the weights as the 16 rows and x as the 8
 // columns, fp32 sums.  The order of K inside a product is free as long as both
 // operands use the same one, so every thread loads 16 contiguous bytes of its
-// row, which are two products' worth.  fp32: eight weight rows and all of x per
-// thread in FFMA, each thread four of K at a time.
+// row, which are two products' worth.  The products truncate their sums like
+// tcgen05.mma (gemm_train.cuh), so each 32 of a warp are added up apart.  fp32:
+// eight weight rows and all of x per thread in FFMA, each thread four of K at a
+// time.
 //
 // Gated feed-forward, 8 rows, 1024 -> 4096, bf16: 16.8 MB of weights, 6.3 us
 // (tiles of 256 rows: 16.5).  Cross entropy, 8 rows, 1024 -> 174, fp32: 10.4 us
@@ -26,6 +28,7 @@ namespace {
 
 constexpr int kWarps = 8, kBlock = 32 * kWarps;
 constexpr int kRows = 16;   // weight rows of a block
+constexpr int kChunk = 4096;   // of K, a warp's share of it 32 steps: then its sums are taken out and added with rounding
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -67,30 +70,41 @@ __device__ __forceinline__ void dot_rows(const T* const (&w)[NM], const T* x, in
 #pragma unroll
     for (int n = 0; n < NT; ++n) b[n] = x + (size_t)min(n * 8 + g, M - 1) * D;
     float c[NM][NT][4] = {};
+#pragma unroll 1
+    for (int k1 = warp * 64; k1 < D; k1 += kChunk) {
+      const int end = min(D, k1 + kChunk);
+      float t[NM][NT][4] = {};
 #pragma unroll 2
-    for (int k0 = warp * 64; k0 < D; k0 += kWarps * 64) {
-      uint4 av[NM][2][2], bv[NT][2];
+      for (int k0 = k1; k0 < end; k0 += kWarps * 64) {
+        uint4 av[NM][2][2], bv[NT][2];
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int k = k0 + p * 32 + q * 8;
-        const bool in = k < D;   // D is a multiple of 8
+        for (int p = 0; p < 2; ++p) {
+          const int k = k0 + p * 32 + q * 8;
+          const bool in = k < D;   // D is a multiple of 8
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
+          for (int m = 0; m < NM; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) av[m][h][p] = in ? load_once(a[m][h] + k) : make_uint4(0, 0, 0, 0);
+            for (int h = 0; h < 2; ++h) av[m][h][p] = in ? load_once(a[m][h] + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          bv[n][p] = in ? __ldg(reinterpret_cast<const uint4*>(b[n] + k)) : make_uint4(0, 0, 0, 0);
+          for (int n = 0; n < NT; ++n)
+            bv[n][p] = in ? __ldg(reinterpret_cast<const uint4*>(b[n] + k)) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816<T>(t[m][n], av[m][0][p].x, av[m][1][p].x, av[m][0][p].y, av[m][1][p].y, bv[n][p].x, bv[n][p].y);
+              mma16816<T>(t[m][n], av[m][0][p].z, av[m][1][p].z, av[m][0][p].w, av[m][1][p].w, bv[n][p].z, bv[n][p].w);
+            }
       }
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int m = 0; m < NM; ++m)
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma16816<T>(c[m][n], av[m][0][p].x, av[m][1][p].x, av[m][0][p].y, av[m][1][p].y, bv[n][p].x, bv[n][p].y);
-            mma16816<T>(c[m][n], av[m][0][p].z, av[m][1][p].z, av[m][0][p].w, av[m][1][p].w, bv[n][p].z, bv[n][p].w);
-          }
+          for (int i = 0; i < 4; ++i) c[m][n][i] += t[m][n][i];
     }
 #pragma unroll
     for (int m = 0; m < NM; ++m)

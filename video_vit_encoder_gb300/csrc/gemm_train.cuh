@@ -15,12 +15,17 @@
 // below 2^-24 of the first.  That is 6 times the work of a bf16 product and
 // still several times the FFMA rate.
 //
-// The tensor core truncates its fp32 accumulator at every step of 16 k: after n
-// steps a sum has lost about n 2^-25 of itself (measured: logits over 1024 k
-// 1.5e-6 too small).  Epilogues whose results are fp32 therefore take the
-// accumulator out every kb_chunk blocks and add the pieces in registers, with
-// rounding; SPLIT does so every block, with the products of the small planes
-// first, whose steps then truncate a small accumulator.
+// The tensor core truncates at every step of 16 k, so that a sum of products of
+// one sign ends too small: by up to 2^-23 of itself a step (measured, all
+// products positive: fp16 2.7 2^-23 after 4 steps, 27 after 32, 0.85 a step from
+// 256 steps on; bf16, whose products are shorter, up to 9.6 after 32, 0.86 a step
+// from 1000 on; logits of products of both signs over 1024 k, bf16: 12.6 after
+// 64).  Epilogues whose results are fp32 therefore take the accumulator out every few
+// blocks (kb_chunk) and add the pieces in registers, with rounding; SPLIT does so
+// every block, with the products of the small planes first, whose steps then
+// truncate a small accumulator.  16-bit results keep sums in it as long as the
+// loss is below half a rounding of theirs: 2048 steps in fp16, 16384 in bf16
+// (long_blocks); REDUCE adds the pieces of longer ones in memory.
 //
 // Work units are runs of tiles: the cross entropy carries its row statistics
 // over a run of column tiles, everything else has runs of one.  The reducing
@@ -123,7 +128,7 @@ struct Params {
   int units[2];          // of each job
   int extra;             // units of job 1 that a pair takes while others do their last of job 0
   int run;               // column tiles per unit
-  int kb_chunk;          // blocks accumulated in tensor memory before the epilogue takes them
+  int kb_chunk;          // blocks accumulated in tensor memory before the epilogue takes them (STORE: all of a unit's)
   int c_plane;           // SPLIT: rows from one plane of C to the next
   void* plain;           // C where TMA cannot store it (rows not multiples of 16 bytes), else null
   long plain_ld;
@@ -1205,14 +1210,27 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
             chunk_taken(acc & 1);
           }
         } else {
-          const int buf = acc & 1;
-          const uint32_t tb = tl + buf * kBN;
-          if (job.out == STORE)
-            store_tile<T>(job, &job.c[t.z], tb + half * (kBN / 2), row - lane, col, buf_s, lane);
-          else
-            slab_tile(job, &job.c[t.z], tb + half * (kBN / 2), row - lane + t.split * job.slab_rows, col, buf_s, lane,
-                      job.out == F32_ADD);
-          chunk_taken(buf);
+          // a sum of several pieces (its C is fp32) adds those after the first to what this warp has stored
+          bool add = job.out == F32_ADD;
+#pragma unroll 1
+          for (int c0 = t.kb0;;) {
+            const int buf = acc & 1;
+            const uint32_t tb = tl + buf * kBN;
+            if (job.out == STORE)
+              store_tile<T>(job, &job.c[t.z], tb + half * (kBN / 2), row - lane, col, buf_s, lane);
+            else
+              slab_tile(job, &job.c[t.z], tb + half * (kBN / 2), row - lane + t.split * job.slab_rows, col, buf_s, lane,
+                        add);
+            chunk_taken(buf);
+            c0 += p.kb_chunk;
+            if (c0 >= t.kb1) break;
+            if (lane == 0) bulk_wait_all();   // the piece before is in memory
+            if (!chunk_ready(acc & 1)) {
+              stop = true;
+              break;
+            }
+            add = true;
+          }
         }
         if constexpr (kRegs) {
           if (stop) break;

@@ -21,7 +21,6 @@ using tg::Params;
 
 constexpr int kBlock = 256;
 constexpr int kPairs = 76;      // CTA pairs of 152 SMs: the plans (and workspaces) assume it, the launch asks the device
-constexpr int kWhole = 1 << 30; // all of K in tensor memory
 
 #define JEPA_TRY_CUDA(expr)                 \
   do {                                      \
@@ -209,7 +208,6 @@ Params forward_params(const Job& j, int run, int* status) {
   p.run = run;
   const long units = (long)j.num_m * ceil_div(j.num_n, run);
   p.units[0] = units > 0x7fffffffl ? -1 : (int)units;   // launch refuses what it cannot count
-  p.kb_chunk = kWhole;
   p.status = status;
   return p;
 }
@@ -314,6 +312,10 @@ PairPlan plan_pair(int dtype, const Product& a, const Product& b) {
   return e.plan;
 }
 
+// K blocks of a sum with a 16-bit result that stay in the accumulator: it then
+// loses at most half as much as the result's rounding.
+int long_blocks(int dtype) { return dtype == DTYPE_F16 ? 512 : 4096; }
+
 // How a product's C of the operator's type comes about: written by the
 // product, or through fp32 slabs, one per split (and z).
 struct Reduce {
@@ -326,7 +328,7 @@ Reduce plan_reduce(int dtype, const Product& pr, int splits, bool add, Carver& c
   Reduce r;
   r.splits = splits;
   // fp32 adds pieces in place; 16-bit pieces add up in fp32
-  r.direct = splits == 1 && (split(dtype) ? pr.N % 4 == 0 : pr.N % 8 == 0 && !add);
+  r.direct = splits == 1 && (split(dtype) ? pr.N % 4 == 0 : pr.N % 8 == 0 && !add && pr.kb <= long_blocks(dtype));
   r.np = round_up(pr.N, 8);
   r.mp = round_up(pr.M, 256);
   if (!r.direct)
@@ -347,8 +349,8 @@ cudaError_t reduce_output(int dtype, const Reduce& rd, Job& j, int z, void* out,
 }
 
 // K blocks between the register sums of a 16-bit product with fp32 results.
-// CE_FWD hides the sums behind its products: 8 (512 k), logits then lose less
-// than 2^-20 of themselves.  Column sums (dbias) of many tiles take up to 12
+// CE_FWD hides the sums behind its products: 8 (512 k), logits then lose about
+// 2^-20 of themselves (27 2^-23 at most, where all products have one sign).  Column sums (dbias) of many tiles take up to 12
 // blocks, evenly: a sum less is 5% of a whole backward pass (1999 x 768 x 50021
 // 344 us with 8 + 4, 326 in one go), and dbias is 6e-7 off in norm; in one go
 // over 16 blocks it would be 1.9e-6 (4096 x 1024 x 32768).  Over few classes
@@ -381,7 +383,7 @@ cudaError_t gemm_reduce(int dtype, const Job* a, const Job* b, const PairPlan& p
   if (jobs[0] == nullptr) return cudaSuccess;
   Params p{};
   p.run = 1;
-  p.kb_chunk = split(dtype) ? 1 : kWhole;
+  p.kb_chunk = split(dtype) ? 1 : long_blocks(dtype);
   p.extra = plan.extra;
   p.status = status;
   for (int k = 0; k < 2; ++k)
@@ -842,7 +844,7 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
       j.a_plane = (int)l.x.plane_rows;
       j.b_plane = (int)l.w.plane_rows;
       Params p = forward_params(j, 1, a.status);
-      p.kb_chunk = sp ? 1 : (dbias != nullptr ? chunk_blocks(j, true) : kWhole);
+      p.kb_chunk = sp ? 1 : (dbias != nullptr ? chunk_blocks(j, true) : long_blocks(a.dtype));
       p.c_plane = l.dz_plane;
       p.ep.bias = a.bias != nullptr ? a.bias + v0 : nullptr;
       p.ep.labels = a.labels;
@@ -951,7 +953,7 @@ cudaError_t ffn_product(const FfnArgs& a, const FfnFwd& l, Job& j, cudaStream_t 
 }
 Params ffn_params(const FfnArgs& a, const Job& j) {
   Params p = forward_params(j, 1, a.status);
-  if (split(a.dtype)) p.kb_chunk = 1;
+  p.kb_chunk = split(a.dtype) ? 1 : long_blocks(a.dtype);
   p.ep.bias = a.bg;
   p.ep.bias2 = a.bu;
   p.ep.act = a.act;
