@@ -459,8 +459,10 @@ JEPA_API jepa_status jepa_linear_ce_fwd(const void* x, const void* W, const floa
  *   dx = dz W (dtype [M, D]), dW = dz^T x (dtype [V, D]), dbias = sum_rows dz
  *   (float [V]); each may be NULL, not all.
  * z is recomputed.  In F16/BF16 dz is rounded to the type before the products
- * dx and dW, in units of max |dloss| (so dloss itself costs no precision, and
- * in F16 small probabilities stay normal numbers); dbias is summed before. */
+ * dx and dW, in units of the largest finite |dloss| (so dloss itself costs no
+ * precision, and in F16 small probabilities stay normal numbers); dbias is
+ * summed before.  A dloss that is not finite makes its row's dx so, and dW and
+ * dbias, but no other row's dx. */
 JEPA_API jepa_status jepa_linear_ce_bwd(const void* x, const void* W, const float* bias, const int64_t* labels,
                                         const float* lse, const float* dloss, void* dx, void* dW, float* dbias, int M,
                                         int D, int V, int dtype, int64_t ignore_index, float smoothing,

@@ -585,6 +585,8 @@ __device__ __forceinline__ RowGrads ce_bwd_rows(const RowLoads& l, const Params&
 }
 
 // max |dloss| over the rows that have a gradient, of this thread's of `threads`.
+// A dloss that is not finite makes its own row's dz so, and leaves the unit to
+// the others.
 __device__ __forceinline__ float dz_max(const float* dloss, const int64_t* labels, long ignore_index, int M, int V,
                                         int thread, int threads) {
   float m = 0.f;
@@ -599,16 +601,16 @@ __device__ __forceinline__ float dz_max(const float* dloss, const int64_t* label
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (label[j] != ignore_index && label[j] >= 0 && label[j] < V) m = fmaxf(m, fabsf(d[j]));
+      if (label[j] != ignore_index && label[j] >= 0 && label[j] < V && fabsf(d[j]) < INFINITY) m = fmaxf(m, fabsf(d[j]));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 // What dz is held in units of, from the maximum over all rows: that, or 1 if it
-// is 0 or not finite.
+// is 0.
 __device__ __forceinline__ float dz_unit(float m, float factor, float smoothing, float* scale) {
-  if (!(m > 0.f && m < INFINITY)) m = 1.f;
+  if (!(m > 0.f)) m = 1.f;
   if (scale != nullptr) {
     scale[0] = m;
     scale[1] = m * (1.0f - smoothing) / factor;

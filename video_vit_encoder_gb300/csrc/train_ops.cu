@@ -669,10 +669,10 @@ cudaError_t ce_join(const CeArgs& a, const float2* ms, const float* sums, const 
   return cudaGetLastError();
 }
 
-// 16-bit dz is held in units of max |dloss| over the rows that have a gradient,
-// times a factor: 1 in bf16; in fp16 a power of 2, so that |dz|, at most factor /
-// (1 - smoothing), stays below fp16's largest value and small probabilities stay
-// normal numbers.
+// 16-bit dz is held in units of the largest finite |dloss| of the rows that have
+// a gradient, times a factor: 1 in bf16; in fp16 a power of 2, so that |dz|, at
+// most factor / (1 - smoothing), stays below fp16's largest value and small
+// probabilities stay normal numbers.
 float dz_factor(int dtype, float smoothing) {
   return dtype == DTYPE_F16 ? ldexpf(1.0f, 14 + (int)floorf(log2f(1.0f - smoothing))) : 1.0f;
 }
