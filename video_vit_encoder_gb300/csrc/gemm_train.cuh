@@ -473,6 +473,14 @@ __device__ __forceinline__ void emit_operand(const Params& p, const CUtensorMap*
 
 // Gate and its slope.  silu: a = g s, a' = s (1 + g (1 - s)) with s = 1 / (1 +
 // 2^(-g log2 e)); gelu: a = g Phi(g), a' = Phi(g) + g phi(g).
+//
+// Phi(-x), x >= 0, is e^(-x^2 / 2) t P(t) with t = 1 / (1 + 11/32 x): t P(t) =
+// e^(x^2 / 2) Phi(-x) is smooth, and a minimax fit of degree 8 over 0 <= x <= 14
+// has a relative error of 2.2e-8.  So gates far on the negative side keep their
+// relative accuracy (1/2 + erf(g / sqrt 2) / 2 cancels there: 4 % off at g = -5, 0
+// from -6 on), and the exponential serves phi too.  16384 x 1024 x 2736 in bf16:
+// 120-128 us, backward 400; through erff 119-125 and 414, through erfcf 151 and
+// 503.
 template <int ACT, bool GRAD>
 __device__ __forceinline__ void gate(float g, float& a, float& da) {
   if constexpr (ACT == ACT_SILU) {
@@ -480,9 +488,19 @@ __device__ __forceinline__ void gate(float g, float& a, float& da) {
     a = g * s;
     if constexpr (GRAD) da = s * fmaf(g, 1.0f - s, 1.0f);
   } else {
-    const float cdf = fmaf(0.5f, erff(g * 0.70710678118654752f), 0.5f);
+    const float e = ex2(g * g * (-0.5f * kLog2e));
+    const float t = __fdividef(1.0f, fmaf(0.34375f, fabsf(g), 1.0f));
+    float q = fmaf(-0x1.c7a0b8p-6f, t, 0x1.269a58p-3f);
+    q = fmaf(q, t, -0x1.163c2ap-2f);
+    q = fmaf(q, t, 0x1.870184p-3f);
+    q = fmaf(q, t, -0x1.4201p-5f);
+    q = fmaf(q, t, 0x1.cd7274p-4f);
+    q = fmaf(q, t, 0x1.de2b3ep-4f);
+    q = fmaf(q, t, 0x1.19afc4p-3f);
+    q = fmaf(q, t, 0x1.18d232p-3f);
+    const float tail = e * t * q, cdf = g < 0.f ? tail : 1.0f - tail;
     a = g * cdf;
-    if constexpr (GRAD) da = fmaf(g * 0.3989422804014327f, ex2(g * g * (-0.5f * kLog2e)), cdf);
+    if constexpr (GRAD) da = fmaf(g * 0.3989422804014327f, e, cdf);
   }
 }
 
