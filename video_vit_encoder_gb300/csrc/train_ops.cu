@@ -4,6 +4,8 @@
 // fp32 matrices are split into three bf16 planes first; 16-bit ones whose rows
 // are not multiples of 16 bytes are copied to rows that are (TMA addresses
 // nothing else).  Everything else reads the caller's matrices in place.
+#include <algorithm>
+
 #include "gemm_train.cuh"
 
 namespace jepa {
@@ -348,20 +350,32 @@ cudaError_t reduce_output(int dtype, const Reduce& rd, Job& j, int z, void* out,
   return map_out32(&j.c[z], slab, (long)j.slab_rows * j.splits, rd.np, rd.np);
 }
 
-// K blocks between the register sums of a 16-bit product with fp32 results.
-// CE_FWD hides the sums behind its products: 8 (512 k), logits then lose about
-// 2^-20 of themselves (27 2^-23 at most, where all products have one sign).  Column sums (dbias) of many tiles take up to 12
-// blocks, evenly: a sum less is 5% of a whole backward pass (1999 x 768 x 50021
-// 344 us with 8 + 4, 326 in one go), and dbias is 6e-7 off in norm; in one go
-// over 16 blocks it would be 1.9e-6 (4096 x 1024 x 32768).  Over few classes
-// they cancel, so that the truncation shows: at 1789 x 448 x 12 they are 4.9e-6
-// off with 8 blocks.  Such products have few tiles, and few blocks are
-// affordable.
-int chunk_blocks(const Job& j, bool column_sums) {
+// K blocks between the register sums of a 16-bit product with column sums
+// (bias gradients).  Many tiles take up to 12 blocks, evenly: a sum less is 5% of
+// a whole backward pass (1999 x 768 x 50021 344 us with 8 + 4, 326 in one go),
+// and dbias is 6e-7 off in norm; in one go over 16 blocks it would be 1.9e-6
+// (4096 x 1024 x 32768).  Of few tiles more sums are affordable.
+int column_blocks(const Job& j) {
   const long tiles = (long)j.num_m * j.num_n;
-  if (!column_sums) return 8;
   if (tiles > 4 * kPairs) return ceil_div(j.kb_seg, ceil_div(j.kb_seg, 12));
   return tiles > kPairs ? 4 : 2;
+}
+// The same of the cross entropy's logits.  The forward pass hides the sums behind
+// its products: 8 (512 k), logits then lose about 2^-20 of themselves (27 2^-23 at
+// most, where all products have one sign).  Where a class has many rows, the
+// entries p - [v = label] of its dbias cancel, but an error of z of one sign adds
+// up over the rows: it counts sqrt(M / V) times as much, so that the blocks go
+// down with M / V, in both passes, for what they share in lse and z cancels too.
+// dbias of 100000 x 768 x 12 is then 1.2e-7 off in norm (bf16, lse of the forward
+// pass; with 8 and 12 blocks 3.0e-6, and 6.4e-6 with an exact lse, now 9e-7), for
+// 66 and 176 us (50 and 153); 73728 x 1024 x 1000 4.5e-7 (and 1.7e-6 with an
+// exact lse, from 3.6e-6), 138 and 397 us (106 and 361); 16384 x 1024 x 174 1.2e-7
+// (2.6e-6), 17.7 and 49.7 us (15.4 and 50).
+int logit_blocks(const Job& j, int M, int V, bool backward) {
+  const long per_class = M / V;
+  if (per_class < 8) return backward ? column_blocks(j) : 8;
+  const int most = per_class >= 128 ? 2 : (per_class >= 32 ? 4 : 8);
+  return std::min(column_blocks(j), most);
 }
 
 cudaError_t gemm(int dtype, int epi, const Params& p, int num_sms, cudaStream_t s) {
@@ -793,7 +807,7 @@ cudaError_t linear_ce_fwd(const CeArgs& a, float* loss, float* lse, void* ws, cu
   j.a_plane = (int)l.x.plane_rows;
   j.b_plane = (int)l.w.plane_rows;
   Params p = forward_params(j, l.run, a.status);
-  p.kb_chunk = split(a.dtype) ? 1 : chunk_blocks(j, false);
+  p.kb_chunk = split(a.dtype) ? 1 : logit_blocks(j, a.M, a.V, false);
   p.ep.bias = a.bias;
   p.ep.labels = a.labels;
   p.ep.V = a.V;
@@ -844,7 +858,7 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
       j.a_plane = (int)l.x.plane_rows;
       j.b_plane = (int)l.w.plane_rows;
       Params p = forward_params(j, 1, a.status);
-      p.kb_chunk = sp ? 1 : (dbias != nullptr ? chunk_blocks(j, true) : long_blocks(a.dtype));
+      p.kb_chunk = sp ? 1 : (dbias != nullptr ? logit_blocks(j, a.M, a.V, true) : long_blocks(a.dtype));
       p.c_plane = l.dz_plane;
       p.ep.bias = a.bias != nullptr ? a.bias + v0 : nullptr;
       p.ep.labels = a.labels;
@@ -1016,7 +1030,7 @@ cudaError_t gated_ffn_bwd(const FfnArgs& a, const void* dh, void* dx, void* dwg,
     for (int k = 0; k < 2; ++k)
       JEPA_TRY_CUDA(map_out16(&j.c[k], l.d[k], sp ? 3 * (long)l.d_plane : a.M, l.fp, l.fp));
     Params p = ffn_params(a, j);
-    if (!sp && (dbg != nullptr || dbu != nullptr)) p.kb_chunk = chunk_blocks(j, true);
+    if (!sp && (dbg != nullptr || dbu != nullptr)) p.kb_chunk = column_blocks(j);
     p.c_plane = l.d_plane;
     p.ep.dh = dh;
     p.ep.dh_vec = (a.F * elem(a.dtype)) % 16 == 0;
