@@ -412,7 +412,8 @@ JEPA_API jepa_status jepa_qkv_rope(const void* A, const void* W, const float* bi
  *     nothing else is shared between calls.
  *   - Outputs must not overlap inputs, the workspace or each other.  Gradients
  *     are written, not added to.
- *   - Results do not depend on scheduling: every sum has a fixed order.
+ *   - Results do not depend on scheduling: every sum has a fixed order.  Nor
+ *     does a gradient depend on which others are asked for.
  *   - The calls only enqueue kernels and memsets and can be captured into a
  *     CUDA graph; the first call of an entry point on a device (which sets its
  *     kernels up, and allocates the device's status word) has to be made

@@ -354,7 +354,11 @@ cudaError_t reduce_output(int dtype, const Reduce& rd, Job& j, int z, void* out,
 // (bias gradients).  Many tiles take up to 12 blocks, evenly: a sum less is 5% of
 // a whole backward pass (1999 x 768 x 50021 344 us with 8 + 4, 326 in one go),
 // and dbias is 6e-7 off in norm; in one go over 16 blocks it would be 1.9e-6
-// (4096 x 1024 x 32768).  Of few tiles more sums are affordable.
+// (4096 x 1024 x 32768).  Of few tiles more sums are affordable.  A call that
+// wants no column sums takes the same blocks, so that its dx and dW are those of
+// one that does (4096 x 1024 x 32768 without dbias 545 us, in one go 516, with it
+// 535; 1024 x 1024 x 1000 29.4, 26.6, 31.8; gates of 16384 x 1024 x 2736 360, 346,
+// 366).
 int column_blocks(const Job& j) {
   const long tiles = (long)j.num_m * j.num_n;
   if (tiles > 4 * kPairs) return ceil_div(j.kb_seg, ceil_div(j.kb_seg, 12));
@@ -858,7 +862,7 @@ cudaError_t linear_ce_bwd(const CeArgs& a, const float* lse, const float* dloss,
       j.a_plane = (int)l.x.plane_rows;
       j.b_plane = (int)l.w.plane_rows;
       Params p = forward_params(j, 1, a.status);
-      p.kb_chunk = sp ? 1 : (dbias != nullptr ? logit_blocks(j, a.M, a.V, true) : long_blocks(a.dtype));
+      p.kb_chunk = sp ? 1 : logit_blocks(j, a.M, a.V, true);
       p.c_plane = l.dz_plane;
       p.ep.bias = a.bias != nullptr ? a.bias + v0 : nullptr;
       p.ep.labels = a.labels;
@@ -1030,7 +1034,7 @@ cudaError_t gated_ffn_bwd(const FfnArgs& a, const void* dh, void* dx, void* dwg,
     for (int k = 0; k < 2; ++k)
       JEPA_TRY_CUDA(map_out16(&j.c[k], l.d[k], sp ? 3 * (long)l.d_plane : a.M, l.fp, l.fp));
     Params p = ffn_params(a, j);
-    if (!sp && (dbg != nullptr || dbu != nullptr)) p.kb_chunk = column_blocks(j);
+    if (!sp) p.kb_chunk = column_blocks(j);
     p.c_plane = l.d_plane;
     p.ep.dh = dh;
     p.ep.dh_vec = (a.F * elem(a.dtype)) % 16 == 0;
