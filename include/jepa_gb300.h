@@ -459,6 +459,9 @@ JEPA_API jepa_status jepa_linear_ce_fwd(const void* x, const void* W, const floa
  * loss: dz = dloss (exp(z - lse) - (1 - smoothing) [v = label] - smoothing / V),
  *   dx = dz W (dtype [M, D]), dW = dz^T x (dtype [V, D]), dbias = sum_rows dz
  *   (float [V]); each may be NULL, not all.
+ * The workspace's largest part is dz of a piece of the vocabulary: 2 bytes (F32:
+ * 6) for every row and column of up to 256 MB, or of 4096 columns where that is
+ * more (8 GB for 2^20 rows in 16 bits).
  * z is recomputed.  In F16/BF16 dz is rounded to the type before the products
  * dx and dW, in units of the largest finite |dloss| (so dloss itself costs no
  * precision, and in F16 small probabilities stay normal numbers); dbias is

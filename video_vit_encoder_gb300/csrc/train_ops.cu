@@ -354,11 +354,14 @@ cudaError_t reduce_output(int dtype, const Reduce& rd, Job& j, int z, void* out,
 // (bias gradients).  Many tiles take up to 12 blocks, evenly: a sum less is 5% of
 // a whole backward pass (1999 x 768 x 50021 344 us with 8 + 4, 326 in one go),
 // and dbias is 6e-7 off in norm; in one go over 16 blocks it would be 1.9e-6
-// (4096 x 1024 x 32768).  Of few tiles more sums are affordable.  A call that
-// wants no column sums takes the same blocks, so that its dx and dW are those of
-// one that does (4096 x 1024 x 32768 without dbias 545 us, in one go 516, with it
-// 535; 1024 x 1024 x 1000 29.4, 26.6, 31.8; gates of 16384 x 1024 x 2736 360, 346,
-// 366).
+// (4096 x 1024 x 32768).  Other widths with limits of 8, 12 and 16, 4096 rows,
+// 32768 classes: 640 442, 412, 412 us; 896 519, 519, 501; 1280 657, 615, 615; 1536
+// 830, 768, 768; 2048 1063, 1044, 1015.  Of few tiles more sums are affordable.
+//
+// A call that wants no column sums takes the same blocks, so that its dx and dW
+// are those of one that does (4096 x 1024 x 32768 without dbias 545 us, in one go
+// 516, with it 535; 1024 x 1024 x 1000 29.4, 26.6, 31.8; gates of 16384 x 1024 x
+// 2736 360, 346, 366).
 int column_blocks(const Job& j) {
   const long tiles = (long)j.num_m * j.num_n;
   if (tiles > 4 * kPairs) return ceil_div(j.kb_seg, ceil_div(j.kb_seg, 12));
@@ -746,7 +749,8 @@ CeFwd ce_fwd_layout(const CeArgs& a, void* ws) {
 }
 
 // The backward pass goes over the vocabulary in pieces whose dz takes at most
-// 256 MB, all of the same width up to rounding to 256.
+// 256 MB, but that have 4096 columns at least (more than 32768 rows in 16 bits,
+// 10922 in fp32: 8 GB at 2^20 rows), all of the same width up to rounding to 256.
 struct CeBwd {
   Mat x, w;
   int piece, dz_plane;
