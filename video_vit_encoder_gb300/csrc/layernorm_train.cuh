@@ -15,27 +15,22 @@
 
 namespace jepa {
 
+// V values from or to 16 bytes or a multiple of them; 16-bit results of four
+// fp32 values take 8.
 template <typename T, int V>
 __device__ __forceinline__ void ln_load(const T* p, float (&v)[V]) {
-  if constexpr (V == 1) {
-    v[0] = DT<T>::to(*p);
-  } else if constexpr (sizeof(T) == 4) {
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < V / 4; ++i) {
       const float4 q = reinterpret_cast<const float4*>(p)[i];
       v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
     }
   } else {
-    uint32_t u[V / 2];
-    if constexpr (V == 8) {
-      const uint4 q = *reinterpret_cast<const uint4*>(p);
-      u[0] = q.x; u[1] = q.y; u[2] = q.z; u[3] = q.w;
-    } else {
-      const uint2 q = *reinterpret_cast<const uint2*>(p);
-      u[0] = q.x; u[1] = q.y;
-    }
+    static_assert(V == 8, "16 bytes");
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       T h[2];
       memcpy(h, &u[i], 4);
       v[2 * i] = DT<T>::to(h[0]);
@@ -46,9 +41,7 @@ __device__ __forceinline__ void ln_load(const T* p, float (&v)[V]) {
 
 template <typename T, int V>
 __device__ __forceinline__ void ln_store(T* p, const float (&v)[V]) {
-  if constexpr (V == 1) {
-    *p = DT<T>::from(v[0]);
-  } else if constexpr (sizeof(T) == 4) {
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < V / 4; ++i)
       reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -56,6 +49,7 @@ __device__ __forceinline__ void ln_store(T* p, const float (&v)[V]) {
     *reinterpret_cast<uint4*>(p) =
         make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
   } else {
+    static_assert(V == 4, "8 bytes");
     *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
   }
 }
