@@ -6,7 +6,7 @@ layer's forward pass is ``linear``).  Every computation runs in
 libjepa_gb300.so; torch supplies device memory and streams.
 
 Tensors are contiguous and on one CUDA device, which need not be the current
-one.  Work is enqueued on ``stream``, or on that device's current stream; the
+one; row counts and widths are at most 2^24 (layer norm's width: 2^20).  Work is enqueued on ``stream``, or on that device's current stream; the
 outputs and the workspace are allocated on the stream that uses them, so
 calls on several streams, and captured graphs, never share one.  ``stream``
 has to have waited for whatever wrote the inputs; they may be dropped as soon
@@ -47,10 +47,27 @@ def _expect(name, t, shape, dtype, device):
     raise ValueError(f"{name} must be contiguous")
 
 
+# the library's limit on row counts and widths; it takes them as C ints, into which a larger one may not be squeezed
+_MOST = 1 << 24
+
+
 def _matrix(name, t):
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, has shape {tuple(t.shape)}")
+    if max(t.shape) > _MOST:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: at most {_MOST} rows and columns")
     return t.shape
+
+
+def _rows(shape):
+    """The leading shape, its number of rows and the last dimension of x's."""
+    if not shape:
+        raise ValueError("x must have at least one dimension")
+    lead = shape[:-1]
+    rows, dim = lead.numel(), shape[-1]
+    if rows > _MOST or dim > _MOST:
+        raise ValueError(f"x has shape {tuple(shape)}: at most {_MOST} rows and columns")
+    return lead, rows, dim
 
 
 def _code(name, dtype):
@@ -108,9 +125,7 @@ def layernorm_fwd(x, w, b, eps, out_dtype=None, stream=None):
     [dim].  y has out_dtype (default x's; another one needs float32 x), mean
     and rstd are float32 of x's leading shape."""
     shape, dt, dev = x.shape, x.dtype, x.device
-    if not shape:
-        raise ValueError("x must have at least one dimension")
-    dim, lead = shape[-1], shape[:-1]
+    lead, rows, dim = _rows(shape)
     out_dtype = out_dtype or dt
     xc, yc = _code("x", dt), _code("out_dtype", out_dtype)
     _expect("x", x, shape, dt, dev)
@@ -123,7 +138,7 @@ def layernorm_fwd(x, w, b, eps, out_dtype=None, stream=None):
     mean = _empty(lead, dtype=_f32, device=dev)
     rstd = _like(mean)
     check(_c().jepa_layernorm_fwd(x.data_ptr(), w.data_ptr(), b.data_ptr(), y.data_ptr(), mean.data_ptr(),
-                                  rstd.data_ptr(), lead.numel(), dim, xc, yc, eps, _raw_stream(dev.index)))
+                                  rstd.data_ptr(), rows, dim, xc, yc, eps, _raw_stream(dev.index)))
     return y, mean, rstd
 
 
@@ -132,9 +147,7 @@ def layernorm_bwd(dy, x, w, mean, rstd, residual=None, needs=(True, True), strea
     mean and rstd.  residual: x's shape and dtype, added to dx.  needs: (dw,
     db)."""
     shape, dt, dev = x.shape, x.dtype, x.device
-    if not shape:
-        raise ValueError("x must have at least one dimension")
-    dim, lead = shape[-1], shape[:-1]
+    lead, rows, dim = _rows(shape)
     xc, yc = _code("x", dt), _code("dy", dy.dtype)
     _expect("x", x, shape, dt, dev)
     _expect("dy", dy, shape, dy.dtype, dev)
@@ -145,7 +158,6 @@ def layernorm_bwd(dy, x, w, mean, rstd, residual=None, needs=(True, True), strea
     if _elsewhere(x, stream):
         with _place(x, stream, dy, w, mean, rstd, residual):
             return layernorm_bwd(dy, x, w, mean, rstd, residual, needs)
-    rows = lead.numel()
     dx = _like(x)
     dw = _like(w) if needs[0] else None
     db = _like(w) if needs[1] else None
