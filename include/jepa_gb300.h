@@ -384,9 +384,10 @@ JEPA_API jepa_status jepa_qkv_rope(const void* A, const void* W, const float* bi
                                    float theta, const int32_t* pos_ids, void* stream);
 
 /* ---------------------------------------------------------------- training operators
- * What training a head on the encoder's tokens needs beside the forward
- * operations above.  The source pages stop at inference; these operators have
- * no counterpart there.
+ * For training a classifier and gated MLP blocks on the encoder's tokens,
+ * beside the forward operations above (attention and the un-gated GELU MLP have
+ * no backward pass here).  The source pages stop at inference; these operators
+ * have no counterpart there.
  *
  * Common to all of them:
  *   - dtype (jepa_dtype) is the type T of the matrices; sums, statistics and

@@ -1,5 +1,5 @@
-"""GB300 (sm_103a) V-JEPA 2 / 2.1 video ViT encoder forward, and the operators
-for training a head on its tokens.
+"""GB300 (sm_103a) V-JEPA 2 / 2.1 video ViT encoder forward, and operators for
+training a classifier and gated MLP blocks on its tokens.
 
 The compute lives in ``libjepa_gb300.so`` (hand-written CUDA behind the C ABI
 of ``include/jepa_gb300.h``); this package only marshals arguments.

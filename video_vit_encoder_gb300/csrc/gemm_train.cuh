@@ -44,10 +44,11 @@
 //
 // What bounds it, on large bf16 products: the tensor pipe in the forward passes
 // (gates 16384 x 1024 x 2736 twice: 100 us, pipe busy 92% of the time; cross
-// entropy 8192 x 2048 x 131072: 2.49 ms, 1.77 PFLOP/s); the epilogue's latency
-// in the backward ones (CE_BWD of 1999 x 768 x 50021: 120 us, pipe 63%; GATE_BWD
-// of 16384 x 1024 x 2736: 127 us, 72%); operand delivery in REDUCE (64 k take 640
-// to 710 clocks against the forward passes' 526; pipe 77 to 83%).
+// entropy 8192 x 2048 x 131072: 2.55 ms, 1.72 PFLOP/s, at the power cap, 2.30 ms
+// below it); the epilogue's latency in the backward ones (CE_BWD of 1999 x 768 x
+// 50021: 116 us, pipe 62%; GATE_BWD of 16384 x 1024 x 2736: 124 us, 72%); operand
+// delivery in REDUCE (64 k take 640 to 710 clocks against the forward passes' 526;
+// pipe 74 to 77%).
 #pragma once
 #include "train.h"
 

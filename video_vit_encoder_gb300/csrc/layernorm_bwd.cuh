@@ -25,8 +25,8 @@ constexpr int kMostSmem = 232448;
 // rows in flight each (8192 x 7001 in fp32 with a residual 177 us, with 16
 // warps 224; 8192 x 4093 in bf16 78 and 84); without its table and masks 16
 // warps with fewer rows in flight are faster (16384 x 1536 in fp32 56 us
-// against 64).  16384 x 1024 in fp32 with a 16-bit dy and a residual: 43.6 us,
-// 0.80 of the copy bandwidth; 73728 x 777 in bf16 73 us, 0.70 of it (SHIFT's
+// against 64).  16384 x 1024 in fp32 with a 16-bit dy and a residual: 41.9 us,
+// 0.83 of the copy bandwidth; 73728 x 777 in bf16 70.6 us, 0.72 of it (SHIFT's
 // masks and w's table add instructions).
 template <typename TX, typename TY, int V, int NV, int TPR, bool SHIFT, bool RES>
 struct BwdShape {

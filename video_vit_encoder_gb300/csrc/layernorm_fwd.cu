@@ -4,8 +4,9 @@
 // mean = sum x / n, rstd = 1 / sqrt(sum (x - mean)^2 / n + eps): the centred
 // variance, both sums in fp32 over a row that stays in registers, so x is read
 // once and y written once.  Bound by HBM: 16384 x 1024, fp32 in and bf16 out,
-// 16.7 us (0.89 of the copy bandwidth); 73728 x 777 in bf16 55 us (0.61: shifted
-// vectors cost instructions); 8192 x 2048 in bf16 17.9 us.
+// 17.8 us with its input from HBM (0.84 of the copy bandwidth; 14.2 where part of
+// it is in L2); 73728 x 777 in bf16 55 us (0.61: shifted vectors cost
+// instructions); 8192 x 2048 in bf16 17.9 us.
 #include "layernorm_train.cuh"
 
 namespace jepa {

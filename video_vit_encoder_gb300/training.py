@@ -3,15 +3,17 @@
 Layer norm, gated feed-forward, softmax cross entropy of a linear classifier
 and the linear layer, each as a forward and a backward function (the linear
 layer's forward pass is ``linear``).  Every computation runs in
-libjepa_gb300.so; torch supplies device memory and streams.
+libjepa_gb300.so; torch supplies device memory and streams.  The functions take
+no part in autograd: results carry no graph, whatever the arguments require.
 
 Tensors are contiguous and on one CUDA device, which need not be the current
-one; row counts and widths are at most 2^24 (layer norm's width: 2^20).  Work is enqueued on ``stream``, or on that device's current stream; the
-outputs and the workspace are allocated on the stream that uses them, so
-calls on several streams, and captured graphs, never share one.  ``stream``
-has to have waited for whatever wrote the inputs; they may be dropped as soon
-as the call returns.  Gradients not asked for (``needs``) are returned as
-None.  The first call of a function on a device is made outside a capture.
+one; row counts and widths are at most 2^24 (layer norm's width: 2^20).  Work is
+enqueued on ``stream``, or on that device's current stream; the outputs and the
+workspace are allocated on the stream that uses them, so calls on several
+streams, and captured graphs, never share one.  ``stream`` has to have waited for
+whatever wrote the inputs; they may be dropped as soon as the call returns.
+Gradients not asked for (``needs``) are returned as None.  The first call of a
+function on a device is made outside a capture.
 """
 from __future__ import annotations
 
