@@ -1,5 +1,5 @@
-"""README's training step, as it stands there, at widths that it names as
-allowed; and what it says of autograd."""
+"""The training step that the documentation shows, run as it stands there, at
+widths that it names as allowed; and what it says of autograd."""
 import os
 import re
 
@@ -11,13 +11,13 @@ import test_gpu_training as base
 
 pytestmark = pytest.mark.gpu
 
-README = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+PAGE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
 jg = base.jg
 
 
 @pytest.mark.parametrize("dim,hidden", [(1024, 2752), (384, 1024)])
 def test_training_step(jg, dim, hidden):
-    with open(README) as f:
+    with open(PAGE) as f:
         code = re.search(r"A training step of one gated MLP block.*?```python\n(.*?)```", f.read(), re.S).group(1)
     rng = np.random.default_rng(dim)
     rows, classes = 300, 174
