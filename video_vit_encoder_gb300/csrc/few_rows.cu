@@ -18,8 +18,8 @@
 //
 // Gated feed-forward, 8 rows, 1024 -> 4096, bf16: 16.8 MB of weights, 5.7 us with
 // the weights from HBM, 4.2 from L2 (tiles of 256 rows: 16.5).  Cross entropy, 8
-// rows, 1024 -> 174, fp32: 7.0 us with its joining kernel (tiles: 41); 16 rows, 1024 -> 131072, bf16: 70 us (17
-// rows, on tiles: 96).
+// rows, 1024 -> 174, fp32: 7.0 us with its joining kernel (tiles: 41); 16 rows,
+// 1024 -> 131072, bf16: 70 us (17 rows, on tiles: 96).
 #include "gemm_train.cuh"
 
 namespace jepa {

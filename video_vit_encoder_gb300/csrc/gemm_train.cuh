@@ -1350,7 +1350,9 @@ cudaError_t launch(const Params& p, int num_sms, cudaStream_t s) {
   }, &dev);
   if (e != cudaSuccess) return e;
   const long units = (long)p.units[0] + p.units[1];
-  if (p.units[0] < 1 || p.units[1] < 0 || units > 0x7fffffffl - 4096) return cudaErrorInvalidValue;
+  if (p.units[0] < 1 || p.units[1] < 0 || units > 0x7fffffffl - 4096 || p.kb_chunk < 1) return cudaErrorInvalidValue;
+  for (const Job& j : p.j)   // a STORE takes its whole sum from tensor memory
+    if (EPI == REDUCE && !SPLIT && j.out == STORE && j.kb_split > p.kb_chunk) return cudaErrorInvalidValue;
   const int clusters = units < resident_on[dev] ? (int)units : resident_on[dev];
   cfg.gridDim = dim3(2 * clusters);
   return cudaLaunchKernelEx(&cfg, kern, p);
