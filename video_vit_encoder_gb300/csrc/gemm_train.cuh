@@ -104,7 +104,7 @@ struct EpiArgs {
   int dz_inline;           // dz_scale is computed here, and written for the kernels that follow
   float smoothing;
   float z_scale;           // DISTILL: log2 e / temperature
-  float z_loss;            // DISTILL: the part of acc that the accumulator's truncation takes off it
+  float z_loss;            // DISTILL, 16-bit: the part of acc that the accumulator's truncation takes off it
   const uint32_t* hits;    // DISTILL_FWD: [M][top] a row's wanted columns (Hits)
   const uint16_t* starts;  // DISTILL_FWD: [M][2][runs + 1] where those of a half and a run begin
   float* hit_z;            // DISTILL_FWD: [M][top] where their z go
@@ -592,7 +592,7 @@ __device__ __forceinline__ float pick(const float* v, int i) {
   return t[0];
 }
 
-template <bool SUM, bool DISTILL = false>
+template <bool SUM, bool DISTILL = false, bool SPLIT = false>
 __device__ __forceinline__ void ce_fwd_tile(const Params& p, float (&v)[128], int row, int col0, int lane, int label,
                                             RowStats& st, Hits& hits, int run_col) {
   const EpiArgs& ep = p.ep;
@@ -609,7 +609,7 @@ __device__ __forceinline__ void ce_fwd_tile(const Params& p, float (&v)[128], in
     const int col = col0 + c * 32;
     if (col >= p.j[0].N) continue;
     float* w = v + c * 32;
-    if constexpr (DISTILL) {
+    if constexpr (DISTILL && !SPLIT) {   // planes lose nothing that is given back; 0 times an infinite sum would be NaN
 #pragma unroll
       for (int j = 0; j < 32; j += 2) fma2(w[j], w[j + 1], ep.z_loss, w[j], w[j + 1]);
     }
@@ -796,7 +796,7 @@ __device__ __forceinline__ void ce_bwd_tile(const Params& p, float (&v)[128], co
       for (int i = 0; i < 4; ++i) {
         float& z0 = v[block_at(q, g, i)];
         float& z1 = v[block_at(q, g, i) + 1];
-        if constexpr (DISTILL) {
+        if constexpr (DISTILL && !SPLIT) {   // as in ce_fwd_tile
           float t0 = z0, t1 = z1;
           add2f(t0, t1, bias.b[g].x, bias.b[g].y);
           fma2(z0, z1, ep.z_loss, t0, t1);
@@ -1374,7 +1374,7 @@ __global__ void __launch_bounds__(Shape<SPLIT, EPI>::kThreads, 1) train_gemm_ker
           if constexpr (ce_fwd(EPI)) {
             if constexpr (EPI == DISTILL_FWD)
               if (r == 0) wait_hits(hits);
-            if constexpr (EPI == DISTILL_FWD) ce_fwd_tile<false, true>(p, v, row, col, lane, label, st, hits, r * kBN + half * (kBN / 2));
+            if constexpr (EPI == DISTILL_FWD) ce_fwd_tile<false, true, SPLIT>(p, v, row, col, lane, label, st, hits, r * kBN + half * (kBN / 2));
             else if (p.ep.part_sum != nullptr) ce_fwd_tile<true>(p, v, row, col, lane, label, st, hits, r * kBN + half * (kBN / 2));
             else ce_fwd_tile<false>(p, v, row, col, lane, label, st, hits, r * kBN + half * (kBN / 2));
           } else if constexpr (ce_bwd(EPI)) {
