@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) teacher_kernel(const TT* __res
                                                                  int* status) {
   extern __shared__ uint64_t keys[];   // of each warp: (class, place), sorted
   if (acc != nullptr)
-    for (int v = blockIdx.x * 32 * kRowWarps + threadIdx.x; v < V; v += gridDim.x * 32 * kRowWarps) acc[v] = 0;
+    for (int v = blockIdx.x * 32 * kRowWarps + threadIdx.x; v < 2 * V; v += gridDim.x * 32 * kRowWarps) acc[v] = 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = power_of_2(K);
   const long row = (long)blockIdx.x * kRowWarps + warp;
   if (row >= M) return;
@@ -219,9 +219,12 @@ __global__ void __launch_bounds__(32 * kRowWarps) teacher_kernel(const TT* __res
   }
 }
 
-// The teacher's part of dbias is summed in whole numbers, whose sum has no order;
-// with HELD a block sums those of a few classes in shared memory first (5555 rows
-// of 62 entries over 80 classes in global memory 64 us).
+// The teacher's part of dbias is summed in whole numbers, whose sum has no order: of
+// 2^-shift of the unit, and of 2^-2 shift for what that leaves of an entry (nothing,
+// unless its dloss times its probability is below 2^(24 - shift) of the unit), so that
+// an entry keeps fp32's accuracy next to a row whose dloss is 2^(2 shift - 24) times as
+// large.  With HELD a block sums those of a few classes in shared memory first (5555
+// rows of 62 entries over 80 classes in global memory 64 us).
 constexpr int kHeldClasses = 2048;
 template <typename T, bool SPLIT, bool HELD>
 __global__ void __launch_bounds__(kBlock) put_kernel(const __grid_constant__ DistillPut q) {
@@ -250,9 +253,13 @@ __global__ void __launch_bounds__(kBlock) put_kernel(const __grid_constant__ Dis
       reinterpret_cast<T*>(q.dz)[row * q.ld + c] = DT<T>::from(ds * (dl / *q.unit * q.factor));
     }
     if (q.acc != nullptr && fabsf(dl) < INFINITY) {
-      const unsigned long long a = (unsigned long long)__float2ll_rn(ldexpf(p * (dl / *q.unit), q.shift));
-      if constexpr (HELD) atomicAdd(held + cls, a);
-      else atomicAdd(reinterpret_cast<unsigned long long*>(q.acc + cls), a);
+      const float t = ldexpf(p * (dl / *q.unit), q.shift);
+      const long long a = __float2ll_rn(t);
+      const float left = t - (float)a;   // exact: a is t's own digits, or t < 2^24
+      if constexpr (HELD) atomicAdd(held + cls, (unsigned long long)a);
+      else atomicAdd(reinterpret_cast<unsigned long long*>(q.acc + cls), (unsigned long long)a);
+      if (left != 0.f)
+        atomicAdd(reinterpret_cast<unsigned long long*>(q.acc + q.V + cls), (unsigned long long)__float2ll_rn(ldexpf(left, q.shift)));
     }
   }
   if constexpr (HELD) {

@@ -69,7 +69,7 @@ cudaError_t distill_join(const DistillArgs& a, const float2* ms, int parts, cons
                          cudaStream_t s);
 // Of each row: label (0, or -1 where it has no gradient) and dloss tau; of each
 // entry its class, or -1 (out, or joined with an earlier one of its class), and probability.
-// acc [V], or null: set to 0.
+// acc [2][V], or null: set to 0.
 cudaError_t distill_teacher(const DistillArgs& a, const float* dloss, int64_t* label, float* dl, int* cls, float* prob,
                             long long* acc, cudaStream_t s);
 // The entries' dz, written over those of the columns v0 .. v0 + n.
@@ -81,7 +81,7 @@ struct DistillPut {
   const float* unit;          // on the device: what dl is divided by (acc: always; 16-bit dz: also)
   uint16_t* dz;               // [M][ld], fp32: planes of plane_rows rows
   long ld, plane_rows;
-  long long* acc;             // [V] or null: gets prob dl / unit 2^shift
+  long long* acc;             // [2][V] or null: gets prob dl / unit 2^shift, and what is left of that times 2^shift
   int shift;
 };
 cudaError_t distill_put(int dtype, const DistillPut& q, int num_sms, cudaStream_t s);

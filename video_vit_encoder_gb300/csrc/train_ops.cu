@@ -456,7 +456,8 @@ struct Finish {
   long ld;
   int part_rows, n, sums;
   unsigned sum_blocks; // of each
-  const long long* less;   // what the first one's are lessened by, in units of *less_unit 2^-less_shift, or null
+  // what the first one's are lessened by, in units of *less_unit 2^-less_shift, and of *less_unit 2^-2 less_shift; or null
+  const long long *less, *less_low;
   const float* less_unit;
   int less_shift;
 };
@@ -475,7 +476,8 @@ __device__ __forceinline__ void part_sum(const Finish& f, int k, int block, cons
   if (g == 0 && c < f.n) {
     for (int j = 1; j < G; ++j) s += sm[j][lane];
     float sum = scale != nullptr ? s * __ldg(scale) : s;
-    if (k == 0 && f.less != nullptr) sum -= ldexpf((float)f.less[c], -f.less_shift) * __ldg(f.less_unit);
+    if (k == 0 && f.less != nullptr)
+      sum -= (ldexpf((float)f.less[c], -f.less_shift) + ldexpf((float)f.less_low[c], -2 * f.less_shift)) * __ldg(f.less_unit);
     f.sum[k][c] = sum;
   }
 }
@@ -850,7 +852,7 @@ cudaError_t ce_statistics(const CeArgs& a, const CeFwd& l, int epi, const tg::Ep
   return gemm(a.dtype, epi, p, a.num_sms, s);
 }
 
-// What the sums of a distillation's dz do not have in them: acc[v] 2^-shift unit.
+// What the sums of a distillation's dz do not have in them: (acc[v] + acc[V + v] 2^-shift) 2^-shift unit.
 struct Less {
   const long long* acc;
   int shift;
@@ -938,6 +940,7 @@ cudaError_t ce_gradients(const CeArgs& a, const CeBwd& l, int epi, float z_scale
     if (dbias != nullptr) add_part_sum(q, l.colp, dbias + v0, l.piece, ceil_div(a.M, 32), n);
     if (less.acc != nullptr) {
       q.less = less.acc + v0;
+      q.less_low = q.less + a.V;
       q.less_unit = l.scale;
       q.less_shift = less.shift;
     }
@@ -995,7 +998,7 @@ DistillBwd distill_bwd_layout(const DistillArgs& a, void* ws) {
   l.dl = cv.take<float>((size_t)a.ce.M * 4);
   l.prob = cv.take<float>(n * 4);
   l.cls = cv.take<int>(n * 4);
-  l.acc = cv.take<long long>((size_t)a.ce.V * 8);
+  l.acc = cv.take<long long>((size_t)a.ce.V * 16);
   l.bytes = cv.used;
   return l;
 }
@@ -1057,7 +1060,8 @@ cudaError_t linear_distill_bwd(const DistillArgs& a, const float* lse, const flo
     dz_unit_kernel<<<1, 1024, 0, s>>>(l.dl, l.label, -1, c.M, c.V, dz_factor(c.dtype, 0.f), 0.f, l.ce.scale);
     JEPA_TRY_CUDA(cudaGetLastError());
   }
-  // a class's sum of up to M probabilities of at most 1 (and the rounding of each) stays below 2^62
+  // a class's sum of up to M probabilities of at most 1 (and the rounding of each) stays below 2^62, and so do M halves of
+  // what is left
   int shift = 61;
   while (((long)1 << (61 - shift)) < c.M) --shift;
   DistillPut q{l.cls, l.prob, z, lse, l.dl, c.M, a.K, 0, 0, c.V, tg::kLog2e / a.tau, dz_factor(c.dtype, 0.f),
