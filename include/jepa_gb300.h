@@ -592,8 +592,8 @@ JEPA_API jepa_status jepa_linear_distill_bwd(const void* x, const void* W, const
 
 /* Synchronises `stream` and reports a device-side timeout recorded by any
  * earlier single-operation call (jepa_attention, jepa_linear, jepa_qkv_rope,
- * jepa_linear_ce_*, jepa_gated_ffn_*, jepa_linear_bwd, jepa_linear_distill_*)
- * of this process (then clears it), or ids outside the grid given to
+ * jepa_linear_ce_*, jepa_gated_ffn_*, jepa_linear_bwd, jepa_linear_distill_*,
+ * jepa_gated_scan_*) of this process (then clears it), or ids outside the grid given to
  * jepa_qkv_rope, or labels, tokens or a teacher's ids outside the vocabulary
  * given to jepa_linear_ce_*, jepa_embedding_* or jepa_linear_distill_*, or
  * lengths outside their range given to jepa_gated_scan_* (JEPA_ERR_ARG). */
@@ -604,6 +604,9 @@ JEPA_API jepa_status jepa_ops_sync(void* stream);
  * synchronises.  Returns JEPA_ERR_DEVICE_TIMEOUT when the kernel reported
  * the expired wait (the expected outcome); the context stays usable. */
 JEPA_API jepa_status jepa_selftest_wait_timeout(int timeout_us, void* stream);
+/* The same of the wait with which the blocks of jepa_gated_scan_* exchange their
+ * maps. */
+JEPA_API jepa_status jepa_selftest_scan_wait_timeout(int timeout_us, void* stream);
 
 /* Patch embedding that allocates no device memory.  The paper has no
  * counterpart: this entry point exists for callers that cannot call

@@ -9,7 +9,7 @@ from .binding import (  # noqa: F401
     Encoder, Head, Predictor, attention, blob_check, encoder_params, encoder_tensor_order, head_params, head_tensor_order,
     layernorm_f32, linear,
     ops_sync, pack_blob, predictor_params, predictor_tensor_order, qkv_rope, rope3d_f32,
-    selftest_wait_timeout,
+    selftest_scan_wait_timeout, selftest_wait_timeout,
 )
 from .decoder import (  # noqa: F401
     embedding_bwd, embedding_fwd, gated_scan_bwd, gated_scan_fwd, linear_distill_bwd, linear_distill_fwd,

@@ -83,6 +83,7 @@ SIGNATURES = {
     "jepa_qkv_rope": (ST, [VP, VP, VP, VP, VP, VP, I, I, I, I, I, I, I, I, I, I, I, I, F, VP, VP]),
     "jepa_ops_sync": (ST, [VP]),
     "jepa_selftest_wait_timeout": (ST, [I, VP]),
+    "jepa_selftest_scan_wait_timeout": (ST, [I, VP]),
     "jepa_patch_embed_static": (ST, [VP, VP, VP, VP, VP, I, I, I, I, I, I, VP]),
     "jepa_head_blob_check": (ST, [VP, U64, C.POINTER(HeadParams)]),
     "jepa_head_create": (ST, [VP, U64, C.POINTER(HeadParams), I, C.POINTER(VP)]),

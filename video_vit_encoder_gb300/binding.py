@@ -453,3 +453,8 @@ def ops_sync():
 def selftest_wait_timeout(timeout_us: int) -> int:
     """Returns the status code (JEPA_ERR_DEVICE_TIMEOUT expected)."""
     return int(load().jepa_selftest_wait_timeout(timeout_us, _stream()))
+
+
+def selftest_scan_wait_timeout(timeout_us: int) -> int:
+    """The same of the gated recurrence's wait."""
+    return int(load().jepa_selftest_scan_wait_timeout(timeout_us, _stream()))

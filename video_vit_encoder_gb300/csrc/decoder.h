@@ -31,5 +31,7 @@ struct ScanArgs {
 cudaError_t gated_scan_fwd(const ScanArgs& a, const float* h0, void* h, float* last, float* states, cudaStream_t s);
 cudaError_t gated_scan_bwd(const ScanArgs& a, const void* dh, const float* states, const float* dlast, void* dgv,
                            float* dh0, cudaStream_t s);
+// A wait of the exchange between blocks that runs out after limit_ns.
+cudaError_t gated_scan_wait_selftest(int* status, uint64_t limit_ns, cudaStream_t s);
 
 }  // namespace jepa

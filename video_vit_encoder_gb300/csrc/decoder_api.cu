@@ -145,6 +145,15 @@ jepa_status jepa_gated_scan_bwd(const void* dh, const void* gv, const float* sta
   return cuda_result(gated_scan_bwd(a, dh, states, dlast, dgv, dh0, (cudaStream_t)stream), "gated_scan_bwd");
 }
 
+jepa_status jepa_selftest_scan_wait_timeout(int timeout_us, void* stream) {
+  if (timeout_us < 1 || timeout_us > 5000000) return api_fail(JEPA_ERR_ARG, "timeout_us %d (1 .. 5e6)", timeout_us);
+  int* status = nullptr;
+  ARG_TRY(api_ops_status(&status));
+  const uint64_t limit_ns = (uint64_t)timeout_us * 1000ull;
+  ARG_TRY(cuda_result(gated_scan_wait_selftest(status, limit_ns, (cudaStream_t)stream), "gated_scan_wait_selftest"));
+  return jepa_ops_sync(stream);
+}
+
 // ============================================================================= distillation
 size_t jepa_linear_distill_workspace_bytes(int M, int D, int V, int K, int dtype, int backward) {
   if (bad_rows(M) || bad_width(D) || bad_width(V) || K < 1 || K > kMaxTop || bad_dtype(dtype)) return 0;

@@ -270,7 +270,7 @@ __device__ __forceinline__ void send_map(uint32_t at, uint32_t bar, const Map<CH
                  "f"(m.v[0].get(0)), "f"(m.v[1].get(0)), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
   const uint32_t a = smem_u32(bar);
   auto arrived = [&] {
     uint32_t ok;
@@ -289,7 +289,7 @@ __device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (arrived()) return true;
-    if ((unsigned long long)(clock64() - t0) > 2ull * kWaitLimitNs) return false;
+    if ((unsigned long long)(clock64() - t0) > 2ull * limit_ns) return false;
   }
 }
 // By one warp.  round: how often this has been called before.  late: a wait has run
@@ -731,6 +731,18 @@ __global__ void __launch_bounds__(kFewThreads) few_bwd_kernel(const __grid_const
   if (dh0 != nullptr) store_state<CH>(dh0 + at, l);
 }
 
+// ----------------------------------------------------------------------------- self test
+// A wait for maps that nobody sends.
+__global__ void wait_maps_kernel(int* status, uint64_t limit_ns) {
+  __shared__ uint64_t bar;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (!wait_maps(&bar, 0, limit_ns)) atomicOr(status, DEV_TIMEOUT);
+}
+
 // ----------------------------------------------------------------------------- launch
 constexpr size_t kAloneBytes = 120 << 10;   // of shared memory, more than any launch takes: no two blocks on one SM
 // How a kernel fills a device: the clusters of each size that run at once.
@@ -830,6 +842,11 @@ int stage_of(const ScanArgs& a, const void* x, const void* y) {
 }
 
 }  // namespace
+
+cudaError_t gated_scan_wait_selftest(int* status, uint64_t limit_ns, cudaStream_t s) {
+  wait_maps_kernel<<<1, 32, 0, s>>>(status, limit_ns);
+  return cudaGetLastError();
+}
 
 cudaError_t gated_scan_fwd(const ScanArgs& a, const float* h0, void* h, float* last, float* states, cudaStream_t s) {
   if (a.batch == 0) return cudaSuccess;
