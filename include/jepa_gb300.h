@@ -523,7 +523,9 @@ JEPA_API jepa_status jepa_embedding_fwd(const int64_t* tokens, const void* table
                                         int table_dtype, int out_dtype, float scale, int64_t ignore_index,
                                         void* stream);
 /* Its gradient: dtable[v, :] = scale * the sum of dout[i, :] over the i with
- * tokens[i] = v, in fp32 and in their order; rows without a token are zeros.
+ * tokens[i] = v, in fp32 and in an order that the tokens alone decide (16 of a
+ * token's places at a time in theirs, then these sums); rows without a token are
+ * zeros.
  *   dout: dout_dtype [n, dim] (the forward pass's out_dtype); dtable:
  *   dtable_dtype [vocab, dim].  Tokens that have no row of the table have no part
  *   in it (one outside [0, vocab) is reported as above). */

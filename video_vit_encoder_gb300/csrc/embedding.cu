@@ -1,9 +1,10 @@
 // Embedding of tokens, out[i] = scale table[token i], and the table's gradient.
 //
 // The gradient of a row is a sum over the places of its token, which is made in
-// their order whatever the schedule: the tokens are sorted, chunks of the sorted
-// places are summed on their own, and runs of one token that cross a chunk's
-// border are joined from the chunks' parts.
+// an order that the tokens alone decide, whatever the schedule: the tokens are
+// sorted, chunks of 16 sorted places are summed on their own, in the places' order,
+// and runs of one token that cross a chunk's border are joined from the chunks'
+// parts, a short run's in order, a long one's by 32 warps that take every 32nd.
 //
 // Both are bound by memory where they are large: 65536 x 1024 of 131072 rows of bf16
 // from and to fp32 takes 50 us forward (0.91 of the copy bandwidth) and 107 backward
