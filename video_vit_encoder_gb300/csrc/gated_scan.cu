@@ -270,7 +270,10 @@ __device__ __forceinline__ void send_map(uint32_t at, uint32_t bar, const Map<CH
                  "f"(m.v[0].get(0)), "f"(m.v[1].get(0)), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
+// late: whether an earlier wait of the block has run out, after which none is
+// waited for.
+__device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity, const volatile uint32_t* late,
+                                          uint64_t limit_ns = kWaitLimitNs) {
   const uint32_t a = smem_u32(bar);
   auto arrived = [&] {
     uint32_t ok;
@@ -284,6 +287,7 @@ __device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity, uint64
     return ok != 0;
   };
   if (arrived()) return true;
+  if (*late != 0) return false;
   const long long t0 = clock64();
   while (true) {
 #pragma unroll 1
@@ -292,20 +296,21 @@ __device__ __forceinline__ bool wait_maps(uint64_t* bar, uint32_t parity, uint64
     if ((unsigned long long)(clock64() - t0) > 2ull * limit_ns) return false;
   }
 }
-// By one warp.  round: how often this has been called before.  late: a wait has run
-// out (it is reported, the results are wrong, and no other wait is begun).  Returns
+// By one warp.  round: how often this has been called before.  A wait that runs out
+// is reported and noted after the barriers, and the results are wrong.  Returns
 // where the round's maps are.
 template <int CH>
 __device__ __forceinline__ const Map<CH, 2> (*exchange(Map<CH, 2> (*ring)[32], uint64_t* bars, const Map<CH, 2>& mine, const Place& p,
-                                                       int lane, int round, bool& late, int* status))[32] {
+                                                       int lane, int round, int* status))[32] {
   uint64_t* bar = bars + (round & 1);
   Map<CH, 2>(*to)[32] = ring + (round & 1) * p.ranks;
   if (lane == 0) mbar_arrive_expect_tx(bar, p.ranks * 32 * (uint32_t)sizeof(Map<CH, 2>));
   const uint32_t at = smem_u32(&to[p.rank][lane]), at_bar = smem_u32(bar);
 #pragma unroll 4
   for (int r = 0; r < p.ranks; ++r) send_map<CH>(mapa_shared(at, r), mapa_shared(at_bar, r), mine);
-  if (!late && !wait_maps(bar, round >> 1 & 1)) {
-    late = true;
+  volatile uint32_t* late = reinterpret_cast<volatile uint32_t*>(bars + 2);
+  if (!wait_maps(bar, round >> 1 & 1, late)) {
+    *late = 1;
     atomicOr(status, DEV_TIMEOUT);
   }
   return to;
@@ -316,22 +321,26 @@ __device__ __forceinline__ void open_cluster(uint64_t* bars) {
   if (threadIdx.x == 0) {
     mbar_init(bars, 1);
     mbar_init(bars + 1, 1);
+    *reinterpret_cast<volatile uint32_t*>(bars + 2) = 0;
     fence_mbar_init();
   }
   __syncwarp();
   cluster_sync();
 }
 // After the last one: no block's shared memory goes while another may write to it.
-__device__ __forceinline__ void close_cluster() {
+// A block whose wait has run out has not waited for all of the maps, which every
+// block has sent by then: it stays until they have long arrived.
+__device__ __forceinline__ void close_cluster(const uint64_t* bars) {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  if (*reinterpret_cast<const volatile uint32_t*>(bars + 2) != 0) __nanosleep(1000000);
 }
 
 // ----------------------------------------------------------------------------- forward
-// Shared memory after the words: the warps' maps, the cluster's maps of two rounds, the state before the piece, and two
-// barriers.
+// Shared memory after the words: the warps' maps, the cluster's maps of two rounds, the state before the piece, two
+// barriers, and whether a wait has run out.
 template <int CH> constexpr size_t fwd_bytes(int ranks) {
-  return (size_t)32 * CH * 4 * (2 * kWarps<kFwdSteps> + 2 * 2 * ranks + 1) + 16;
+  return (size_t)32 * CH * 4 * (2 * kWarps<kFwdSteps> + 2 * 2 * ranks + 1) + 32;
 }
 template <typename T, int CH, int STAGE>
 __global__ void __launch_bounds__(kThreads<kFwdSteps>, 2) scan_fwd_kernel(const __grid_constant__ ScanArgs a, int ranks,
@@ -369,7 +378,6 @@ __global__ void __launch_bounds__(kThreads<kFwdSteps>, 2) scan_fwd_kernel(const 
   if (p.ranks > 1) open_cluster(bars);
   if constexpr (STAGE != PLAIN)
     if (p.pieces > 0) fetch(p.rank, 0);
-  bool late = false;
   for (int first = 0, round = 0; first < p.pieces; first += p.ranks, ++round) {
     const int piece = first + p.rank;
     const int t0 = piece * kScanPiece + warp * S;
@@ -430,7 +438,7 @@ __global__ void __launch_bounds__(kThreads<kFwdSteps>, 2) scan_fwd_kernel(const 
       }
       V x = carry;
       if (p.ranks > 1) {
-        const auto at = exchange<CH>(ring, bars, all, p, lane, round, late, a.status);
+        const auto at = exchange<CH>(ring, bars, all, p, lane, round, a.status);
 #pragma unroll 4
         for (int r = 0; r < p.ranks; ++r) {
           if (r == p.rank) x = carry;
@@ -465,14 +473,14 @@ __global__ void __launch_bounds__(kThreads<kFwdSteps>, 2) scan_fwd_kernel(const 
       }
     }
   }
-  if (p.ranks > 1) close_cluster();
+  if (p.ranks > 1) close_cluster(bars);
   if (last != nullptr && p.on && p.rank == 0 && warp == 0) store_state<CH>(last + p.b * C + p.c, carry);
 }
 
 // ----------------------------------------------------------------------------- backward
 // As fwd_bytes, with the maps of both directions, those of what is after each warp's steps, and the states before them.
 template <int CH> constexpr size_t bwd_bytes(int ranks) {
-  return (size_t)32 * CH * 4 * (6 * kWarps<kBwdSteps> + 2 * 2 * ranks + 1) + 16;
+  return (size_t)32 * CH * 4 * (6 * kWarps<kBwdSteps> + 2 * 2 * ranks + 1) + 32;
 }
 template <typename T, int CH, int STAGE>
 __global__ void __launch_bounds__(kThreads<kBwdSteps>, 512 / kThreads<kBwdSteps>)
@@ -524,7 +532,6 @@ __global__ void __launch_bounds__(kThreads<kBwdSteps>, 512 / kThreads<kBwdSteps>
       fetch_dh((groups - 1) * p.ranks + p.rank, 0);
       copy_commit();
     }
-  bool late = false;
   for (int group = groups - 1, round = 0; group >= 0; --group, ++round) {
     const int piece = group * p.ranks + p.rank;
     const int t0 = piece * kScanPiece + warp * S;
@@ -603,7 +610,7 @@ __global__ void __launch_bounds__(kThreads<kBwdSteps>, 512 / kThreads<kBwdSteps>
       }
       V l = carry;
       if (p.ranks > 1) {
-        const auto at = exchange<CH>(ring, bars, all, p, lane, round, late, a.status);
+        const auto at = exchange<CH>(ring, bars, all, p, lane, round, a.status);
 #pragma unroll 4
         for (int r = p.ranks - 1; r >= 0; --r) {
           if (r == p.rank) l = carry;
@@ -654,7 +661,7 @@ __global__ void __launch_bounds__(kThreads<kBwdSteps>, 512 / kThreads<kBwdSteps>
       }
     }
   }
-  if (p.ranks > 1) close_cluster();
+  if (p.ranks > 1) close_cluster(bars);
   if (dh0 != nullptr && p.on && p.rank == 0 && warp == 0) store_state<CH>(dh0 + p.b * C + p.c, carry);
 }
 
@@ -735,12 +742,14 @@ __global__ void __launch_bounds__(kFewThreads) few_bwd_kernel(const __grid_const
 // A wait for maps that nobody sends.
 __global__ void wait_maps_kernel(int* status, uint64_t limit_ns) {
   __shared__ uint64_t bar;
+  __shared__ uint32_t late;
   if (threadIdx.x == 0) {
+    late = 0;
     mbar_init(&bar, 1);
     fence_mbar_init();
   }
   __syncwarp();
-  if (!wait_maps(&bar, 0, limit_ns)) atomicOr(status, DEV_TIMEOUT);
+  if (!wait_maps(&bar, 0, &late, limit_ns)) atomicOr(status, DEV_TIMEOUT);
 }
 
 // ----------------------------------------------------------------------------- launch
