@@ -219,7 +219,7 @@ __device__ __forceinline__ W staged(const uint8_t* tile, int i, const Shift& s, 
 // ----------------------------------------------------------------------------- blocks
 // A thread's place: its sequence, its channels (c; the slab's first is c0).
 struct Place {
-  int b, c0, c, n, end, rank, ranks, pieces;   // n: steps that count, end: that there are (both 0 past the last channel)
+  int b, c0, c, n, end, rank, ranks, pieces;   // n: the sequence's steps, for every lane; end: those of gv, 0 past the last channel
   bool on, full;                               // its channels exist, all the slab's do
 };
 template <int CH>
@@ -406,6 +406,8 @@ __global__ void __launch_bounds__(kThreads<kFwdSteps>, 2) scan_fwd_kernel(const 
           if (whole || (p.on && t0 + i < p.n)) {
             gw[i] = *reinterpret_cast<const W*>(src + (size_t)i * 2 * C);
             vw[i] = *reinterpret_cast<const W*>(src + (size_t)i * 2 * C + C);
+          } else {
+            gw[i] = vw[i] = W{};
           }
       }
 #pragma unroll
@@ -561,6 +563,8 @@ __global__ void __launch_bounds__(kThreads<kBwdSteps>, 512 / kThreads<kBwdSteps>
             gw[i] = *reinterpret_cast<const W*>(src + (size_t)i * 2 * C);
             vw[i] = *reinterpret_cast<const W*>(src + (size_t)i * 2 * C + C);
             dw[i] = *reinterpret_cast<const W*>(dh + (size_t)(t0 + i) * C + p.c);
+          } else {
+            gw[i] = vw[i] = dw[i] = W{};
           }
       }
 #pragma unroll
