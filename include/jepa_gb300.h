@@ -575,6 +575,10 @@ JEPA_API jepa_status jepa_gated_scan_bwd(const void* dh, const void* gv, const f
  * named twice counts twice.  An id outside [0, V) that is not ignore_index gives
  * its row loss NaN, no gradient, and JEPA_ERR_ARG from the next jepa_ops_sync.
  * A teacher's logit of NaN or +infinity makes its row's loss and gradient NaN.
+ * In F16/BF16 a logit is given back what the tensor core's truncation takes off a
+ * sum of D products on average; one whose sum is exact comes out larger by that, at
+ * most 7 x 2^-23 of itself (not so where M is at most 16 and D a multiple of 8,
+ * whose products are made elsewhere).
  * K is 1 .. 1024, the temperature 0.001 .. 1000. */
 JEPA_API size_t jepa_linear_distill_workspace_bytes(int M, int D, int V, int K, int dtype, int backward);
 JEPA_API jepa_status jepa_linear_distill_fwd(const void* x, const void* W, const float* bias, const void* top_logits,
