@@ -28,14 +28,16 @@
 // rows of 16-bit channels that are not aligned to words are read in place, one
 // channel a thread (two from shared memory take more to read than they save: 3 x
 // 4609 x 777 in bf16 40 us forward and 56 backward, with SHIFTED rows 44 and 74, when
-// this was decided; now 30 and 51).
+// this was decided; now 27 and 48, for a floor of 9.5 and 16).
 //
 // 16-bit types move 6 bytes of memory a channel and step forward and 10 backward.
-// 16 x 2048 x 1024 in bf16 takes 36 us forward and 58 backward, 0.83 and 0.85 of the
-// copy bandwidth: issue and the waits for the one warp.  f and u of 16 steps are 64 of
-// a thread's 128 registers, which leaves 16 warps an SM.  One sequence of 73728 x 1024
-// (121 us, 0.55) is bound by its chain of rounds, 2.7 us each: read, map, exchange,
-// write.
+// 16 x 2048 x 1024 in bf16 takes 35 us forward and 59 backward, 0.84 of the copy
+// bandwidth both: issue and the waits for the one warp.  f and u of 16 steps are 64 of
+// a thread's 128 registers, which leaves 16 warps an SM; backward f, k and h - v are
+// 96 of them, and the 16-bit forms spill, 68 bytes of stores and 52 of loads a thread
+// where rows are copied 16 bytes at a time, 264 and 224 where 4 (even widths that are
+// no multiple of 8: 3 x 4609 x 778 73 us, 776 53).  One sequence of 73728 x 1024 (118
+// us, 0.57) is bound by its chain of rounds, 2.6 us each: read, map, exchange, write.
 #include <cmath>
 
 #include "decoder.h"

@@ -198,7 +198,9 @@ def linear_distill_bwd(dloss, x, W, bias, top_logits, top_ids, lse, z, temperatu
                        needs=(True, True, True), stream=None):
     """(dx, dW, dbias) from dloss, the gradient of each row's loss (float [M],
     or one number for all rows: 1 / n for the mean of n rows), and the forward
-    pass's lse and z.  needs: (dx, dW, dbias)."""
+    pass's lse and z.  needs: (dx, dW, dbias).  In 16 bits the logits' gradient
+    is rounded to the type between the products, so that dx and dW carry one
+    rounding more than their own; in float32 it is not."""
     M, D, V, K, code, tcode = _distill_args(x, W, bias, top_logits, top_ids)
     dev = x.device
     _expect("lse", lse, (M,), _f32, dev)
