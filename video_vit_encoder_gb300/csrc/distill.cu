@@ -129,11 +129,11 @@ __global__ void __launch_bounds__(32 * kRowWarps) hits_kernel(const int64_t* __r
   }
 }
 
-// A row's sum p (log p - z / tau), and its kind, by a warp.
+// A row's sum p (log p - (z / tau - lse)), by a warp: entry by entry, or what the logits have in common would be
+// taken off lse only after the sum, of which it takes digits.
 template <typename TT>
-__device__ __forceinline__ float2 row_term(const TT* top, const int64_t* ids, const float* z, int K, int V, long ignore,
-                                           float inv_tau, int lane) {
-  const Teacher t = teacher_row(top, ids, K, V, ignore, inv_tau, lane);
+__device__ __forceinline__ float row_term(const Teacher& t, const TT* top, const int64_t* ids, const float* z, float lse, int K,
+                                          int V, long ignore, float inv_tau, int lane) {
   const float log_sum = logf(t.sum);
   float term = 0.f;
   for (int j = lane; j < K; j += 32) {
@@ -141,9 +141,9 @@ __device__ __forceinline__ float2 row_term(const TT* top, const int64_t* ids, co
     if (id == ignore || id < 0 || id >= V) continue;
     const float a = (DT<TT>::to(top[j]) - t.max) * inv_tau;
     const float p = expf(a) / t.sum;
-    if (!(p == 0.f)) term += p * ((a - log_sum) - z[j] * inv_tau);   // a class without mass adds nothing, whatever its z
+    if (!(p == 0.f)) term += p * ((a - log_sum) - (z[j] * inv_tau - lse));   // a class without mass adds nothing, whatever its z
   }
-  return make_float2(warp_sum(term), (float)t.kind);
+  return warp_sum(term);
 }
 // A warp a row: its parts, every 32nd a lane, then its entries.
 template <typename TT>
@@ -161,17 +161,19 @@ __global__ void __launch_bounds__(kBlock) distill_join_kernel(const float2* __re
     const float2 q = __ldg(ms + (size_t)k * M + row);
     ms_join(a, q.x, q.y, 0.f);
   }
-  const float2 t = row_term(top + row * K, ids + row * K, z + row * K, K, V, ignore, 1.0f / tau, lane);
+  const float inv_tau = 1.0f / tau;
+  const Teacher t = teacher_row(top + row * K, ids + row * K, K, V, ignore, inv_tau, lane);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float m = __shfl_xor_sync(0xffffffffu, a.m, o), v = __shfl_xor_sync(0xffffffffu, a.s, o);
     ms_join(a, m, v, 0.f);
   }
+  const float lse = __shfl_sync(0xffffffffu, (a.m + log2f(a.s)) * 0.69314718055994531f, 0);   // ln(2^m s)
+  const float term = row_term(t, top + row * K, ids + row * K, z + row * K, lse, K, V, ignore, inv_tau, lane);
   if (lane != 0) return;
-  const float lse = (a.m + log2f(a.s)) * 0.69314718055994531f;   // ln(2^m s)
   lse_out[row] = lse;
-  if (loss != nullptr) loss[row] = t.y == 0.f ? 0.f : (t.y < 0.f ? NAN : tau * tau * (t.x + lse));
-  if (t.y < 0.f) atomicOr(status, DEV_BAD_INDEX);
+  if (loss != nullptr) loss[row] = t.kind == 0 ? 0.f : (t.kind < 0 ? NAN : tau * tau * term);
+  if (t.kind < 0) atomicOr(status, DEV_BAD_INDEX);
 }
 
 // A warp a row.  Entries of one class are joined into the first of them.
